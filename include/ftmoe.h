@@ -410,6 +410,53 @@ ft_status ft_cache_snapshot(const ft_cache* cache, int32_t* slot_for_id, int32_t
 /* Copy slot `slot`'s S record bytes to host memory `dst` (synchronises). */
 ft_status ft_cache_read_slot(const ft_cache* cache, int64_t slot, void* dst);
 
+/* ---------------------------------------------------------------------------
+ * Operators over resident weights: records (or single matrices in a record's
+ * format) that stay in device memory, without a slot cache.
+ *
+ * ft_workspace_create — device scratch of `bytes` for those operators, plus
+ * their arrival counters, on the current device.  Each operator's
+ * ..._workspace query says how many bytes a call of up to max_tokens tokens
+ * needs; one workspace may serve several operators and shapes (take the
+ * largest).  Calls that use one workspace must not overlap in time: keep them
+ * on one stream, or order them by events; a captured graph keeps using the
+ * workspace it was captured with, so two graphs that may run at the same time
+ * need two.  Synchronises.  Errors: FT_ERR_ARG, FT_ERR_NOMEM, FT_ERR_HIP.
+ * ft_workspace_destroy synchronises; NULL is accepted.
+ * ------------------------------------------------------------------------- */
+typedef struct ft_workspace ft_workspace;
+ft_status ft_workspace_create(size_t bytes, ft_workspace** out);
+ft_status ft_workspace_destroy(ft_workspace* ws);
+
+/* ---------------------------------------------------------------------------
+ * ft_moe_layer — a whole mixture-of-experts layer for a few tokens over
+ * resident records: routing, the routed experts and the weighted combine,
+ *   ids[t], w[t] as ft_moe_route (fp64 logits, top-k, softmax over the k),
+ *   y[t] = base[t] + sum_j w[t,j] * FFN_{ids[t,j]}(x[t]),
+ * accumulated in fp32 and written as bf16 ("Making Large MoE Models Practical
+ * on a Single Machine", section 1; the expert FFN of one record as in
+ * ft_moe_forward).  Inside an expert the SwiGLU output keeps 16 significant
+ * bits.
+ * shape: experts <= 256; layers is not read.
+ * x [T x d] bf16, wr [d x E] bf16, records: E records of ft_record_bytes()
+ *   in device memory, record_stride bytes apart (a multiple of 16); x, wr and
+ *   records 16-byte aligned.  base [T x d] bf16 or NULL (no addend); it may be
+ *   y.  Out: ids [T x k] int32, w [T x k] fp32, y [T x d] bf16.  Apart from
+ *   base = y no output may overlap an input or another output.
+ * T: 0..64 (0 enqueues nothing).  A NaN logit ranks as minus infinity, so ids
+ *   always name experts of the layer; its token's w and y are NaN when it is
+ *   chosen or x itself is NaN.
+ * Everything is enqueued on `stream`; the call may be captured into a graph.
+ * Results do not depend on timing: equal inputs give equal bits.
+ * Errors: FT_ERR_ARG (shape, T, null or misaligned pointers, stride, a
+ * workspace that is too small or of another device than the current one or
+ * the stream's), FT_ERR_HIP.
+ * ------------------------------------------------------------------------- */
+int64_t ft_moe_layer_workspace(const ft_shape* shape, int32_t max_tokens);   /* bytes; 0 if invalid */
+ft_status ft_moe_layer(const ft_shape* shape, const uint16_t* x, const uint16_t* wr, const void* records,
+                       int64_t record_stride, int32_t T, const uint16_t* base, int32_t* ids, float* w, uint16_t* y,
+                       ft_workspace* ws, void* stream);
+
 /* Pinned, device-mapped host memory for host banks (hipHostMalloc).  Banks
  * larger than torch's power-of-two pinned allocator can serve come from here. */
 ft_status ft_host_alloc(size_t bytes, void** ptr);

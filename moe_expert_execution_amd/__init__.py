@@ -83,6 +83,10 @@ _SIGS = {
     "ft_cache_set_timing": (i32, [vp, i32]),
     "ft_cache_timing": (i32, [vp, ctypes.POINTER(FtTiming)]),
     "ft_cache_read_slot": (i32, [vp, i64, vp]),
+    "ft_workspace_create": (i32, [ctypes.c_size_t, ctypes.POINTER(vp)]),
+    "ft_workspace_destroy": (i32, [vp]),
+    "ft_moe_layer_workspace": (i64, [ctypes.POINTER(FtShape), i32]),
+    "ft_moe_layer": (i32, [ctypes.POINTER(FtShape), vp, vp, vp, i64, i32, vp, vp, vp, vp, vp, vp]),
     "ft_host_alloc": (i32, [ctypes.c_size_t, ctypes.POINTER(vp)]),
     "ft_host_free": (i32, [vp]),
     "ft_last_error": (ctypes.c_char_p, []),
@@ -220,3 +224,23 @@ def ft_cache_read_slot(h: int, slot: int, nbytes: int) -> np.ndarray:
     out = np.empty(nbytes, np.uint8)
     _check(lib().ft_cache_read_slot(h, slot, out.ctypes.data))
     return out
+
+
+def ft_workspace_create(nbytes: int) -> int:
+    h = vp()
+    _check(lib().ft_workspace_create(nbytes, ctypes.byref(h)))
+    return h.value
+
+
+def ft_workspace_destroy(ws: int) -> None:
+    _check(lib().ft_workspace_destroy(ws))
+
+
+def ft_moe_layer_workspace(shp: FtShape, max_tokens: int) -> int:
+    return lib().ft_moe_layer_workspace(ctypes.byref(shp), max_tokens)
+
+
+def ft_moe_layer(shp: FtShape, x: int, wr: int, records: int, record_stride: int, T: int, base: int, ids: int, w: int,
+                 y: int, ws: int, stream: int = 0) -> None:
+    """`base` may be 0 (no addend)."""
+    _check(lib().ft_moe_layer(ctypes.byref(shp), x, wr, records, record_stride, T, base, ids, w, y, ws, stream))

@@ -1,0 +1,40 @@
+// Host-side declarations of the operators over resident weights: the
+// workspace handle and the kernel launchers.
+#pragma once
+#include "common.h"
+
+namespace ftmoe {
+
+// ---- the workspace handle --------------------------------------------------------
+// [0, kCounterBytes): arrival counters, zero between calls; then the calls' buffers.
+constexpr size_t kCounterBytes = 64 << 10;
+constexpr int kMaxLayerTokens = 64;       // tokens of one ft_moe_layer call
+constexpr int kMaxRouteExperts = 256;     // experts of one ft_moe_layer call
+
+}  // namespace ftmoe
+
+struct ft_workspace {
+    uint8_t* mem;
+    size_t bytes;        // of the buffers after the counters
+    int device;
+    uint64_t magic;      // set while the handle is valid
+};
+
+namespace ftmoe {
+
+struct LayerArgs {
+    const uint16_t* x;
+    const uint16_t* wr;
+    const uint8_t* rec;
+    int64_t stride;
+    RecordLayout rl;
+    int T;
+    const uint16_t* base;
+    int32_t* ids;
+    float* w;
+    uint16_t* y;
+};
+size_t layer_workspace(const ft_shape& s, int T);
+hipError_t launch_layer(const ft_shape& s, const LayerArgs& a, ft_workspace* ws, hipStream_t st);
+
+}  // namespace ftmoe

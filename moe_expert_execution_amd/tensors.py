@@ -7,7 +7,7 @@ import numpy as np
 import torch
 
 from . import (FtClassifyOut, ft_cache_create, ft_cache_create_layers, ft_cache_destroy, ft_host_alloc,
-               ft_host_free, host_array, profile, shape)
+               ft_host_free, ft_workspace_create, ft_workspace_destroy, host_array, profile, shape)
 
 
 class ClassifyBuffers:
@@ -85,6 +85,26 @@ class SlotCache:
     def close(self):
         if self.handle:
             ft_cache_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Workspace:
+    """An ft_workspace of `nbytes` on the current device (closed on close()).
+    Calls that use one workspace must not overlap in time."""
+
+    def __init__(self, nbytes: int):
+        self.nbytes = nbytes
+        self.handle = ft_workspace_create(nbytes)
+
+    def close(self):
+        if self.handle:
+            ft_workspace_destroy(self.handle)
             self.handle = 0
 
     def __del__(self):
