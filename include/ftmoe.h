@@ -457,6 +457,69 @@ ft_status ft_moe_layer(const ft_shape* shape, const uint16_t* x, const uint16_t*
                        int64_t record_stride, int32_t T, const uint16_t* base, int32_t* ids, float* w, uint16_t* y,
                        ft_workspace* ws, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside shared projections.
+ *
+ * ft_lora — a pool of adapters of one projection [n x K], in device memory:
+ *   a [count x max_rank x K] bf16, b [count x n x max_rank] bf16, both 16-byte
+ *   aligned; rank [count] int32 (the adapter's ranks, clamped to 0..max_rank;
+ *   what the pool holds past them is not used, whatever it is); scale [count]
+ *   fp32.  max_rank: a multiple of 16, 16..128.  count = 0 (or a NULL ft_lora
+ *   where one is taken) means no adapters.
+ * adapter [T] int32, device: the adapter of each token; any value outside
+ *   0..count-1 means none.  Tokens of one adapter need not be neighbours, but
+ *   an adapter is read once per 32 consecutive tokens that name it.
+ *   May be NULL when the call has no adapters.
+ *
+ * ft_lora_project:
+ *   y[t] = base[t] + x[t] W^T + scale_a (x[t] A_a^T) B_a^T,  a = adapter[t],
+ *   x [T x K] bf16, W = `m` [n x K], base [T x n] bf16 or NULL, y [T x n] bf16.
+ * ft_lora_expert: one record as a SwiGLU FFN (a shared expert), each of its
+ *   projections with an adapter pool of its own (gate, up: [f x d]; down:
+ *   [d x f]), any of them NULL:
+ *   h[t] = silu(x Wg + lora_gate(x)) * (x Wu + lora_up(x)),
+ *   y[t] = base[t] + h Wd + lora_down(h).
+ * fp32 sums, one bf16 rounding of y; the x A products and h keep 16
+ * significant bits in between.  An adapter's weights reach only the
+ * tokens that name it, and a token's result does not depend on the batch
+ * around it beyond the order of fp32 sums.
+ * T: 0..65535 (0 enqueues nothing).  x and the weights 16-byte aligned.  base
+ * may be y; apart from that y may overlap nothing.  shape of ft_lora_expert:
+ * d_model, d_ff and fmt are read.  Everything is enqueued on `stream`; calls
+ * may be captured into a graph.  Equal inputs give equal bits.
+ * The workspace queries take the largest max_rank of the pools (0: none).
+ * Errors: FT_ERR_ARG (shape, T, rank, null or misaligned pointers, a workspace
+ * that is too small or of another device than the current one or the
+ * stream's), FT_ERR_HIP.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t count;
+    int32_t max_rank;
+    const int32_t* rank;
+    const float* scale;
+    const uint16_t* a;
+    const uint16_t* b;
+} ft_lora;
+
+/* One resident matrix [n x K] (n, K multiples of 128, at most 32768) in a
+ * record's format and panel order: codes, and scales where the format has
+ * them (fp8: fp32 [n/128 x K/128] row-major; mxfp4: e8m0 in panel order). */
+typedef struct {
+    int32_t n, K;
+    int32_t fmt;
+    int32_t reserved;        /* 0 */
+    const void* codes;
+    const void* scales;      /* NULL for bf16 */
+} ft_matrix;
+
+int64_t ft_lora_project_workspace(const ft_matrix* m, int32_t max_rank, int32_t max_tokens);   /* 0 if invalid */
+ft_status ft_lora_project(const ft_matrix* m, const ft_lora* lora, const uint16_t* x, const int32_t* adapter,
+                          int32_t T, const uint16_t* base, uint16_t* y, ft_workspace* ws, void* stream);
+int64_t ft_lora_expert_workspace(const ft_shape* shape, int32_t max_rank, int32_t max_tokens); /* 0 if invalid */
+ft_status ft_lora_expert(const ft_shape* shape, const void* record, const ft_lora* gate, const ft_lora* up,
+                         const ft_lora* down, const uint16_t* x, const int32_t* adapter, int32_t T,
+                         const uint16_t* base, uint16_t* y, ft_workspace* ws, void* stream);
+
 /* Pinned, device-mapped host memory for host banks (hipHostMalloc).  Banks
  * larger than torch's power-of-two pinned allocator can serve come from here. */
 ft_status ft_host_alloc(size_t bytes, void** ptr);

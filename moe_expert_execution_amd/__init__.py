@@ -56,6 +56,14 @@ class FtTiming(ctypes.Structure):
                 ("gemm_experts", u64), ("gemm_rows", u64)]
 
 
+class FtLora(ctypes.Structure):
+    _fields_ = [("count", i32), ("max_rank", i32), ("rank", vp), ("scale", vp), ("a", vp), ("b", vp)]
+
+
+class FtMatrix(ctypes.Structure):
+    _fields_ = [("n", i32), ("K", i32), ("fmt", i32), ("reserved", i32), ("codes", vp), ("scales", vp)]
+
+
 class FtError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__(f"ftmoe status {status}: {msg}")
@@ -87,6 +95,11 @@ _SIGS = {
     "ft_workspace_destroy": (i32, [vp]),
     "ft_moe_layer_workspace": (i64, [ctypes.POINTER(FtShape), i32]),
     "ft_moe_layer": (i32, [ctypes.POINTER(FtShape), vp, vp, vp, i64, i32, vp, vp, vp, vp, vp, vp]),
+    "ft_lora_project_workspace": (i64, [ctypes.POINTER(FtMatrix), i32, i32]),
+    "ft_lora_project": (i32, [ctypes.POINTER(FtMatrix), ctypes.POINTER(FtLora), vp, vp, i32, vp, vp, vp, vp]),
+    "ft_lora_expert_workspace": (i64, [ctypes.POINTER(FtShape), i32, i32]),
+    "ft_lora_expert": (i32, [ctypes.POINTER(FtShape), vp, ctypes.POINTER(FtLora), ctypes.POINTER(FtLora),
+                             ctypes.POINTER(FtLora), vp, vp, i32, vp, vp, vp, vp]),
     "ft_host_alloc": (i32, [ctypes.c_size_t, ctypes.POINTER(vp)]),
     "ft_host_free": (i32, [vp]),
     "ft_last_error": (ctypes.c_char_p, []),
@@ -123,6 +136,11 @@ def shape(layers, experts, top_k, d_model, d_ff, fmt="bf16") -> FtShape:
 
 def profile(bp_mbps, bh_mbps, max_fetch=-1) -> FtProfile:
     return FtProfile(bp_mbps, bh_mbps, max_fetch)
+
+
+def matrix(n, K, fmt, codes: int, scales: int = 0) -> FtMatrix:
+    """A resident matrix [n x K]: device addresses of its codes and (fp8, mxfp4) scales."""
+    return FtMatrix(n, K, FMT[fmt] if isinstance(fmt, str) else fmt, 0, codes, scales)
 
 
 def ft_record_bytes(shp: FtShape) -> int:
@@ -244,3 +262,28 @@ def ft_moe_layer(shp: FtShape, x: int, wr: int, records: int, record_stride: int
                  y: int, ws: int, stream: int = 0) -> None:
     """`base` may be 0 (no addend)."""
     _check(lib().ft_moe_layer(ctypes.byref(shp), x, wr, records, record_stride, T, base, ids, w, y, ws, stream))
+
+
+def _opt(struct):
+    return ctypes.byref(struct) if struct is not None else None
+
+
+def ft_lora_project_workspace(m: FtMatrix, max_rank: int, max_tokens: int) -> int:
+    return lib().ft_lora_project_workspace(ctypes.byref(m), max_rank, max_tokens)
+
+
+def ft_lora_project(m: FtMatrix, lora, x: int, adapter: int, T: int, base: int, y: int, ws: int,
+                    stream: int = 0) -> None:
+    """`lora`: an FtLora or None; `base` and (without adapters) `adapter` may be 0."""
+    _check(lib().ft_lora_project(ctypes.byref(m), _opt(lora), x, adapter, T, base, y, ws, stream))
+
+
+def ft_lora_expert_workspace(shp: FtShape, max_rank: int, max_tokens: int) -> int:
+    return lib().ft_lora_expert_workspace(ctypes.byref(shp), max_rank, max_tokens)
+
+
+def ft_lora_expert(shp: FtShape, record: int, gate, up, down, x: int, adapter: int, T: int, base: int, y: int, ws: int,
+                   stream: int = 0) -> None:
+    """`gate`, `up`, `down`: FtLora or None; `base` and (without adapters) `adapter` may be 0."""
+    _check(lib().ft_lora_expert(ctypes.byref(shp), record, _opt(gate), _opt(up), _opt(down), x, adapter, T, base, y,
+                                ws, stream))

@@ -238,36 +238,6 @@ __device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int 
     __syncthreads();
 }
 
-__device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
-
-constexpr int kRedRow = 36;               // floats of a token's 32 panel rows in LDS, padded
-
-// Adds the waves' accumulators in wave order: red[wave][token][row].
-__device__ __forceinline__ void put_acc(float* red, const f32x16_t& acc, int wave, int tile_tokens, int lane) {
-    const int m = lane & 31, g = lane >> 5;
-    if (m < tile_tokens) {
-        float* p = red + ((int64_t)wave * tile_tokens + m) * kRedRow + 4 * g;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<f32x4_t*>(p + 8 * q) =
-                f32x4_t{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
-    }
-}
-
-// out[i] = the waves' sum at place tid + i kThreads of the tile's [nt][32]
-__device__ __forceinline__ void sum_waves(float (&out)[kTile * 32 / kThreads], const float* red, int nt, int tid) {
-#pragma unroll
-    for (int i = 0; i < kTile * 32 / kThreads; ++i) {
-        const int t = (tid + i * kThreads) >> 5, n = tid & 31;
-        float s = 0.0f;
-        if (t < nt) {
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) s += red[(w * nt + t) * kRedRow + n];
-        }
-        out[i] = s;
-    }
-}
-
 // Gate/up and SwiGLU: workgroups take items (tile of at most 32 routes of one
 // expert, 32 neurons); the waves split K = d.
 template <int FMT>

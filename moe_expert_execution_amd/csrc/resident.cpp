@@ -41,6 +41,54 @@ ft_status check_layer_shape(const ft_shape* s) {
     return FT_OK;
 }
 
+ft_status check_rank(int32_t r) {
+    FT_REQUIRE(r == 0 || (r >= 16 && r <= kMaxRank && r % 16 == 0), "max_rank must be a multiple of 16 in 16..%d",
+               kMaxRank);
+    return FT_OK;
+}
+
+// *out: the pool's device view, count 0 when there are no adapters
+ft_status check_lora(const ft_lora* l, const int32_t* adapter, const char* name, LoraView* out) {
+    *out = LoraView();
+    if (!l) return FT_OK;
+    FT_REQUIRE(l->count >= 0, "%s: count must be >= 0", name);
+    if (l->count == 0) return FT_OK;
+    FT_REQUIRE(l->max_rank > 0 && check_rank(l->max_rank) == FT_OK,
+               "%s: max_rank must be a multiple of 16 in 16..%d", name, kMaxRank);
+    FT_REQUIRE(l->rank && l->scale && l->a && l->b, "%s: null pointer", name);
+    FT_REQUIRE(aligned(l->a, 16) && aligned(l->b, 16), "%s: a and b must be 16-byte aligned", name);
+    FT_REQUIRE(aligned(l->rank, 4) && aligned(l->scale, 4), "%s: rank and scale must be 4-byte aligned", name);
+    FT_REQUIRE(adapter, "%s: adapters are given but adapter is null", name);
+    FT_REQUIRE(aligned(adapter, 4), "adapter must be 4-byte aligned");
+    out->count = l->count;
+    out->max_rank = l->max_rank;
+    out->rank = l->rank;
+    out->scale = l->scale;
+    out->a = l->a;
+    out->b = l->b;
+    return FT_OK;
+}
+
+ft_status check_matrix(const ft_matrix* m) {
+    FT_REQUIRE(m, "matrix is null");
+    FT_REQUIRE(m->n >= 128 && m->K >= 128 && m->n % 128 == 0 && m->K % 128 == 0 && m->n <= 32768 && m->K <= 32768,
+               "n and K must be multiples of 128 in 128..32768");
+    FT_REQUIRE(m->fmt == FT_FMT_BF16 || m->fmt == FT_FMT_FP8_B128 || m->fmt == FT_FMT_MXFP4_B32, "bad fmt");
+    return FT_OK;
+}
+
+ft_status check_expert_shape(const ft_shape* s) {
+    FT_REQUIRE(s, "shape is null");
+    RecordLayout rl;
+    FT_REQUIRE(record_layout(*s, &rl), "d_model and d_ff must be positive multiples of 128 and fmt valid");
+    return FT_OK;
+}
+
+ft_status check_lora_tokens(int32_t T) {
+    FT_REQUIRE(T >= 0 && T <= kMaxLoraTokens, "T must be in 0..%d", kMaxLoraTokens);
+    return FT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -128,6 +176,83 @@ ft_status ft_moe_layer(const ft_shape* shape, const uint16_t* x, const uint16_t*
     a.w = w;
     a.y = y;
     FT_HIP(launch_layer(*shape, a, ws, (hipStream_t)stream));
+    return FT_OK;
+}
+
+int64_t ft_lora_project_workspace(const ft_matrix* m, int32_t max_rank, int32_t max_tokens) {
+    clear_error();
+    if (check_matrix(m) != FT_OK || check_rank(max_rank) != FT_OK) return 0;
+    if (max_tokens < 1 || max_tokens > kMaxLoraTokens) {
+        set_error("max_tokens must be in 1..%d", kMaxLoraTokens);
+        return 0;
+    }
+
+    return (int64_t)lora_project_workspace(m->n, m->K, max_rank, max_tokens) + 256;
+}
+
+ft_status ft_lora_project(const ft_matrix* m, const ft_lora* lora, const uint16_t* x, const int32_t* adapter,
+                          int32_t T, const uint16_t* base, uint16_t* y, ft_workspace* ws, void* stream) {
+    clear_error();
+    ft_status s = check_matrix(m);
+    if (s == FT_OK) s = check_lora_tokens(T);
+    if (s != FT_OK) return s;
+    if (T == 0) return FT_OK;
+    FT_REQUIRE(m->codes && (m->fmt == FT_FMT_BF16 || m->scales) && x && y, "null pointer");
+    FT_REQUIRE(aligned(m->codes, 16) && aligned(x, 16), "x and the codes must be 16-byte aligned");
+    FT_REQUIRE(aligned(m->scales, m->fmt == FT_FMT_FP8_B128 ? 4 : 1), "the scales must be 4-byte aligned");
+    FT_REQUIRE(aligned(y, 2) && aligned(base, 2), "misaligned output or base");
+    LoraView l;
+    s = check_lora(lora, adapter, "lora", &l);
+    if (s != FT_OK) return s;
+    s = check_workspace(ws, lora_project_workspace(m->n, m->K, l.max_rank, T), stream);
+    if (s != FT_OK) return s;
+    MatrixView v;
+    v.n = m->n;
+    v.K = m->K;
+    v.fmt = m->fmt;
+    v.codes = static_cast<const uint8_t*>(m->codes);
+    v.scales = static_cast<const uint8_t*>(m->scales);
+    FT_HIP(launch_lora_project(v, l.count > 0 ? &l : nullptr, adapter, x, T, base, y, ws, (hipStream_t)stream));
+    return FT_OK;
+}
+
+int64_t ft_lora_expert_workspace(const ft_shape* shape, int32_t max_rank, int32_t max_tokens) {
+    clear_error();
+    if (check_expert_shape(shape) != FT_OK || check_rank(max_rank) != FT_OK) return 0;
+    if (max_tokens < 1 || max_tokens > kMaxLoraTokens) {
+        set_error("max_tokens must be in 1..%d", kMaxLoraTokens);
+        return 0;
+    }
+    return (int64_t)lora_expert_workspace(*shape, max_rank, max_tokens);
+}
+
+ft_status ft_lora_expert(const ft_shape* shape, const void* record, const ft_lora* gate, const ft_lora* up,
+                         const ft_lora* down, const uint16_t* x, const int32_t* adapter, int32_t T,
+                         const uint16_t* base, uint16_t* y, ft_workspace* ws, void* stream) {
+    clear_error();
+    ft_status s = check_expert_shape(shape);
+    if (s == FT_OK) s = check_lora_tokens(T);
+    if (s != FT_OK) return s;
+    if (T == 0) return FT_OK;
+    FT_REQUIRE(record && x && y, "null pointer");
+    FT_REQUIRE(aligned(record, 16) && aligned(x, 16), "x and the record must be 16-byte aligned");
+    FT_REQUIRE(aligned(y, 2) && aligned(base, 2), "misaligned output or base");
+    const ft_lora* pools[3] = {gate, up, down};
+    const char* names[3] = {"gate", "up", "down"};
+    LoraView l[3];
+    int32_t R = 0;
+    for (int i = 0; i < 3; ++i) {
+        s = check_lora(pools[i], adapter, names[i], &l[i]);
+        if (s != FT_OK) return s;
+        if (l[i].max_rank > R) R = l[i].max_rank;
+    }
+    s = check_workspace(ws, lora_expert_workspace(*shape, R, T), stream);
+    if (s != FT_OK) return s;
+    RecordLayout rl;
+    (void)record_layout(*shape, &rl);
+    auto view = [&](int i) { return l[i].count > 0 ? &l[i] : nullptr; };
+    FT_HIP(launch_lora_expert(*shape, rl, static_cast<const uint8_t*>(record), view(0), view(1), view(2), adapter, x, T,
+                              base, y, ws, (hipStream_t)stream));
     return FT_OK;
 }
 

@@ -37,4 +37,28 @@ struct LayerArgs {
 size_t layer_workspace(const ft_shape& s, int T);
 hipError_t launch_layer(const ft_shape& s, const LayerArgs& a, ft_workspace* ws, hipStream_t st);
 
+constexpr int kMaxRank = 128;             // ranks of an adapter
+constexpr int kMaxLoraTokens = 65535;
+
+// The device side of an ft_lora (count 0: no adapters).
+struct LoraView {
+    int count = 0, max_rank = 0;
+    const int32_t* rank = nullptr;
+    const float* scale = nullptr;
+    const uint16_t* a = nullptr;
+    const uint16_t* b = nullptr;
+};
+struct MatrixView {
+    int n, K, fmt;
+    const uint8_t* codes;
+    const uint8_t* scales;
+};
+size_t lora_project_workspace(int n, int K, int max_rank, int max_tokens);
+size_t lora_expert_workspace(const ft_shape& s, int max_rank, int max_tokens);
+hipError_t launch_lora_project(const MatrixView& m, const LoraView* lora, const int32_t* adapter, const uint16_t* x,
+                               int T, const uint16_t* base, uint16_t* y, ft_workspace* ws, hipStream_t st);
+hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const uint8_t* rec, const LoraView* gate,
+                              const LoraView* up, const LoraView* down, const int32_t* adapter, const uint16_t* x,
+                              int T, const uint16_t* base, uint16_t* y, ft_workspace* ws, hipStream_t st);
+
 }  // namespace ftmoe

@@ -6,7 +6,7 @@ pinned host banks from ft_host_alloc exposed as NumPy views.
 import numpy as np
 import torch
 
-from . import (FtClassifyOut, ft_cache_create, ft_cache_create_layers, ft_cache_destroy, ft_host_alloc,
+from . import (FtClassifyOut, FtLora, ft_cache_create, ft_cache_create_layers, ft_cache_destroy, ft_host_alloc,
                ft_host_free, ft_workspace_create, ft_workspace_destroy, host_array, profile, shape)
 
 
@@ -112,3 +112,19 @@ class Workspace:
             self.close()
         except Exception:
             pass
+
+
+class LoraPool:
+    """A pool of adapters of one projection [n x K] as device tensors, kept alive with its ft_lora:
+    a [count x max_rank x K] and b [count x n x max_rank] (bf16, contiguous), rank [count] int32,
+    scale [count] fp32."""
+
+    def __init__(self, a, b, rank, scale):
+        count, max_rank, _ = a.shape
+        if b.shape[0] != count or b.shape[2] != max_rank or rank.shape != (count,) or scale.shape != (count,):
+            raise ValueError("a, b, rank and scale describe different pools")
+        for t, dt in ((a, torch.bfloat16), (b, torch.bfloat16), (rank, torch.int32), (scale, torch.float32)):
+            if t.dtype != dt or not t.is_contiguous() or t.device.type != "cuda" or t.device != a.device:
+                raise ValueError("pools are contiguous device tensors: a and b bf16, rank int32, scale fp32")
+        self.a, self.b, self.rank, self.scale = a, b, rank, scale
+        self.struct = FtLora(count, max_rank, rank.data_ptr(), scale.data_ptr(), a.data_ptr(), b.data_ptr())
