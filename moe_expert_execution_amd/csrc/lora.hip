@@ -354,13 +354,18 @@ ExpertBuffers expert_buffers(const ft_shape& s, int max_rank, int T) {
 
 }  // namespace
 
+size_t lora_project_call_bytes(int n, int K, int max_rank, int T) {
+    return part_bytes(1, n, K, T) + 2 * align256((size_t)T * max_rank * 2);
+}
+size_t lora_expert_call_bytes(const ft_shape& s, int max_rank, int T) { return expert_buffers(s, max_rank, T).total; }
+
 // The largest need of any call of up to max_tokens tokens: the partial sums
 // shrink when a call's tiles alone fill the card, so every tile count up to
 // that point is looked at.
 size_t lora_project_workspace(int n, int K, int max_rank, int max_tokens) {
     size_t most = 0;
     for (int T = 1;; T = T + kTile < max_tokens ? (T / kTile + 1) * kTile : max_tokens) {
-        const size_t b = part_bytes(1, n, K, T) + 2 * align256((size_t)T * max_rank * 2);
+        const size_t b = lora_project_call_bytes(n, K, max_rank, T);
         most = b > most ? b : most;
         if (T >= max_tokens) break;
     }
@@ -370,7 +375,7 @@ size_t lora_project_workspace(int n, int K, int max_rank, int max_tokens) {
 size_t lora_expert_workspace(const ft_shape& s, int max_rank, int max_tokens) {
     size_t most = 0;
     for (int T = 1;; T = T + kTile < max_tokens ? (T / kTile + 1) * kTile : max_tokens) {
-        const size_t b = expert_buffers(s, max_rank, T).total;
+        const size_t b = lora_expert_call_bytes(s, max_rank, T);
         most = b > most ? b : most;
         if (T >= max_tokens) break;
     }

@@ -19,133 +19,172 @@ using namespace rs;
 
 // ---- routing ----------------------------------------------------------------------
 
-constexpr int kRouteThreads = 256;
-constexpr int kRouteTokens = 8;           // tokens of one routing workgroup
-constexpr int kRouteRows = 64;            // router rows of one slice
-constexpr int kRouteMaxSlices = 64;
+constexpr int kRouteTokens = 16;          // tokens of one matrix-core tile
+constexpr int kRouteExperts = 64;         // experts of one workgroup
 
-// Slices of the hidden size: each is kRouteRows rows or more, so that the
-// partial logits (one fp64 per slice, token and expert) stay small.
-inline int route_slices(int d) {
-    const int s = (d + kRouteRows - 1) / kRouteRows;
-    return s < kRouteMaxSlices ? s : kRouteMaxSlices;
+// Rows of the router one wave takes.  A slice (a workgroup's 8 waves) ends in
+// one fp64 partial logit per token and expert, which the group's last
+// workgroup reads back, so longer slices are taken as tokens grow.
+inline int route_rows(int T) { return T <= 2 ? 32 : T <= 8 ? 64 : 128; }
+inline int route_slices(int d, int T) {
+    const int per = kWaves * route_rows(T);
+    return (d + per - 1) / per;
 }
 
 struct RouteArgs {
     const uint16_t* x;
     const uint16_t* wr;
-    int T, d, E, k, slices;
+    int T, d, E, k, rows, slices;
     double* part;          // [slices][T][E]
-    uint32_t* counters;    // one per token group
+    uint32_t* counters;    // one per token tile
     int32_t* ids;
     float* w;
 };
 
-__device__ __forceinline__ double bf16_f64(uint32_t u) { return (double)__uint_as_float(u << 16); }
+// The largest of the 64 lanes' values, in every lane.
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_max(uint64_t v) {
+    const uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
+    const uint32_t l2 = (uint32_t)__builtin_amdgcn_update_dpp((int)lo, (int)lo, CTRL, 0xF, 0xF, false);
+    const uint32_t h2 = (uint32_t)__builtin_amdgcn_update_dpp((int)hi, (int)hi, CTRL, 0xF, 0xF, false);
+    const uint64_t o = ((uint64_t)h2 << 32) | l2;
+    return o > v ? o : v;
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+    v = dpp_max<0x111>(v);        // row_shr 1, 2, 4, 8: the largest of each 16 lanes in its last
+    v = dpp_max<0x112>(v);
+    v = dpp_max<0x114>(v);
+    v = dpp_max<0x118>(v);
+    v = dpp_max<0x142>(v);        // row_bcast 15, 31: across the four rows, in lane 63
+    v = dpp_max<0x143>(v);
+    return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), 63) << 32) |
+           (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
 
-// Workgroup (slice, group of 8 tokens): the slice's part of every logit of its
-// tokens, products exact and sums in fp64.  A thread takes VE experts of the
-// rows rs, rs + RPI, ... of the slice; the row groups are added in order.  The
-// group's last workgroup adds the slices in order, takes each token's k
-// largest logits by rank (an expert's rank is the number of experts before
-// it: a larger logit, or an equal one of a lower index) and their softmax.
-// A NaN logit counts as minus infinity in the order, so every rank is taken
-// exactly once and every id is a valid expert.
-template <int VE>
-__global__ void __launch_bounds__(kRouteThreads) layer_route_kernel(RouteArgs a) {
-    __shared__ double red[kRouteThreads * VE];
-    __shared__ double z[kMaxRouteExperts];
-    __shared__ double zsel[kMaxTopK];
-    __shared__ int esel[kMaxTopK];
+// One wave picks the k largest of a token's E logits z (LDS), ties to the
+// lower expert, and writes ids and the softmax of the chosen.  The order is
+// that of 64-bit keys rising with the logit (-0 equals +0); a NaN ranks as
+// minus infinity, so there are always k experts to take.
+__device__ __forceinline__ void select_experts(const double* z, int E, int k, int lane, int32_t* ids, float* w) {
+    constexpr int V = kMaxRouteExperts / 64;
+    uint64_t key[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int e = lane + 64 * j;
+        key[j] = 0;
+        if (e < E) {
+            const double v = z[e] == z[e] ? z[e] + 0.0 : -INFINITY;
+            const uint64_t b = (uint64_t)__double_as_longlong(v);
+            key[j] = (b >> 63) ? ~b : b | (1ull << 63);
+        }
+    }
+    int mine = 0;                  // lane r keeps the r-th expert
+    for (int r = 0; r < k; ++r) {
+        uint64_t m = key[0];
+#pragma unroll
+        for (int j = 1; j < V; ++j) m = key[j] > m ? key[j] : m;
+        m = wave_max(m);
+        int e = -1;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const uint64_t b = __ballot(key[j] == m);
+            if (e < 0 && b) e = 64 * j + __builtin_ctzll(b);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (lane + 64 * j == e) key[j] = 0;
+        if (lane == r) mine = e;
+    }
+    if (lane < k) {
+        const double ex = exp(z[mine] - z[__builtin_amdgcn_readfirstlane(mine)]);
+        double sum = 0.0;
+        for (int r = 0; r < k; ++r) sum += __shfl(ex, r, 64);
+        ids[lane] = mine;
+        w[lane] = (float)(ex / sum);
+    }
+}
+
+// Workgroup (slice of d, 64 experts, 16 tokens): partial logits on the fp64
+// matrix cores (bf16 products are exact in fp64, sums are fp64).  Per 32 rows
+// lane group g = l / 16 takes rows 8 g .. 8 g + 7, so MFMA step s contracts
+// rows 8 g + s; column c = l % 16 of tile n is expert 4 c + n, so one 8-byte
+// load gives a lane its four tiles' weights of a row, and one 16-byte load its
+// token's 8 activations.  The waves' sums are added in order, the tile's
+// last workgroup adds the slices in order and selects, one wave per token.
+__global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
+    extern __shared__ __attribute__((aligned(16))) double zred[];
     __shared__ uint32_t flag;
-    const int tid = threadIdx.x;
-    const int slice = blockIdx.x, t0 = blockIdx.y * kRouteTokens;
+    typedef double f64x4 __attribute__((ext_vector_type(4)));
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+    const int g = lane >> 4, c = lane & 15;
+    const int slice = blockIdx.x, e0 = blockIdx.y * kRouteExperts, t0 = blockIdx.z * kRouteTokens;
     const int nt = min(kRouteTokens, a.T - t0);
-    const int ncg = (a.E + VE - 1) / VE;          // expert groups (VE divides E)
-    const int rpi = kRouteThreads / ncg;
-    const int cg = tid % ncg, rsub = tid / ncg;
-    const int span = (a.d + a.slices - 1) / a.slices;
-    const int r0 = slice * span, r1 = min(a.d, r0 + span);
-
-    double acc[kRouteTokens][VE];
+    const int k0 = (slice * kWaves + wid) * a.rows, k1 = min(a.d, k0 + a.rows);
+    const int e4 = e0 + 4 * c;
+    const bool vec = (a.E & 3) == 0;      // rows of the router aligned for 8-byte loads
+    f64x4 acc[4];
 #pragma unroll
-    for (int t = 0; t < kRouteTokens; ++t)
+    for (int n = 0; n < 4; ++n) acc[n] = f64x4{0.0, 0.0, 0.0, 0.0};
+    const uint16_t* xrow = a.x + (int64_t)(t0 + min(c, nt - 1)) * a.d + 8 * g;
+    for (int kk = k0; kk < k1; kk += 32) {
+        const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(xrow + kk);
+        u32x2_t wv[8];
 #pragma unroll
-        for (int j = 0; j < VE; ++j) acc[t][j] = 0.0;
-    if (rsub < rpi) {
-#pragma unroll 2
-        for (int r = r0 + rsub; r < r1; r += rpi) {
-            double wv[VE];
-            if constexpr (VE == 8) {
-                const u32x4_t v = *reinterpret_cast<const u32x4_t*>(a.wr + (int64_t)r * a.E + cg * 8);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    wv[2 * j] = (double)bf16lo(v[j]);
-                    wv[2 * j + 1] = (double)bf16hi(v[j]);
-                }
+        for (int s = 0; s < 8; ++s) {
+            const uint16_t* p = a.wr + (int64_t)(kk + 8 * g + s) * a.E + e4;
+            wv[s] = u32x2_t{0u, 0u};
+            if (vec) {
+                if (e4 < a.E) wv[s] = *reinterpret_cast<const u32x2_t*>(p);
             } else {
-                wv[0] = bf16_f64(a.wr[(int64_t)r * a.E + cg]);
+                uint32_t h[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) h[n] = e4 + n < a.E ? p[n] : 0u;
+                wv[s] = u32x2_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
             }
+        }
 #pragma unroll
-            for (int t = 0; t < kRouteTokens; ++t)
-                if (t < nt) {
-                    const double xv = bf16_f64(a.x[(int64_t)(t0 + t) * a.d + r]);
+        for (int s = 0; s < 8; ++s) {
+            const uint32_t xw = xv[s >> 1];
+            const double av = (double)((s & 1) ? bf16hi(xw) : bf16lo(xw));
 #pragma unroll
-                    for (int j = 0; j < VE; ++j) acc[t][j] = fma(xv, wv[j], acc[t][j]);
-                }
+            for (int n = 0; n < 4; ++n) {
+                const uint32_t u = wv[s][n >> 1];
+                const double bv = (double)((n & 1) ? bf16hi(u) : bf16lo(u));
+                acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64(av, bv, acc[n], 0, 0, 0);
+            }
         }
     }
-    for (int t = 0; t < nt; ++t) {
-        __syncthreads();
-        double mine[VE];
+    // accumulator element v of lane l: token 4 v + l / 16, expert 4 (l % 16) + n
 #pragma unroll
-        for (int tt = 0; tt < kRouteTokens; ++tt)
-            if (tt == t)
+    for (int v = 0; v < 4; ++v) {
+        const int t = 4 * v + g;
+        if (t < nt)
 #pragma unroll
-                for (int j = 0; j < VE; ++j) mine[j] = acc[tt][j];
-        if (rsub < rpi)
-#pragma unroll
-            for (int j = 0; j < VE; ++j) red[rsub * a.E + cg * VE + j] = mine[j];
-        __syncthreads();
-        for (int e = tid; e < a.E; e += kRouteThreads) {
-            double s = 0.0;
-            for (int q = 0; q < rpi; ++q) s += red[q * a.E + e];
-            put_agent(a.part + ((int64_t)slice * a.T + t0 + t) * a.E + e, s);
-        }
+            for (int n = 0; n < 4; ++n) zred[(wid * nt + t) * kRouteExperts + 4 * c + n] = acc[n][v];
     }
-    if (!last_arrival(a.counters + blockIdx.y, a.slices, &flag)) return;
+    __syncthreads();
+    for (int i = tid; i < nt * kRouteExperts; i += kThreads) {
+        const int t = i / kRouteExperts, e = e0 + i % kRouteExperts;
+        double s = 0.0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) s += zred[w * nt * kRouteExperts + i];
+        if (e < a.E) put_agent(a.part + ((int64_t)slice * a.T + t0 + t) * a.E + e, s);
+    }
+    if (!last_arrival(a.counters + blockIdx.z, a.slices * gridDim.y, &flag)) return;
 
-    for (int t = 0; t < nt; ++t) {
-        if (tid < a.E) {
-            double s = 0.0;
-            const double* p = a.part + (int64_t)(t0 + t) * a.E + tid;
-#pragma unroll 16
-            for (int q = 0; q < a.slices; ++q) s += get_agent(p + (int64_t)q * a.T * a.E);
-            z[tid] = s == s ? s : -INFINITY;
-            red[tid] = s;
-        }
-        __syncthreads();
-        if (tid < a.E) {
-            const double mz = z[tid];
-            int rank = 0;
-            for (int e = 0; e < a.E; ++e) {
-                const double o = z[e];
-                rank += (o > mz || (o == mz && e < tid)) ? 1 : 0;
-            }
-            if (rank < a.k) {
-                esel[rank] = tid;
-                zsel[rank] = red[tid];
-            }
-        }
-        __syncthreads();
-        if (tid < a.k) {
-            double s = 0.0;
-            for (int r = 0; r < a.k; ++r) s += exp(zsel[r] - zsel[0]);
-            a.ids[(int64_t)(t0 + t) * a.k + tid] = esel[tid];
-            a.w[(int64_t)(t0 + t) * a.k + tid] = (float)(exp(zsel[tid] - zsel[0]) / s);
-        }
-        __syncthreads();
+    const int n = nt * a.E;
+    const double* p = a.part + (int64_t)t0 * a.E;
+    const int64_t step = (int64_t)a.T * a.E;
+    for (int i = tid; i < n; i += kThreads) {
+        double s = 0.0;
+#pragma unroll 8
+        for (int q = 0; q < a.slices; ++q) s += get_agent(p + q * step + i);
+        zred[i] = s;
     }
+    __syncthreads();
+    for (int t = wid; t < nt; t += kWaves)
+        select_experts(zred + t * a.E, a.E, a.k, lane, a.ids + (int64_t)(t0 + t) * a.k, a.w + (int64_t)(t0 + t) * a.k);
 }
 
 // ---- the routed experts --------------------------------------------------------------
@@ -452,7 +491,7 @@ LayerBuffers layer_buffers(const ft_shape& s, int T) {
     LayerBuffers b;
     const size_t R = (size_t)T * s.top_k;
     b.logits = 0;
-    b.hhi = align256((size_t)route_slices(s.d_model) * T * s.experts * sizeof(double));
+    b.hhi = align256((size_t)route_slices(s.d_model, T) * T * s.experts * sizeof(double));
     b.hlo = b.hhi + align256(R * s.d_ff * 2);
     b.part = b.hlo + align256(R * s.d_ff * 2);
     b.total = b.part + align256((size_t)down_splits(s, T) * T * s.d_model * sizeof(float));
@@ -461,9 +500,12 @@ LayerBuffers layer_buffers(const ft_shape& s, int T) {
 
 template <int FMT>
 hipError_t launch_fmt(const ft_shape& s, const RouteArgs& r, const ExpertArgs& a, hipStream_t st) {
-    const dim3 rg(r.slices, (r.T + kRouteTokens - 1) / kRouteTokens);
-    if (r.E % 8 == 0) hipLaunchKernelGGL(layer_route_kernel<8>, rg, dim3(kRouteThreads), 0, st, r);
-    else hipLaunchKernelGGL(layer_route_kernel<1>, rg, dim3(kRouteThreads), 0, st, r);
+    const dim3 rg(r.slices, (r.E + kRouteExperts - 1) / kRouteExperts, (r.T + kRouteTokens - 1) / kRouteTokens);
+    const int rt = r.T < kRouteTokens ? r.T : kRouteTokens;
+    // the waves' partial logits, then whole rows
+    static_assert(kWaves * kRouteExperts >= kMaxRouteExperts, "a token's logits fit its partial sums' place");
+    hipLaunchKernelGGL(layer_route_kernel, rg, dim3(kThreads), (size_t)rt * kWaves * kRouteExperts * sizeof(double), st,
+                       r);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
 
@@ -486,7 +528,17 @@ hipError_t launch_fmt(const ft_shape& s, const RouteArgs& r, const ExpertArgs& a
 
 }  // namespace
 
-size_t layer_workspace(const ft_shape& s, int T) { return layer_buffers(s, T).total; }
+size_t layer_call_bytes(const ft_shape& s, int T) { return layer_buffers(s, T).total; }
+
+// the largest need of any call of up to T tokens (fewer tokens may take more slices)
+size_t layer_workspace(const ft_shape& s, int T) {
+    size_t most = 0;
+    for (int t = 1; t <= T; ++t) {
+        const size_t b = layer_call_bytes(s, t);
+        most = b > most ? b : most;
+    }
+    return most;
+}
 
 hipError_t launch_layer(const ft_shape& s, const LayerArgs& la, ft_workspace* ws, hipStream_t st) {
     const LayerBuffers b = layer_buffers(s, la.T);
@@ -500,7 +552,8 @@ hipError_t launch_layer(const ft_shape& s, const LayerArgs& la, ft_workspace* ws
     r.d = s.d_model;
     r.E = s.experts;
     r.k = s.top_k;
-    r.slices = route_slices(s.d_model);
+    r.rows = route_rows(la.T);
+    r.slices = route_slices(s.d_model, la.T);
     r.part = reinterpret_cast<double*>(m + b.logits);
     r.counters = counters;
     r.ids = la.ids;

@@ -164,7 +164,7 @@ ft_status ft_moe_layer(const ft_shape* shape, const uint16_t* x, const uint16_t*
                "record_stride must be a multiple of 16 and at least the record's %lld bytes", (long long)a.rl.S);
     FT_REQUIRE(aligned(x, 16) && aligned(wr, 16) && aligned(records, 16), "x, wr and records must be 16-byte aligned");
     FT_REQUIRE(aligned(y, 2) && aligned(base, 2) && aligned(ids, 4) && aligned(w, 4), "misaligned output or base");
-    s = check_workspace(ws, layer_workspace(*shape, T), stream);
+    s = check_workspace(ws, layer_call_bytes(*shape, T), stream);
     if (s != FT_OK) return s;
     a.x = x;
     a.wr = wr;
@@ -204,7 +204,7 @@ ft_status ft_lora_project(const ft_matrix* m, const ft_lora* lora, const uint16_
     LoraView l;
     s = check_lora(lora, adapter, "lora", &l);
     if (s != FT_OK) return s;
-    s = check_workspace(ws, lora_project_workspace(m->n, m->K, l.max_rank, T), stream);
+    s = check_workspace(ws, lora_project_call_bytes(m->n, m->K, l.max_rank, T), stream);
     if (s != FT_OK) return s;
     MatrixView v;
     v.n = m->n;
@@ -246,7 +246,7 @@ ft_status ft_lora_expert(const ft_shape* shape, const void* record, const ft_lor
         if (s != FT_OK) return s;
         if (l[i].max_rank > R) R = l[i].max_rank;
     }
-    s = check_workspace(ws, lora_expert_workspace(*shape, R, T), stream);
+    s = check_workspace(ws, lora_expert_call_bytes(*shape, R, T), stream);
     if (s != FT_OK) return s;
     RecordLayout rl;
     (void)record_layout(*shape, &rl);

@@ -34,6 +34,9 @@ struct LayerArgs {
     float* w;
     uint16_t* y;
 };
+// ..._call_bytes: what a call of exactly T tokens takes; ..._workspace: the
+// largest of any call of up to T.
+size_t layer_call_bytes(const ft_shape& s, int T);
 size_t layer_workspace(const ft_shape& s, int T);
 hipError_t launch_layer(const ft_shape& s, const LayerArgs& a, ft_workspace* ws, hipStream_t st);
 
@@ -53,6 +56,8 @@ struct MatrixView {
     const uint8_t* codes;
     const uint8_t* scales;
 };
+size_t lora_project_call_bytes(int n, int K, int max_rank, int T);
+size_t lora_expert_call_bytes(const ft_shape& s, int max_rank, int T);
 size_t lora_project_workspace(int n, int K, int max_rank, int max_tokens);
 size_t lora_expert_workspace(const ft_shape& s, int max_rank, int max_tokens);
 hipError_t launch_lora_project(const MatrixView& m, const LoraView* lora, const int32_t* adapter, const uint16_t* x,
