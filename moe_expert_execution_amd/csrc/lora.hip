@@ -44,73 +44,81 @@ struct ShrinkArgs {
     uint16_t* vlo[2];
     const int32_t* adapter;
     const uint16_t* xhi;
-    const uint16_t* xlo;   // second plane of x (null: x is plain bf16)
-    int T, K, panels;      // rank panels of 32 per projection
+    const uint16_t* xlo;   // second plane of x (PL = 2)
+    int T, K, panels;      // rank panels of 16 per projection
 };
 
 // Workgroup (tile of 32 tokens, stride over the tile's adapters, projection
-// and rank panel): 32 ranks of v for every token of the adapter; the waves
-// split K.  Both operands are row-major: a lane takes 32 consecutive K of
-// each 64, so a 128-byte line is used by one instruction group.
-template <bool HL>
+// and 16 ranks): v for every token of the adapter; the waves split K.  Both
+// operands are row-major: of 128 K a lane takes 32 consecutive ones, so the
+// four lanes of a row use its 256 bytes.
+template <int PL>
 __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(ShrinkArgs s) {
     extern __shared__ __attribute__((aligned(16))) float red[];
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
     const int t0 = blockIdx.x * kTile, nt = min(kTile, s.T - t0);
-    const int proj = blockIdx.z / s.panels, rp = blockIdx.z - proj * s.panels;
+    const int proj = blockIdx.z / s.panels, r0 = (blockIdx.z - proj * s.panels) * 16;
     const LoraView lo = s.lora[proj];
     const int R = lo.max_rank;
-    if (rp * 32 >= R) return;
+    if (r0 >= R) return;
     const int id = tile_adapter(s.adapter, t0, s.T, lo.count, lane);
     const int units = s.K / kUnit;
     const int u0 = wid * units / kWaves, u1 = (wid + 1) * units / kWaves;
-    const int64_t xo = (int64_t)(t0 + min(lane & 31, nt - 1)) * s.K;
+    int64_t xo[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) xo[i] = (int64_t)(t0 + min(i * kCols + (lane & 15), nt - 1)) * s.K;
+    const int nx = nt > kCols ? 2 : 1;
     each_adapter(id, [&](int i, int a) {
         if (i % (int)gridDim.y != (int)blockIdx.y) return;
         const int rank = min(max(lo.rank[a], 0), R);
-        if (rp * 32 >= rank) {
-            // the expand reads v in steps of 16 up to the rank: nothing here
-            return;
-        }
-        const uint16_t* arow = lo.a + ((int64_t)a * R + min(rp * 32 + (lane & 31), rank - 1)) * s.K;
-        f32x16_t acc = zero16();
-        XUnit au[2], xh[2], xl[2];
+        if (r0 >= rank) return;           // the expand reads v in steps of 16 up to the rank
+        const uint16_t* arow = lo.a + ((int64_t)a * R + min(r0 + (lane & 15), rank - 1)) * s.K;
+        f32x4_t acc[2] = {f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}};
+        XUnit au[2], x[2][2][PL];
         auto load = [&](int b, int u) {
             load_x<FT_FMT_MXFP4_B32>(au[b], arow, u, lane);
-            load_x<FT_FMT_MXFP4_B32>(xh[b], s.xhi + xo, u, lane);
-            if constexpr (HL) load_x<FT_FMT_MXFP4_B32>(xl[b], s.xlo + xo, u, lane);
-        };
-        auto mma = [&](int b) {
 #pragma unroll
-            for (int v = 0; v < 8; ++v) {
-                const bf16x8_t av = __builtin_bit_cast(bf16x8_t, au[b].v[v]);
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av, __builtin_bit_cast(bf16x8_t, xh[b].v[v]), acc, 0, 0, 0);
-                if constexpr (HL)
-                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av, __builtin_bit_cast(bf16x8_t, xl[b].v[v]), acc, 0, 0, 0);
-            }
+            for (int q = 0; q < 2; ++q)
+                if (q < nx) {
+                    load_x<FT_FMT_MXFP4_B32>(x[b][q][0], s.xhi + xo[q], u, lane);
+                    if constexpr (PL == 2) load_x<FT_FMT_MXFP4_B32>(x[b][q][PL - 1], s.xlo + xo[q], u, lane);
+                }
+        };
+        auto step = [&](int b) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (q < nx)
+#pragma unroll
+                        for (int p = 0; p < PL; ++p)
+                            acc[q] = mma(__builtin_bit_cast(bf16x8_t, au[b].v[v]), x[b][q][p].v[v], acc[q]);
         };
         if (u0 < u1) load(0, u0);
         for (int u = u0; u < u1; u += 2) {
             if (u + 1 < u1) load(1, u + 1);
-            mma(0);
+            step(0);
             if (u + 1 < u1) {
                 if (u + 2 < u1) load(0, u + 2);
-                mma(1);
+                step(1);
             }
         }
-        float v[kTile * 32 / kThreads];
-        put_acc(red, acc, wid, nt, lane);
+        // 16 ranks of up to 32 tokens: one place per thread
         __syncthreads();
-        sum_waves(v, red, nt, tid);
-        __syncthreads();
-        const float scale = lo.scale[a];
 #pragma unroll
-        for (int q = 0; q < kTile * 32 / kThreads; ++q) {
-            const int t = (tid + q * kThreads) >> 5, n = rp * 32 + (tid & 31);
-            if (t >= nt || n >= R || s.adapter[t0 + t] != a) continue;
+        for (int q = 0; q < 2; ++q) {
+            const int m = q * kCols + (lane & 15);
+            if (m < nt) *reinterpret_cast<f32x4_t*>(red + (wid * nt + m) * 20 + 4 * (lane >> 4)) = acc[q];
+        }
+        __syncthreads();
+        const int t = tid >> 4, n = r0 + (tid & 15);
+        if (t < nt && s.adapter[t0 + t] == a) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) v += red[(w * nt + t) * 20 + (tid & 15)];
             // v in 16 significant bits; zero past the adapter's rank
             uint16_t h, l;
-            split_bf16(n < rank ? scale * v[q] : 0.0f, h, l);
+            split_bf16(n < rank ? lo.scale[a] * v : 0.0f, h, l);
             const int64_t o = (int64_t)(t0 + t) * R + n;
             s.vhi[proj][o] = h;
             s.vlo[proj][o] = l;
@@ -118,35 +126,50 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(ShrinkArgs s) 
     });
 }
 
-// acc += v B_a^T for row panel p of B [n x R] and the tile's tokens of adapter
-// a; the other tokens' products are selected away (an adapter's infinities
-// and NaN stay with its own requests), and ranks past the adapter's own are
-// masked out of B, whatever the pool holds there.
-__device__ __forceinline__ void expand(f32x16_t& acc, const LoraView& lo, const uint16_t* vhi, const uint16_t* vlo,
-                                       int n, int p, int a, int id, int t, int lane) {
-    const int R = lo.max_rank, g = lane >> 5;
+// acc += v B_a^T for row panel p of B [n x R] and the 16 tokens `id` (the
+// lane's column's adapter) and `t` (its token); the other tokens' products
+// are selected away (an adapter's infinities and NaN stay with its own
+// requests), and ranks past the adapter's own are masked out of B, whatever
+// the pool holds there.
+__device__ __forceinline__ void expand(Acc& acc, const LoraView& lo, const uint16_t* vhi, const uint16_t* vlo, int n,
+                                       int p, int a, int id, int t, int lane) {
+    if (__ballot(id == a) == 0) return;
+    const int R = lo.max_rank, g = lane >> 4;
     const int rank = min(max(lo.rank[a], 0), R);
-    const uint16_t* brow = lo.b + ((int64_t)a * n + p * 32 + (lane & 31)) * R + g * 8;
+    const uint16_t* brow = lo.b + ((int64_t)a * n + p * 32 + (lane & 15)) * R + g * 8;
     const int64_t vo = (int64_t)t * R + g * 8;
-    f32x16_t sum = zero16();
-    for (int k0 = 0; k0 < rank; k0 += 16) {
-        u32x4_t b = *reinterpret_cast<const u32x4_t*>(brow + k0);
-        u32x4_t h = u32x4_t{0u, 0u, 0u, 0u}, l = h;
-        if (id == a) {
-            h = *reinterpret_cast<const u32x4_t*>(vhi + vo + k0);
-            l = *reinterpret_cast<const u32x4_t*>(vlo + vo + k0);
-        }
+    const u32x4_t none = u32x4_t{0u, 0u, 0u, 0u};
+    Acc sum = zero_acc();
+    for (int k0 = 0; k0 < rank; k0 += 32) {
+        u32x4_t b[2] = {none, none}, h = none, l = none;
         const int left = rank - k0 - g * 8;          // ranks of this lane's eight that exist
+        if (left > 0) {
+            b[0] = *reinterpret_cast<const u32x4_t*>(brow + k0);
+            b[1] = *reinterpret_cast<const u32x4_t*>(brow + 16 * R + k0);
+            if (id == a) {
+                h = *reinterpret_cast<const u32x4_t*>(vhi + vo + k0);
+                l = *reinterpret_cast<const u32x4_t*>(vlo + vo + k0);
+            }
+        }
         if (left < 8) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] &= left >= 2 * j + 2 ? 0xFFFFFFFFu : left == 2 * j + 1 ? 0xFFFFu : 0u;
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t keep = left >= 2 * j + 2 ? 0xFFFFFFFFu : left == 2 * j + 1 ? 0xFFFFu : 0u;
+                b[0][j] &= keep;
+                b[1][j] &= keep;
+            }
         }
-        const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, b);
-        sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf, __builtin_bit_cast(bf16x8_t, h), sum, 0, 0, 0);
-        sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf, __builtin_bit_cast(bf16x8_t, l), sum, 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, b[q]);
+            sum.h[q] = mma(bf, h, sum.h[q]);
+            sum.h[q] = mma(bf, l, sum.h[q]);
+        }
     }
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[v] = id == a ? acc[v] + sum[v] : acc[v];
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc.h[q][v] = id == a ? acc.h[q][v] + sum.h[q][v] : acc.h[q][v];
 }
 
 // ---- the projections -----------------------------------------------------------------
@@ -159,7 +182,7 @@ struct ProjectArgs {
     const uint16_t* vlo[2];
     const int32_t* adapter;
     const uint16_t* xhi;
-    const uint16_t* xlo;       // second plane of x (HL)
+    const uint16_t* xlo;       // second plane of x (PL = 2)
     int T, n, K, splits;
     float* part;               // [splits][NM][T][n]
     uint32_t* counters;        // one per (panel, tile) with several splits
@@ -171,73 +194,76 @@ struct ProjectArgs {
 
 // Workgroup (row panel, split of K, tile of 32 tokens): the waves and splits
 // divide K evenly and the tile's adapters in turn; sums in wave order, then
-// in split order by the last workgroup of the (panel, tile).
-template <int FMT, int NM, bool HL>
+// in split order by the last workgroup of the (panel, tile).  NM matrices
+// share x; PL planes of x add up.
+template <int FMT, int NM, int PL, int NX>
 __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a) {
     extern __shared__ __attribute__((aligned(16))) float red[];
     __shared__ uint32_t flag;
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
     const int p = blockIdx.x, split = blockIdx.y, t0 = blockIdx.z * kTile;
-    const int nt = min(kTile, a.T - t0);
+    const int nt = min(kTile, a.T - t0), nx = nt > kCols ? 2 : 1;
     const int units = a.K / kUnit, parts = a.splits * kWaves, me = split * kWaves + wid;
     const int u0 = me * units / parts, u1 = (me + 1) * units / parts;
-    const int t = t0 + min(lane & 31, nt - 1);
-    const int64_t xo = (int64_t)t * a.K;
+    int t[NX];
+#pragma unroll
+    for (int i = 0; i < NX; ++i) t[i] = t0 + min(i * kCols + (lane & 15), nt - 1);
 
     PanelRef pr[NM];
-    f32x16_t acc[NM][1];
+    Acc acc[NM][NX];
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
         pr[m] = panel_ref<FMT>(a.codes[m], a.scales[m], a.K, p);
-        acc[m][0] = zero16();
+#pragma unroll
+        for (int i = 0; i < NX; ++i) acc[m][i] = zero_acc();
     }
     WUnit<FMT> w[2][NM];
-    constexpr int XB = HL ? 1 : 2;       // two x buffers where the registers hold them
-    XUnit xh[XB], xl[1];
+    XUnit x[2][NX][PL];
     auto load = [&](int b, int u) {
 #pragma unroll
         for (int m = 0; m < NM; ++m) load_unit<FMT>(w[b][m], pr[m], u, lane);
-        if constexpr (!HL) load_x<FMT>(xh[b], a.xhi + xo, u, lane);
-    };
-    auto mma = [&](int b, int u) {
-        if constexpr (HL) {
-            load_x<FMT>(xh[0], a.xhi + xo, u, lane);
-            load_x<FMT>(xl[0], a.xlo + xo, u, lane);
-        }
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            const XUnit* const x0[1] = {&xh[b % XB]};
-            mma_unit<FMT, 1>(acc[m], w[b][m], x0);
-            if constexpr (HL) {
-                const XUnit* const x1[1] = {&xl[0]};
-                mma_unit<FMT, 1>(acc[m], w[b][m], x1);
+        for (int i = 0; i < NX; ++i)
+            if (i < nx) {
+                load_x<FMT>(x[b][i][0], a.xhi + (int64_t)t[i] * a.K, u, lane);
+                if constexpr (PL == 2) load_x<FMT>(x[b][i][PL - 1], a.xlo + (int64_t)t[i] * a.K, u, lane);
             }
-        }
+    };
+    auto step = [&](int b) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m) mma_unit<FMT, NX, PL>(acc[m], w[b][m], x[b], nx);
     };
     if (u0 < u1) load(0, u0);
     for (int u = u0; u < u1; u += 2) {
         if (u + 1 < u1) load(1, u + 1);
-        mma(0, u);
+        step(0);
         if (u + 1 < u1) {
             if (u + 2 < u1) load(0, u + 2);
-            mma(1, u + 1);
+            step(1);
         }
     }
 #pragma unroll
     for (int m = 0; m < NM; ++m)
         if (a.lora[m].count > 0) {
             const int id = tile_adapter(a.adapter, t0, a.T, a.lora[m].count, lane);
+            int col[NX];                 // the columns' adapters
+#pragma unroll
+            for (int i = 0; i < NX; ++i) col[i] = __shfl(id, i * kCols + (lane & 15), 64);
             each_adapter(id, [&](int i, int ad) {
-                if (i % parts == me) expand(acc[m][0], a.lora[m], a.vhi[m], a.vlo[m], a.n, p, ad, id, t, lane);
+                if (i % parts != me) return;
+#pragma unroll
+                for (int q = 0; q < NX; ++q)
+                    expand(acc[m][q], a.lora[m], a.vhi[m], a.vlo[m], a.n, p, ad, col[q], t[q], lane);
             });
         }
 
-    constexpr int PT = kTile * 32 / kThreads;
+    constexpr int PT = kPlaces;
     float s[NM][PT];
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
         if (m > 0) __syncthreads();
-        put_acc(red, acc[m][0], wid, nt, lane);
+#pragma unroll
+        for (int i = 0; i < NX; ++i) put_acc(red, acc[m][i], i, wid, nt, lane);
         __syncthreads();
         sum_waves(s[m], red, nt, tid);
     }
@@ -309,25 +335,26 @@ hipError_t launch_shrink(const ShrinkArgs& s, int projections, hipStream_t st) {
     if (gy > s.T) gy = s.T;
     if (tiles >= 32 && gy > 4) gy = 4;
     const dim3 grid(tiles, gy, projections * s.panels);
-    if (s.xlo) hipLaunchKernelGGL(lora_shrink_kernel<true>, grid, dim3(kThreads), lds_bytes(s.T), st, s);
-    else hipLaunchKernelGGL(lora_shrink_kernel<false>, grid, dim3(kThreads), lds_bytes(s.T), st, s);
+    if (s.xlo) hipLaunchKernelGGL(lora_shrink_kernel<2>, grid, dim3(kThreads), lds_bytes(s.T), st, s);
+    else hipLaunchKernelGGL(lora_shrink_kernel<1>, grid, dim3(kThreads), lds_bytes(s.T), st, s);
     return hipGetLastError();
 }
 
-template <int NM, bool HL>
-hipError_t launch_project_fmt(int fmt, const ProjectArgs& a, hipStream_t st) {
+template <int FMT, int NM, int PL>
+void launch_project_nx(const ProjectArgs& a, hipStream_t st) {
     const dim3 grid(a.n / 32, a.splits, (a.T + kTile - 1) / kTile);
-    const size_t lds = lds_bytes(a.T);
+    if (a.T <= kCols)
+        hipLaunchKernelGGL((lora_project_kernel<FMT, NM, PL, 1>), grid, dim3(kThreads), lds_bytes(a.T), st, a);
+    else
+        hipLaunchKernelGGL((lora_project_kernel<FMT, NM, PL, 2>), grid, dim3(kThreads), lds_bytes(a.T), st, a);
+}
+
+template <int NM, int PL>
+hipError_t launch_project(int fmt, const ProjectArgs& a, hipStream_t st) {
     switch (fmt) {
-        case FT_FMT_BF16:
-            hipLaunchKernelGGL((lora_project_kernel<FT_FMT_BF16, NM, HL>), grid, dim3(kThreads), lds, st, a);
-            break;
-        case FT_FMT_FP8_B128:
-            hipLaunchKernelGGL((lora_project_kernel<FT_FMT_FP8_B128, NM, HL>), grid, dim3(kThreads), lds, st, a);
-            break;
-        case FT_FMT_MXFP4_B32:
-            hipLaunchKernelGGL((lora_project_kernel<FT_FMT_MXFP4_B32, NM, HL>), grid, dim3(kThreads), lds, st, a);
-            break;
+        case FT_FMT_BF16: launch_project_nx<FT_FMT_BF16, NM, PL>(a, st); break;
+        case FT_FMT_FP8_B128: launch_project_nx<FT_FMT_FP8_B128, NM, PL>(a, st); break;
+        case FT_FMT_MXFP4_B32: launch_project_nx<FT_FMT_MXFP4_B32, NM, PL>(a, st); break;
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
@@ -411,7 +438,7 @@ hipError_t launch_lora_project(const MatrixView& m, const LoraView* lora, const 
         s.xhi = x;
         s.T = T;
         s.K = m.K;
-        s.panels = (lora->max_rank + 31) / 32;
+        s.panels = lora->max_rank / 16;
         hipError_t e = launch_shrink(s, 1, st);
         if (e != hipSuccess) return e;
         a.vhi[0] = s.vhi[0];
@@ -419,7 +446,7 @@ hipError_t launch_lora_project(const MatrixView& m, const LoraView* lora, const 
         o = 2 * plane;
     }
     a.part = reinterpret_cast<float*>(mem + o);
-    return launch_project_fmt<1, false>(m.fmt, a, st);
+    return launch_project<1, 1>(m.fmt, a, st);
 }
 
 hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const uint8_t* rec, const LoraView* gate,
@@ -449,7 +476,7 @@ hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const 
             s.lora[n] = *gu[i];
             s.vhi[n] = v_hi(i);
             s.vlo[n] = v_lo(i);
-            const int p = (gu[i]->max_rank + 31) / 32;
+            const int p = gu[i]->max_rank / 16;
             s.panels = p > s.panels ? p : s.panels;
             ++n;
         }
@@ -476,7 +503,7 @@ hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const 
     a.counters = reinterpret_cast<uint32_t*>(ws->mem);
     a.hhi = hhi;
     a.hlo = hlo;
-    if ((e = launch_project_fmt<2, false>(sh.fmt, a, st)) != hipSuccess) return e;
+    if ((e = launch_project<2, 1>(sh.fmt, a, st)) != hipSuccess) return e;
 
     if (down && down->count > 0) {
         ShrinkArgs d = {};
@@ -489,7 +516,7 @@ hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const 
         d.xlo = hlo;
         d.T = T;
         d.K = sh.d_ff;
-        d.panels = (down->max_rank + 31) / 32;
+        d.panels = down->max_rank / 16;
         if ((e = launch_shrink(d, 1, st)) != hipSuccess) return e;
     }
     ProjectArgs c = {};
@@ -510,7 +537,7 @@ hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const 
     c.counters = a.counters;
     c.base = base;
     c.y = y;
-    return launch_project_fmt<1, true>(sh.fmt, c, st);
+    return launch_project<1, 2>(sh.fmt, c, st);
 }
 
 }  // namespace ftmoe

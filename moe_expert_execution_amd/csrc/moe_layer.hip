@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
 // ---- the routed experts --------------------------------------------------------------
 
 constexpr int kMaxRoutes = kMaxLayerTokens * kMaxTopK;       // 1024
+constexpr int kMaxTiles = kMaxRouteExperts + kMaxRoutes / (kTile + 1);
 
 struct ExpertArgs {
     const uint16_t* x;
@@ -212,9 +213,9 @@ struct ExpertArgs {
 struct Groups {
     unsigned long long mask[kMaxRouteExperts];   // tokens routed to the expert
     int start[kMaxRouteExperts];                 // first of its routes in `route`
-    int active[kMaxRouteExperts];                // active experts, ascending
-    int tile0[kMaxRouteExperts + 1];             // first tile of an active expert
-    int n_active, n_tiles;
+    int tile0[kMaxRouteExperts];                 // first tile of an expert
+    int n_tiles;                                 // tiles of at most kTile routes of one expert, by expert
+    uint16_t expert[kMaxTiles];                  // a tile's expert
     uint16_t route[kMaxRoutes];                  // routes t k + j by expert
 };
 
@@ -237,7 +238,7 @@ __device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int 
     }
     __syncthreads();
     if (tid < 64) {
-        int base = 0, act = 0, tiles = 0;
+        int base = 0, tiles = 0;
         for (int e0 = 0; e0 < E; e0 += 64) {
             const int e = e0 + lane;
             const int c = e < E ? __popcll(g.mask[e]) : 0;
@@ -251,22 +252,15 @@ __device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int 
                     st += b0;
                 }
             }
-            const uint64_t m = __ballot(c > 0);
             if (c > 0) {
-                const int r = act + __popcll(m & ((1ull << lane) - 1));
                 g.start[e] = base + sc - c;
-                g.active[r] = e;
-                g.tile0[r] = tiles + st - tl;
+                g.tile0[e] = tiles + st - tl;
+                for (int q = 0; q < tl; ++q) g.expert[tiles + st - tl + q] = (uint16_t)e;
             }
             base += __shfl(sc, 63, 64);
             tiles += __shfl(st, 63, 64);
-            act += __popcll(m);
         }
-        if (lane == 0) {
-            g.n_active = act;
-            g.n_tiles = tiles;
-            g.tile0[act] = tiles;
-        }
+        if (lane == 0) g.n_tiles = tiles;
     }
     __syncthreads();
 #pragma unroll
@@ -277,9 +271,23 @@ __device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int 
     __syncthreads();
 }
 
-// Gate/up and SwiGLU: workgroups take items (tile of at most 32 routes of one
-// expert, 32 neurons); the waves split K = d.
-template <int FMT>
+// A tile's routes: expert, first place in Groups::route, count.
+struct Tile {
+    int e, first, nt;
+};
+__device__ __forceinline__ Tile tile_of(const Groups& g, int tile) {
+    Tile t;
+    t.e = __builtin_amdgcn_readfirstlane(g.expert[tile]);
+    const int off = (tile - g.tile0[t.e]) * kTile;
+    t.first = __builtin_amdgcn_readfirstlane(g.start[t.e] + off);
+    t.nt = __builtin_amdgcn_readfirstlane(min(kTile, (int)__popcll(g.mask[t.e]) - off));
+    return t;
+}
+
+// Gate/up and SwiGLU: workgroups take items (tile, 32 neurons); the waves split
+// K = d.  The next unit's loads are in flight while one is multiplied, across
+// items too, so the stream does not stop for an item's sums.
+template <int FMT, int NX>
 __global__ void __launch_bounds__(kThreads, 2) layer_gateup_kernel(ExpertArgs a) {
     extern __shared__ __attribute__((aligned(16))) float red[];
     __shared__ Groups g;
@@ -287,196 +295,244 @@ __global__ void __launch_bounds__(kThreads, 2) layer_gateup_kernel(ExpertArgs a)
     group_routes(g, a.ids, a.T * a.k, a.E, a.k);
     const int panels = a.f >> 5, items = g.n_tiles * panels;
     const int units = a.d / kUnit;
-    const int u0 = wid * units / kWaves, u1 = (wid + 1) * units / kWaves;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int tile = item / panels, p = item - tile * panels;
-        // the tile's expert: the last active one whose first tile is not past it
-        int lo = 0, hi = g.n_active;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (g.tile0[mid] <= tile) lo = mid;
-            else hi = mid;
-        }
-        const int e = g.active[lo];
-        const int first = g.start[e] + (tile - g.tile0[lo]) * kTile;
-        const int nt = min(kTile, g.start[e] + (int)__popcll(g.mask[e]) - first);
-        const uint8_t* rec = a.rec + (int64_t)e * a.stride;
-        const PanelRef pg = panel_ref<FMT>(rec + a.off_gate, rec + a.off_sg, a.d, p);
-        const PanelRef pu = panel_ref<FMT>(rec + a.off_up, rec + a.off_su, a.d, p);
-        // lanes past the tile's routes repeat its last one: their columns are not stored
-        const uint16_t* xrow = a.x + (int64_t)(g.route[first + min(lane & 31, nt - 1)] / a.k) * a.d;
+    const int u0 = wid * units / kWaves, nu = (wid + 1) * units / kWaves - u0;
+    const int steps = max(nu, 1);         // a wave without units (d < 1024) loads one and leaves it
 
-        f32x16_t ag[1] = {zero16()}, au[1] = {zero16()};
-        WUnit<FMT> wg[2], wu[2];
-        XUnit xu[2];
-        auto load = [&](int b, int u) {
-            load_unit<FMT>(wg[b], pg, u, lane);
-            load_unit<FMT>(wu[b], pu, u, lane);
-            load_x<FMT>(xu[b], xrow, u, lane);
-        };
-        auto mma = [&](int b) {
-            const XUnit* const xs[1] = {&xu[b]};
-            mma_unit<FMT, 1>(ag, wg[b], xs);
-            mma_unit<FMT, 1>(au, wu[b], xs);
-        };
-        if (u0 < u1) load(0, u0);
-        for (int u = u0; u < u1; u += 2) {
-            if (u + 1 < u1) load(1, u + 1);
-            mma(0);
-            if (u + 1 < u1) {
-                if (u + 2 < u1) load(0, u + 2);
-                mma(1);
-            }
-        }
-        // gate, then up, through the same LDS: a thread sums the waves of its (token, neuron) places
-        constexpr int PT = kTile * 32 / kThreads;
-        float gs[PT], us[PT];
-        put_acc(red, ag[0], wid, nt, lane);
-        __syncthreads();
-        sum_waves(gs, red, nt, tid);
-        __syncthreads();
-        put_acc(red, au[0], wid, nt, lane);
-        __syncthreads();
-        sum_waves(us, red, nt, tid);
+    struct Cursor {
+        int item, step;
+        Tile t;
+        PanelRef pg, pu;
+        const uint16_t* x[NX];
+    };
+    auto enter = [&](Cursor& c, int item) {
+        c.item = item;
+        c.step = 0;
+        const int tile = item / panels, p = item - tile * panels;
+        c.t = tile_of(g, tile);
+        const uint8_t* rec = a.rec + (int64_t)c.t.e * a.stride;
+        c.pg = panel_ref<FMT>(rec + a.off_gate, rec + a.off_sg, a.d, p);
+        c.pu = panel_ref<FMT>(rec + a.off_up, rec + a.off_su, a.d, p);
+        // lanes past the tile's routes repeat its last one: their columns are not stored
 #pragma unroll
-        for (int i = 0; i < PT; ++i) {
-            const int t = (tid + i * kThreads) >> 5, n = tid & 31;
-            if (t >= nt) break;
+        for (int i = 0; i < NX; ++i)
+            c.x[i] = a.x + (int64_t)(g.route[c.t.first + min(i * kCols + (lane & 15), c.t.nt - 1)] / a.k) * a.d;
+    };
+    WUnit<FMT> wg[2], wu[2];
+    XUnit xu[2][NX][1];
+    Cursor ld;                            // the next unit to load
+    auto load = [&](int b) {
+        const int u = min(u0 + ld.step, units - 1);
+        load_unit<FMT>(wg[b], ld.pg, u, lane);
+        load_unit<FMT>(wu[b], ld.pu, u, lane);
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+            if (i == 0 || ld.t.nt > i * kCols) load_x<FMT>(xu[b][i][0], ld.x[i], u, lane);
+        if (++ld.step == steps && ld.item + (int)gridDim.x < items) enter(ld, ld.item + gridDim.x);
+    };
+    Acc ag[NX], au[NX];
+    int item = blockIdx.x, step = 0;
+    if (item >= items) return;
+    enter(ld, item);
+    load(0);
+    Tile t = tile_of(g, item / panels);
+#pragma unroll
+    for (int i = 0; i < NX; ++i) ag[i] = au[i] = zero_acc();
+    // one step: unit `step` of `item`; after the item's last one its sums; true at the end
+    auto advance = [&](int b) -> bool {
+        if (step < nu) {
+            const int nx = t.nt > kCols ? 2 : 1;
+            mma_unit<FMT, NX, 1>(ag, wg[b], xu[b], nx);
+            mma_unit<FMT, NX, 1>(au, wu[b], xu[b], nx);
+        }
+        if (++step < steps) return false;
+        const int half = kWaves * t.nt * kRedRow;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            put_acc(red, ag[i], i, wid, t.nt, lane);
+            put_acc(red + half, au[i], i, wid, t.nt, lane);
+            ag[i] = au[i] = zero_acc();
+        }
+        __syncthreads();
+        float gs[kPlaces], us[kPlaces];
+        sum_waves(gs, red, t.nt, tid);
+        sum_waves(us, red + half, t.nt, tid);
+        const int p = item % panels;
+#pragma unroll
+        for (int i = 0; i < kPlaces; ++i) {
+            const int m = (tid + i * kThreads) >> 5;
+            if (m >= t.nt) break;
             // h in 16 significant bits: its rounding stays far below that of y
             uint16_t h, l;
             split_bf16(silu(gs[i]) * us[i], h, l);
-            const int64_t o = (int64_t)g.route[first + t] * a.f + p * 32 + n;
+            const int64_t o = (int64_t)g.route[t.first + m] * a.f + p * 32 + (tid & 31);
             a.hhi[o] = h;
             a.hlo[o] = l;
         }
-        __syncthreads();
+        item += gridDim.x;
+        if (item >= items) return true;
+        step = 0;
+        t = tile_of(g, item / panels);
+        return false;
+    };
+    // whether a step follows the current one
+    auto more = [&]() { return step + 1 < steps || item + (int)gridDim.x < items; };
+    for (;;) {
+        if (more()) load(1);
+        if (advance(0)) return;
+        if (more()) load(0);
+        if (advance(1)) return;
     }
 }
 
-// Down and combine: workgroup (row panel of WdT, split).  The active experts'
-// K = f units form one axis, divided evenly over the splits and their waves;
-// a wave sums an expert's units for every token at once (lane = token; a lane
-// whose token is not routed to the expert computes on another route's h and
-// drops the result), then adds w times the sum to the tokens routed there.  The
-// waves' sums are added in order, and with several splits the panel's last
-// workgroup adds the splits in order, so y does not depend on timing.
-template <int FMT, int NT>
-__global__ void __launch_bounds__(kThreads, 2) layer_down_kernel(ExpertArgs a) {
-    extern __shared__ __attribute__((aligned(16))) float red[];
-    __shared__ Groups g;
-    __shared__ uint32_t flag;
-    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-    group_routes(g, a.ids, a.T * a.k, a.E, a.k);
-    const int na = g.n_active;
+// Down and combine: workgroup (NP row panels of WdT, split).  The tiles' K = f
+// units form one axis, divided evenly over the splits and their waves.  A
+// wave sums a tile's units with the tile's routes as columns, then adds w
+// times the sum to its own [token][row] sums in LDS: a token's sums see the
+// tiles in order, whatever else the tile holds, and a column past the tile's
+// routes goes nowhere.  The waves' sums are added in order, and with several
+// splits the panels' last workgroup adds the splits in order, so y does not
+// depend on timing.
+template <int NP>
+constexpr int sum_row() { return 32 * NP + 4; }      // floats of a token's sums in LDS, padded
 
-    const int p = blockIdx.x, split = blockIdx.y;
-    const int uf = a.f / kUnit, units = na * uf;
+template <int FMT, int NX, int NP>
+__global__ void __launch_bounds__(kThreads, 2) layer_down_kernel(ExpertArgs a) {
+    extern __shared__ __attribute__((aligned(16))) float sums[];     // [kWaves][T][sum_row]
+    __shared__ Groups g;
+    __shared__ float wr[kMaxRoutes];
+    __shared__ uint32_t flag;
+    constexpr int SR = sum_row<NP>();
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+    for (int r = tid; r < a.T * a.k; r += kThreads) wr[r] = a.w[r];
+    float* mine = sums + wid * a.T * SR;
+    for (int i = lane * 4; i < a.T * SR; i += 256) *reinterpret_cast<f32x4_t*>(mine + i) = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    group_routes(g, a.ids, a.T * a.k, a.E, a.k);
+
+    const int p0 = blockIdx.x * NP, split = blockIdx.y;
+    const int uf = a.f / kUnit, units = g.n_tiles * uf;
     const int part = split * kWaves + wid, parts = a.splits * kWaves;
     const int u0 = (int)((int64_t)part * units / parts), u1 = (int)((int64_t)(part + 1) * units / parts);
 
-    f32x16_t acc[NT];
+    struct Cursor {
+        int tile, kk;
+        Tile t;
+        PanelRef pd[NP];
+        int64_t h[NX];
+    };
+    auto enter = [&](Cursor& c, int tile) {
+        c.tile = tile;
+        c.kk = 0;
+        c.t = tile_of(g, tile);
+        const uint8_t* rec = a.rec + (int64_t)c.t.e * a.stride;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = zero16();
-    for (int u = u0; u < u1;) {
-        const int ai = u / uf, ue = min(u1, (ai + 1) * uf);
-        const int e = g.active[ai];
-        const uint8_t* rec = a.rec + (int64_t)e * a.stride;
-        const PanelRef pd = panel_ref<FMT>(rec + a.off_down, rec + a.off_sd, a.f, p);
-        const uint16_t *hrow[NT], *lrow[NT];
-        float wt[NT];
-        bool on[NT];
+        for (int n = 0; n < NP; ++n) c.pd[n] = panel_ref<FMT>(rec + a.off_down, rec + a.off_sd, a.f, p0 + n);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int t = i * kTile + (lane & 31);
-            const unsigned long long m = g.mask[e];
-            on[i] = (m >> t) & 1;
-            const int r = g.route[g.start[e] + (on[i] ? __popcll(m & ((1ull << t) - 1)) : 0)];
-            wt[i] = on[i] ? a.w[r] : 0.0f;
-            hrow[i] = a.hhi + (int64_t)r * a.f;
-            lrow[i] = a.hlo + (int64_t)r * a.f;
+        for (int i = 0; i < NX; ++i)
+            c.h[i] = (int64_t)g.route[c.t.first + min(i * kCols + (lane & 15), c.t.nt - 1)] * a.f;
+    };
+    WUnit<FMT> wd[2][NP];
+    XUnit hu[2][NX][2];
+    Cursor ld;
+    auto load = [&](int b) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) load_unit<FMT>(wd[b][n], ld.pd[n], ld.kk, lane);
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+            if (i == 0 || ld.t.nt > i * kCols) {
+                load_x<FMT>(hu[b][i][0], a.hhi + ld.h[i], ld.kk, lane);
+                load_x<FMT>(hu[b][i][1], a.hlo + ld.h[i], ld.kk, lane);
+            }
+        if (++ld.kk == uf && ld.tile + 1 < g.n_tiles) enter(ld, ld.tile + 1);
+    };
+    if (u0 < u1) {
+        Acc acc[NP][NX];
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int i = 0; i < NX; ++i) acc[n][i] = zero_acc();
+        int u = u0, tile = u0 / uf, kk = u0 - tile * uf;
+        enter(ld, tile);
+        ld.kk = kk;
+        load(0);
+        Tile t = tile_of(g, tile);
+        auto advance = [&](int b) -> bool {
+            const int nx = t.nt > kCols ? 2 : 1;
+#pragma unroll
+            for (int n = 0; n < NP; ++n) mma_unit<FMT, NX, 2>(acc[n], wd[b][n], hu[b], nx);
+            const bool last = ++u == u1;
+            if (++kk < uf && !last) return false;
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const int m = i * kCols + (lane & 15);
+                if (m < t.nt) {
+                    const int r = g.route[t.first + m];
+                    const float w = wr[r];
+                    float* s = mine + (r / a.k) * SR + 4 * (lane >> 4);
+#pragma unroll
+                    for (int n = 0; n < NP; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            f32x4_t* q = reinterpret_cast<f32x4_t*>(s + 32 * n + 16 * h);
+                            f32x4_t v = *q;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = fmaf(w, acc[n][i].h[h][e], v[e]);
+                            *q = v;
+                        }
+                }
+#pragma unroll
+                for (int n = 0; n < NP; ++n) acc[n][i] = zero_acc();
+            }
+            if (last) return true;
+            kk = 0;
+            t = tile_of(g, ++tile);
+            return false;
+        };
+        for (;;) {
+            if (u + 1 < u1) load(1);
+            if (advance(0)) break;
+            if (u + 1 < u1) load(0);
+            if (advance(1)) break;
         }
-        f32x16_t sum[NT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) sum[i] = zero16();
-        // two weight buffers; h in two as well where the registers hold them
-        constexpr int HB = NT == 1 && FMT != FT_FMT_FP8_B128 ? 2 : 1;
-        WUnit<FMT> wd[2];
-        XUnit hu[HB][NT], lu[HB][NT];
-        auto load_h = [&](int b, int uu) {
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                load_x<FMT>(hu[b][i], hrow[i], uu - ai * uf, lane);
-                load_x<FMT>(lu[b][i], lrow[i], uu - ai * uf, lane);
-            }
-        };
-        auto load = [&](int b, int uu) {
-            load_unit<FMT>(wd[b], pd, uu - ai * uf, lane);
-            if constexpr (HB == 2) load_h(b, uu);
-        };
-        auto mma = [&](int b, int uu) {
-            if constexpr (HB == 1) load_h(0, uu);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                f32x16_t s2[1] = {sum[i]};
-                const XUnit* const x0[1] = {&hu[b % HB][i]};
-                const XUnit* const x1[1] = {&lu[b % HB][i]};
-                mma_unit<FMT, 1>(s2, wd[b], x0);
-                mma_unit<FMT, 1>(s2, wd[b], x1);
-                sum[i] = s2[0];
-            }
-        };
-        load(0, u);
-        for (; u < ue; u += 2) {
-            if (u + 1 < ue) load(1, u + 1);
-            mma(0, u);
-            if (u + 1 < ue) {
-                if (u + 2 < ue) load(0, u + 2);
-                mma(1, u + 1);
-            }
-        }
-        u = ue;
-        // the product of an unrouted token may be anything, infinities among it: selected away
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][v] = on[i] ? fmaf(wt[i], sum[i][v], acc[i][v]) : acc[i][v];
     }
+    __syncthreads();
     auto emit = [&](int t, int n, float v) {
-        const int64_t o = (int64_t)t * a.d + p * 32 + n;
+        const int64_t o = (int64_t)t * a.d + p0 * 32 + n;
         if (a.base) v += __uint_as_float((uint32_t)a.base[o] << 16);
         a.y[o] = f32_to_bf16_rne(v);
     };
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int nt = min(kTile, a.T - i * kTile);
-        float s[kTile * 32 / kThreads];
-        if (i > 0) __syncthreads();
-        put_acc(red, acc[i], wid, nt, lane);
-        __syncthreads();
-        sum_waves(s, red, nt, tid);
-#pragma unroll
-        for (int q = 0; q < kTile * 32 / kThreads; ++q) {
-            const int t = (tid + q * kThreads) >> 5, n = tid & 31;
-            if (t >= nt) break;
-            if (a.splits == 1) emit(i * kTile + t, n, s[q]);
-            else put_agent(a.part + ((int64_t)split * a.T + i * kTile + t) * a.d + p * 32 + n, s[q]);
-        }
-    }
-    if (a.splits == 1 || !last_arrival(a.counters + p, a.splits, &flag)) return;
-    for (int i = tid; i < a.T * 32; i += kThreads) {
-        const int t = i >> 5, n = i & 31;
+    constexpr int C = 32 * NP;
+    for (int i = tid; i < a.T * C; i += kThreads) {
+        const int t = i / C, n = i % C;
         float s = 0.0f;
-        for (int q = 0; q < a.splits; ++q) s += get_agent(a.part + ((int64_t)q * a.T + t) * a.d + p * 32 + n);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) s += sums[(w * a.T + t) * SR + n];
+        if (a.splits == 1) emit(t, n, s);
+        else put_agent(a.part + ((int64_t)split * a.T + t) * a.d + p0 * 32 + n, s);
+    }
+    if (a.splits == 1 || !last_arrival(a.counters + blockIdx.x, a.splits, &flag)) return;
+    for (int i = tid; i < a.T * C; i += kThreads) {
+        const int t = i / C, n = i % C;
+        float s = 0.0f;
+#pragma unroll 4
+        for (int q = 0; q < a.splits; ++q) s += get_agent(a.part + ((int64_t)q * a.T + t) * a.d + p0 * 32 + n);
         emit(t, n, s);
     }
 }
 
-// Workgroups over a row panel of WdT: enough for the card, and no more than
+// Row panels per down workgroup.  The h loads beside an MXFP4 panel outweigh its
+// codes fourfold, so two panels share them once there are experts enough to
+// fill the card all the same.
+int down_panels(const ft_shape& s, int T) {
+    return s.fmt == FT_FMT_MXFP4_B32 && (int64_t)T * s.top_k >= 32 ? 2 : 1;
+}
+
+// Splits of the tiles' axis: enough workgroups for the card, and no more than
 // leaves each wave a unit when every route has an expert of its own.
 int down_splits(const ft_shape& s, int T) {
-    const int panels = s.d_model / 32;
+    const int wgs = s.d_model / 32 / down_panels(s, T);
     const int64_t units = (int64_t)(T * s.top_k < s.experts ? T * s.top_k : s.experts) * (s.d_ff / kUnit);
-    int64_t n = (256 + panels - 1) / panels;
+    int64_t n = (256 + wgs - 1) / wgs;
     const int64_t most = (units + kWaves - 1) / kWaves;
     if (n > most) n = most;
     return n < 1 ? 1 : (int)n;
@@ -512,17 +568,27 @@ hipError_t launch_fmt(const ft_shape& s, const RouteArgs& r, const ExpertArgs& a
     const int R = a.T * a.k;
     const int tiles = (R < a.E ? R : a.E) + R / (kTile + 1);
     const int64_t items = (int64_t)tiles * (a.f / 32);
+    const dim3 gg((unsigned)(items < 256 ? items : 256));
     const int nt = a.T < kTile ? a.T : kTile;
-    const size_t lds = (size_t)kWaves * nt * kRedRow * sizeof(float);
-    hipLaunchKernelGGL(layer_gateup_kernel<FMT>, dim3((unsigned)(items < 512 ? items : 512)), dim3(kThreads), lds, st, a);
+    const size_t glds = (size_t)2 * kWaves * nt * kRedRow * sizeof(float);
+    const bool one = a.T <= kCols;        // every tile fits one operand
+    if (one) hipLaunchKernelGGL((layer_gateup_kernel<FMT, 1>), gg, dim3(kThreads), glds, st, a);
+    else hipLaunchKernelGGL((layer_gateup_kernel<FMT, 2>), gg, dim3(kThreads), glds, st, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
 
-    const dim3 dg(a.d / 32, a.splits);
-    if (a.T <= kTile)
-        hipLaunchKernelGGL((layer_down_kernel<FMT, 1>), dg, dim3(kThreads), lds, st, a);
-    else
-        hipLaunchKernelGGL((layer_down_kernel<FMT, 2>), dg, dim3(kThreads), lds, st, a);
+    const int np = down_panels(s, a.T);
+    const dim3 dg(a.d / 32 / np, a.splits);
+    const size_t dlds = (size_t)kWaves * a.T * (32 * np + 4) * sizeof(float);
+    if constexpr (FMT == FT_FMT_MXFP4_B32) {
+        if (np == 2) {
+            if (one) hipLaunchKernelGGL((layer_down_kernel<FMT, 1, 2>), dg, dim3(kThreads), dlds, st, a);
+            else hipLaunchKernelGGL((layer_down_kernel<FMT, 2, 2>), dg, dim3(kThreads), dlds, st, a);
+            return hipGetLastError();
+        }
+    }
+    if (one) hipLaunchKernelGGL((layer_down_kernel<FMT, 1, 1>), dg, dim3(kThreads), dlds, st, a);
+    else hipLaunchKernelGGL((layer_down_kernel<FMT, 2, 1>), dg, dim3(kThreads), dlds, st, a);
     return hipGetLastError();
 }
 

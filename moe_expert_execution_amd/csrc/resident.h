@@ -2,17 +2,18 @@
 // cores: the device code shared by the operators over resident weights
 // (moe_layer.hip, lora.hip).
 //
-// A 32-row panel is read in units of 128 along K, each unit LBU lane blocks
-// of 1 KiB: lane l of a wave holds row l % 32 at chunk column l / 32, which is
-// the A operand of v_mfma_f32_32x32x16_bf16 as it stands (codes are converted
-// to bf16 in registers, which is exact for e4m3 and for e2m1 times a power of
-// two).  The tokens are the B operand: lane l holds token l % 32 at the same
-// K positions, read from memory (L2) as EPC contiguous bf16.  So a panel
-// streams from HBM once whatever the token count up to 32, and lane l ends
-// with token l % 32 and, per group q, rows 8 q + 4 (l / 32) .. + 3 of the panel.
-// A matrix-core step takes 32 cycles per KiB of bf16 weights (16 KiB of
-// e2m1: 128), several times faster than a CU's share of HBM, so the columns
-// past the token count cost nothing.
+// A 32-row panel is read in units of 128 along K.  Lane l of a wave takes row
+// l % 16 of one half of the panel at chunk column l / 16 of four, which is the
+// A operand of v_mfma_f32_16x16x32_bf16 as it stands (codes are converted to
+// bf16 in registers, exact for e4m3 and for e2m1 times a power of two); a load
+// is four runs of 256 bytes.  Up to 16 tokens are the B operand: lane l holds
+// token l % 16 at the same K positions, read from memory (L2).  So a panel
+// streams from HBM once whatever the token count, and lane l ends with token
+// l % 16 and rows 4 (l / 16) .. + 3 of each half.  16 columns and not 32: a
+// token load returns 1 KiB to the lanes whatever its rows hold, at 64 bytes
+// per cycle and CU, so narrower tiles halve what stands beside the weights on
+// that path (the layer's down product over MXFP4, 64 tokens on 256 experts,
+// ran at a fifth of the card's bandwidth with 32 columns).
 #pragma once
 #include "resident_api.h"
 #include "wfmt.h"
@@ -23,23 +24,25 @@ namespace rs {
 constexpr int kWaves = 8;                 // waves of a streaming workgroup, splitting K
 constexpr int kThreads = kWaves * 64;
 constexpr int kUnit = 128;                // elements along K per unit (one fp8 scale block)
-constexpr int kTile = 32;                 // tokens of one operand tile
+constexpr int kCols = 16;                 // tokens of one operand
+constexpr int kTile = 2 * kCols;          // tokens of one tile: at most two operands
 
 template <int FMT>
 struct Panel {
     static constexpr int EPC = WF<FMT>::EPC;
-    static constexpr int LBU = kUnit / (2 * EPC);      // lane blocks per unit: 8, 4, 2
+    static constexpr int LPH = kUnit / (4 * EPC);      // loads per half panel and unit: 4, 2, 1
+    static constexpr int UB = 32 * kUnit * 16 / EPC;   // bytes of a unit
     static constexpr int64_t row_bytes(int K) { return (int64_t)K * 16 / EPC; }
 };
 
 // One unit of one panel in registers: codes and scales as stored.
 template <int FMT>
 struct WUnit {
-    u32x4_t c[Panel<FMT>::LBU];
-    uint32_t s[FMT == FT_FMT_MXFP4_B32 ? Panel<FMT>::LBU : 1];
+    u32x4_t c[2][Panel<FMT>::LPH];
+    uint32_t s[FMT == FT_FMT_MXFP4_B32 ? 2 : 1];
 };
 
-// A panel's place: codes of row panel p, its scales, and the matrix's K.
+// A panel's place: its codes and its scales.
 struct PanelRef {
     const uint8_t* codes;      // the panel's first byte
     const uint8_t* scales;     // fp8: the fp32 row of block scales; mxfp4: the panel's e8m0 bytes
@@ -55,37 +58,47 @@ __device__ __forceinline__ PanelRef panel_ref(const uint8_t* codes, const uint8_
     return r;
 }
 
+// The lane's unit inside a lane block pair: chunk column l / 16, row l % 16 of the first half.
+__device__ __forceinline__ int lane_unit(int lane) {
+    const int g = lane >> 4;
+    return (g >> 1) * 64 + (g & 1) * 32 + (lane & 15);
+}
+
 // Weights are read once per call: non-temporal, so that they leave the caches
 // to the tokens and the partial sums.
 template <int FMT>
 __device__ __forceinline__ void load_unit(WUnit<FMT>& u, const PanelRef& p, int unit, int lane) {
-    constexpr int LBU = Panel<FMT>::LBU;
-    const uint8_t* c = p.codes + (int64_t)unit * (LBU * 1024) + lane * 16;
+    constexpr int LPH = Panel<FMT>::LPH;
+    const int lu = lane_unit(lane);
+    const uint8_t* c = p.codes + (int64_t)unit * Panel<FMT>::UB + lu * 16;
 #pragma unroll
-    for (int b = 0; b < LBU; ++b) u.c[b] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(c + b * 1024));
+    for (int b = 0; b < LPH; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            u.c[h][b] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(c + b * 2048 + h * 256));
     if constexpr (FMT == FT_FMT_FP8_B128) {
         u.s[0] = reinterpret_cast<const uint32_t*>(p.scales)[unit];
     } else if constexpr (FMT == FT_FMT_MXFP4_B32) {
 #pragma unroll
-        for (int b = 0; b < LBU; ++b) u.s[b] = p.scales[(unit * LBU + b) * 64 + lane];
+        for (int h = 0; h < 2; ++h) u.s[h] = p.scales[unit * 128 + lu + h * 16];
     }
 }
 
 // The lane's token values of one unit: `row` is the token's bf16 row.
 struct XUnit {
-    u32x4_t v[8];
+    u32x4_t v[4];
 };
 template <int FMT>
 __device__ __forceinline__ void load_x(XUnit& x, const uint16_t* row, int unit, int lane) {
-    constexpr int EPC = Panel<FMT>::EPC, LBU = Panel<FMT>::LBU, V = EPC / 8;
-    const uint16_t* p = row + unit * kUnit + (lane >> 5) * EPC;
+    constexpr int EPC = Panel<FMT>::EPC, V = EPC / 8;
+    const uint16_t* p = row + unit * kUnit + (lane >> 4) * EPC;
 #pragma unroll
-    for (int b = 0; b < LBU; ++b)
+    for (int b = 0; b < 4 / V; ++b)
 #pragma unroll
-        for (int j = 0; j < V; ++j) x.v[b * V + j] = *reinterpret_cast<const u32x4_t*>(p + b * 2 * EPC + j * 8);
+        for (int j = 0; j < V; ++j) x.v[b * V + j] = *reinterpret_cast<const u32x4_t*>(p + b * 4 * EPC + j * 8);
 }
 
-// The A operand of MFMA step j of a lane block.
+// The A operand of MFMA step j of a 16-byte chunk.
 template <int FMT>
 __device__ __forceinline__ bf16x8_t a_frag(const u32x4_t c, int j, float scale) {
     if constexpr (FMT == FT_FMT_BF16) {
@@ -107,52 +120,63 @@ __device__ __forceinline__ bf16x8_t a_frag(const u32x4_t c, int j, float scale) 
     }
 }
 
-__device__ __forceinline__ f32x16_t zero16() {
-    f32x16_t z;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-    return z;
+// A panel's sums for 16 tokens: rows 16 h + 4 (l / 16) + v of token l % 16.
+struct Acc {
+    f32x4_t h[2];
+};
+__device__ __forceinline__ Acc zero_acc() {
+    Acc a;
+    a.h[0] = a.h[1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    return a;
 }
 
-// acc += panel unit x tokens, for NX operand sets that share the weights
-// (token tiles, or the high and low halves of one).  An fp8 unit is one scale
-// block: its products are summed unscaled and the fp32 scale multiplies the
-// sum, so no weight is rounded.
-template <int FMT, int NX>
-__device__ __forceinline__ void mma_unit(f32x16_t (&acc)[NX], const WUnit<FMT>& w, const XUnit* const (&x)[NX]) {
-    constexpr int LBU = Panel<FMT>::LBU, V = Panel<FMT>::EPC / 8;
+__device__ __forceinline__ f32x4_t mma(const bf16x8_t a, const u32x4_t b, const f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// acc[i] += panel unit x operand set i, for NX sets that share the weights.
+// Only the first nx sets are computed.  The PL planes of a set add to the same
+// sums (the high and low halves of a value).  An fp8 unit is one scale block: its
+// products are summed unscaled and the fp32 scale multiplies the sum, so no
+// weight is rounded.
+template <int FMT, int NX, int PL>
+__device__ __forceinline__ void mma_unit(Acc (&acc)[NX], const WUnit<FMT>& w, const XUnit (&x)[NX][PL], int nx) {
+    constexpr int LPH = Panel<FMT>::LPH, V = Panel<FMT>::EPC / 8;
+    Acc blk[NX];
     if constexpr (FMT == FT_FMT_FP8_B128) {
-        f32x16_t blk[NX];
 #pragma unroll
-        for (int i = 0; i < NX; ++i) blk[i] = zero16();
+        for (int i = 0; i < NX; ++i) blk[i] = zero_acc();
+    }
+    float s[2] = {1.0f, 1.0f};
+    if constexpr (FMT == FT_FMT_MXFP4_B32) {
+        s[0] = e8m0_to_f32(w.s[0]);
+        s[1] = e8m0_to_f32(w.s[FMT == FT_FMT_MXFP4_B32 ? 1 : 0]);
+    }
 #pragma unroll
-        for (int b = 0; b < LBU; ++b)
+    for (int b = 0; b < LPH; ++b)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const bf16x8_t a = a_frag<FMT>(w.c[b], j, 1.0f);
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bf16x8_t a = a_frag<FMT>(w.c[h][b], j, s[h]);
 #pragma unroll
                 for (int i = 0; i < NX; ++i)
-                    blk[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, __builtin_bit_cast(bf16x8_t, x[i]->v[b * V + j]),
-                                                                     blk[i], 0, 0, 0);
+                    if (i == 0 || i < nx) {
+#pragma unroll
+                        for (int p = 0; p < PL; ++p) {
+                            f32x4_t& d = FMT == FT_FMT_FP8_B128 ? blk[i].h[h] : acc[i].h[h];
+                            d = mma(a, x[i][p].v[b * V + j], d);
+                        }
+                    }
             }
-        const float s = __uint_as_float(w.s[0]);
+    if constexpr (FMT == FT_FMT_FP8_B128) {
+        const float sc = __uint_as_float(w.s[0]);
 #pragma unroll
         for (int i = 0; i < NX; ++i)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][v] = fmaf(s, blk[i][v], acc[i][v]);
-    } else {
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int b = 0; b < LBU; ++b) {
-            const float s = FMT == FT_FMT_MXFP4_B32 ? e8m0_to_f32(w.s[FMT == FT_FMT_MXFP4_B32 ? b : 0]) : 1.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const bf16x8_t a = a_frag<FMT>(w.c[b], j, s);
-#pragma unroll
-                for (int i = 0; i < NX; ++i)
-                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, __builtin_bit_cast(bf16x8_t, x[i]->v[b * V + j]),
-                                                                     acc[i], 0, 0, 0);
-            }
-        }
+                for (int v = 0; v < 4; ++v) acc[i].h[h][v] = fmaf(sc, blk[i].h[h][v], acc[i].h[h][v]);
     }
 }
 
@@ -161,30 +185,30 @@ __device__ __forceinline__ void mma_unit(f32x16_t (&acc)[NX], const WUnit<FMT>& 
 __device__ __forceinline__ void split_bf16(float v, uint16_t& hi, uint16_t& lo) {
     hi = f32_to_bf16_rne(v);
     const float r = v - __uint_as_float((uint32_t)hi << 16);
-    // an infinity or NaN is whole in the high half (its rest would be NaN)
-    lo = (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u ? 0 : f32_to_bf16_rne(r);
+    // an infinity (also one that the rounding made) or NaN is whole in the high half
+    lo = (hi & 0x7F80u) == 0x7F80u ? 0 : f32_to_bf16_rne(r);
 }
 
 __device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 constexpr int kRedRow = 36;               // floats of a token's 32 panel rows in LDS, padded
 
-// Adds the waves' accumulators in wave order: red[wave][token][row].
-__device__ __forceinline__ void put_acc(float* red, const f32x16_t& acc, int wave, int tile_tokens, int lane) {
-    const int m = lane & 31, g = lane >> 5;
-    if (m < tile_tokens) {
-        float* p = red + ((int64_t)wave * tile_tokens + m) * kRedRow + 4 * g;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<f32x4_t*>(p + 8 * q) =
-                f32x4_t{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+// The wave's sums of operand set i into red[wave][token][row] (nt tokens).
+__device__ __forceinline__ void put_acc(float* red, const Acc& acc, int i, int wave, int nt, int lane) {
+    const int m = i * kCols + (lane & 15);
+    if (m < nt) {
+        float* p = red + (wave * nt + m) * kRedRow + 4 * (lane >> 4);
+        *reinterpret_cast<f32x4_t*>(p) = acc.h[0];
+        *reinterpret_cast<f32x4_t*>(p + 16) = acc.h[1];
     }
 }
 
-// out[i] = the waves' sum at place tid + i kThreads of the tile's [nt][32]
-__device__ __forceinline__ void sum_waves(float (&out)[kTile * 32 / kThreads], const float* red, int nt, int tid) {
+constexpr int kPlaces = kTile * 32 / kThreads;       // (token, row) places of a tile per thread
+
+// out[i] = the waves' sum, in wave order, at place tid + i kThreads of the tile's [nt][32]
+__device__ __forceinline__ void sum_waves(float (&out)[kPlaces], const float* red, int nt, int tid) {
 #pragma unroll
-    for (int i = 0; i < kTile * 32 / kThreads; ++i) {
+    for (int i = 0; i < kPlaces; ++i) {
         const int t = (tid + i * kThreads) >> 5, n = tid & 31;
         float s = 0.0f;
         if (t < nt) {
