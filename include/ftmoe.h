@@ -479,8 +479,9 @@ ft_status ft_moe_layer(const ft_shape* shape, const uint16_t* x, const uint16_t*
  *   [d x f]), any of them NULL:
  *   h[t] = silu(x Wg + lora_gate(x)) * (x Wu + lora_up(x)),
  *   y[t] = base[t] + h Wd + lora_down(h).
- * fp32 sums, one bf16 rounding of y; the x A products and h keep 16
- * significant bits in between.  An adapter's weights reach only the
+ * fp32 sums, one bf16 rounding of y; the x A products keep 16 significant
+ * bits in between, and so does h up to 64 tokens (above that it may be
+ * rounded to bf16).  An adapter's weights reach only the
  * tokens that name it, and a token's result does not depend on the batch
  * around it beyond the order of fp32 sums.
  * T: 0..65535 (0 enqueues nothing).  x and the weights 16-byte aligned.  base

@@ -20,6 +20,7 @@
 // Router", section "One logical expert, two physical levels of memory".
 #include <type_traits>
 
+#include "resident_api.h"
 #include "wfmt.h"
 
 namespace ftmoe {
@@ -100,12 +101,99 @@ __device__ __forceinline__ bf16x8_t b_frag(const u32x4_t (&r)[Frag<FMT>::LBK], i
     }
 }
 
+// The same of an e4m3 K-step without its scale: the codes' values times the
+// power of two `conv`, exact in bf16.
+template <int LBK>
+__device__ __forceinline__ bf16x8_t b_frag_codes(const u32x4_t (&r)[LBK], int ks, float conv) {
+    const u32x4_t w = r[(ks >> 1) % LBK];
+    const uint32_t w0 = (ks & 1) ? w[2] : w[0];
+    const uint32_t w1 = (ks & 1) ? w[3] : w[1];
+    const bf16x2_t q0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, conv, false);
+    const bf16x2_t q1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, conv, true);
+    const bf16x2_t q2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, conv, false);
+    const bf16x2_t q3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, conv, true);
+    return bf16x8_t{q0[0], q0[1], q1[0], q1[1], q2[0], q2[1], q3[0], q3[1]};
+}
+
 // Wait until at most N vector-memory operations of this wave are outstanding
 // (they complete in issue order); the other counters are left alone.
 template <int N>
 __device__ __forceinline__ void vm_wait() {
     static_assert(N >= 0 && N < 64, "vmcnt holds 6 bits");
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x70 | 0xF00);
+}
+
+// The adapters of a row tile: for each one named in it, acc += v B_a^T on the
+// rows that name it (v as two bf16 planes; B_a's rows are the A operand, 32
+// ranks at a time, masked past the adapter's own).  Other rows' products are
+// selected away, so an adapter's infinities stay with its requests.
+template <bool GU, int MI>
+__device__ __forceinline__ void lora_rows(f32x16_t (&acc)[MI][2], const LoraGemmArgs& a, int row0, int rows_valid,
+                                          const int (&pn)[2], int lane) {
+    const int g = lane >> 5, n = GU ? a.f : a.d;
+    constexpr int POOLS = GU ? 2 : 1;
+#pragma unroll
+    for (int pool = 0; pool < POOLS; ++pool) {
+        const LoraView& lo = a.lora[pool];
+        if (lo.count == 0) continue;
+        const int R = lo.max_rank;
+        int id[MI];
+        uint32_t left[MI];
+        int64_t vrow[MI];
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+            const int r = mi * 32 + (lane & 31);
+            const int v = r < rows_valid ? a.adapter[row0 + r] : -1;
+            id[mi] = (uint32_t)v < (uint32_t)lo.count ? v : -1;
+            left[mi] = (uint32_t)__ballot(id[mi] >= 0);
+            vrow[mi] = (int64_t)(row0 + min(r, rows_valid - 1)) * R + g * 8;
+        }
+        for (;;) {
+            int ad = -1;
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+                if (ad < 0 && left[mi]) ad = __builtin_amdgcn_readlane(id[mi], __builtin_ctz(left[mi]));
+            if (ad < 0) break;
+            uint32_t hit[MI];
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) {
+                hit[mi] = (uint32_t)__ballot(id[mi] == ad);
+                left[mi] &= ~hit[mi];
+            }
+            const int rank = min(max(lo.rank[ad], 0), R);
+            for (int k0 = 0; k0 < rank; k0 += 16) {
+                const int have = rank - k0 - g * 8;      // ranks of this lane's eight that exist
+#pragma unroll
+                for (int ni = 0; ni < 2; ++ni) {
+                    if (GU && ni != pool) continue;
+                    u32x4_t bw = *reinterpret_cast<const u32x4_t*>(
+                        lo.b + ((int64_t)ad * n + pn[ni] * 32 + (lane & 31)) * R + k0 + g * 8);
+                    if (have < 8) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            bw[j] &= have >= 2 * j + 2 ? 0xFFFFFFFFu : have == 2 * j + 1 ? 0xFFFFu : 0u;
+                    }
+                    const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, bw);
+#pragma unroll
+                    for (int mi = 0; mi < MI; ++mi) {
+                        if (!hit[mi]) continue;
+                        u32x4_t h = u32x4_t{0u, 0u, 0u, 0u}, l = h;
+                        if (id[mi] == ad) {
+                            h = *reinterpret_cast<const u32x4_t*>(a.vhi[pool] + vrow[mi] + k0);
+                            l = *reinterpret_cast<const u32x4_t*>(a.vlo[pool] + vrow[mi] + k0);
+                        }
+                        f32x16_t sum;
+#pragma unroll
+                        for (int v = 0; v < 16; ++v) sum[v] = 0.0f;
+                        sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf, __builtin_bit_cast(bf16x8_t, h), sum, 0, 0, 0);
+                        sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf, __builtin_bit_cast(bf16x8_t, l), sum, 0, 0, 0);
+#pragma unroll
+                        for (int v = 0; v < 16; ++v) acc[mi][ni][v] = id[mi] == ad ? acc[mi][ni][v] + sum[v] : acc[mi][ni][v];
+                    }
+                }
+            }
+        }
+    }
 }
 
 // Tile (kBM rows of one slot) x (kBN columns) per workgroup; 4 waves side by
@@ -129,100 +217,134 @@ __device__ __forceinline__ void vm_wait() {
 // rows one ds_read_b128 serves per cycle fall in distinct banks.  Waits are
 // explicit (vmcnt + s_barrier): a __syncthreads would also drain the weight
 // loads that are in flight for later steps.
-template <int FMT, bool GU>
-__global__ void __launch_bounds__(kGemmThreads, 2) gemm_kernel(GemmArgs a) {
+//
+// With LoraGemmArgs (LORA): one resident matrix pair (GU) or matrix for T tokens in order, no
+// plan: row tile i is tokens 128 i ..; before the epilogue each adapter named
+// in the tile adds v B_a^T to its own rows' sums (lora_rows), and the down
+// form adds `base` before the rounding.
+//
+// WM: waves along M.  1 is the tile above; 2 is half of it each way (64 rows x
+// 128 columns, wave (wm, wn) computing 32 x 64), four times the workgroups of
+// a batch that would leave most of the card idle.
+template <int FMT, bool GU, typename Args, int WM>
+__global__ void __launch_bounds__(kGemmThreads, 2) gemm_kernel(Args a) {
+    constexpr bool LORA = std::is_same_v<Args, LoraGemmArgs>;
     using FR = Frag<FMT>;
     constexpr int LBK = FR::LBK;
     constexpr int NB = 2 * LBK;                   // weight loads per wave per K-step
-    __shared__ __attribute__((aligned(1024))) uint16_t As[kStages][kBM * kBK];
+    constexpr int BM = kBM / WM, BN = kBN / WM;   // the tile
+    constexpr int LA = BM / 32;                   // activation loads per wave per K-step
+    constexpr int MMAX = BM / (32 * WM);          // row blocks of a wave
+    __shared__ __attribute__((aligned(1024))) uint16_t As[kStages][BM * kBK];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int w = wave % (4 / WM), wm = wave / (4 / WM);
     // d (a multiple of 128) may end in a half N-tile of the down product: its
     // waves 2 and 3 have no columns, re-read the last panel and store nothing
-    const int NT = GU ? a.f / (kBN / 2) : (a.d + kBN - 1) / kBN;
-    const int V = a.meta[1] * NT;                 // valid workgroups
+    const int NT = GU ? a.f / (BN / 2) : (a.d + BN - 1) / BN;
+    int V;                                        // valid workgroups
+    if constexpr (LORA) V = gridDim.x;
+    else V = a.meta[1] * NT;
     const int b = blockIdx.x;
     if (b >= V) return;
     const int q8 = V >> 3, r8 = V & 7, x8 = b & 7;
     const int lb = x8 * q8 + (x8 < r8 ? x8 : r8) + (b >> 3);
     // within one slot's blocks [t0 NT, (t0 + mt) NT): N-tile major, M-tile minor,
     // so the M-tiles sharing a weight panel run side by side
-    const int ai = a.tile_active[lb / NT];
-    const int t0 = a.tile_first[ai], mt = a.tile_first[ai + 1] - t0;
-    const int local = lb - t0 * NT;
-    const int nt = local / mt;
-    const int tile = t0 + (local - nt * mt);
-    const int row0 = a.tile_row0[tile];
-    const int seg_end = a.seg[ai + 1];
-    const int slot = a.active_slot[ai];
-    int rows_valid = seg_end - row0;
-    rows_valid = rows_valid > kBM ? kBM : rows_valid;
+    int nt, row0, rows_valid;
+    const uint8_t* rec = nullptr;
+    if constexpr (LORA) {
+        const int mt = (a.T + BM - 1) / BM;
+        nt = lb / mt;
+        row0 = (lb - nt * mt) * BM;
+        rows_valid = a.T - row0;
+    } else {
+        const int ai = a.tile_active[lb / NT];
+        const int t0 = a.tile_first[ai], mt = a.tile_first[ai + 1] - t0;
+        const int local = lb - t0 * NT;
+        nt = local / mt;
+        const int tile = t0 + (local - nt * mt);
+        row0 = a.tile_row0[tile];
+        rows_valid = a.seg[ai + 1] - row0;
+        rec = a.pool + (int64_t)a.active_slot[ai] * a.S;
+    }
+    rows_valid = rows_valid > BM ? BM : rows_valid;
     const int K = GU ? a.d : a.f;
-    const uint8_t* rec = a.pool + (int64_t)slot * a.S;
     const int64_t rowb = WF<FMT>::row_bytes(K);
     const int64_t panel_bytes = 32 * rowb;
 
     // this wave's two weight panels (+ lane offset); their scale locations
     const uint8_t* bp[2];
-    int64_t soff[2];
+    const uint8_t* sp[2];
     int pn[2];
     if (GU) {
-        pn[0] = pn[1] = nt * 4 + w;
-        bp[0] = rec + a.off_gate + pn[0] * panel_bytes + lane * 16;
-        bp[1] = rec + a.off_up + pn[1] * panel_bytes + lane * 16;
-        soff[0] = a.off_sg;
-        soff[1] = a.off_su;
+        pn[0] = pn[1] = nt * (BN / 64) + w;
     } else {
         const int last = a.d / 32 - 1;
-        pn[0] = min(nt * 8 + 2 * w, last);
-        pn[1] = min(nt * 8 + 2 * w + 1, last);
+        pn[0] = min(nt * (BN / 32) + 2 * w, last);
+        pn[1] = min(nt * (BN / 32) + 2 * w + 1, last);
+    }
+    if constexpr (LORA) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            bp[i] = a.codes[GU ? i : 0] + pn[i] * panel_bytes + lane * 16;
+            sp[i] = a.scales[GU ? i : 0];
+        }
+    } else if (GU) {
+        bp[0] = rec + a.off_gate + pn[0] * panel_bytes + lane * 16;
+        bp[1] = rec + a.off_up + pn[1] * panel_bytes + lane * 16;
+        sp[0] = rec + a.off_sg;
+        sp[1] = rec + a.off_su;
+    } else {
         bp[0] = rec + a.off_down + pn[0] * panel_bytes + lane * 16;
         bp[1] = rec + a.off_down + pn[1] * panel_bytes + lane * 16;
-        soff[0] = soff[1] = a.off_sd;
+        sp[0] = sp[1] = rec + a.off_sd;
     }
     // per-K-step weight scale of panel i, as stored: FP8 — the 128 x 128
     // block's fp32 (uniform over the panel); MXFP4 — the lane's e8m0 byte for
     // its chunk
     auto scale_of = [&](int i, int kt) -> typename FR::SRaw {
         if constexpr (FMT == FT_FMT_FP8_B128) {
-            return reinterpret_cast<const uint32_t*>(rec + soff[i])[(pn[i] >> 2) * (K >> 7) + (kt >> 1)];
+            return reinterpret_cast<const uint32_t*>(sp[i])[(pn[i] >> 2) * (K >> 7) + (kt >> 1)];
         } else if constexpr (FMT == FT_FMT_MXFP4_B32) {
-            return rec[soff[i] + (int64_t)pn[i] * K + kt * 64 + lane];
+            return sp[i][(int64_t)pn[i] * K + kt * 64 + lane];
         } else {
             return 0;
         }
     };
 
-    // A: wave w fills rows [32 w, 32 w + 32) of a buffer with 4 loads, load i
-    // covering the 1 KiB of rows 32 w + 8 i .. + 7: lane l takes row
-    // 32 w + 8 i + l / 8 at physical chunk l % 8, i.e. logical chunk
-    // (l % 8) ^ (l / 8) ^ (i & 1).  Rows past the tile's end repeat its last
+    // A: wave v fills rows [8 LA v, 8 LA (v + 1)) of a buffer with LA loads, load
+    // i covering the 1 KiB of 8 rows from r = 8 (LA v + i): lane l takes row
+    // r + l / 8 at physical chunk l % 8, i.e. logical chunk
+    // (l % 8) ^ (l / 8) ^ (r / 8 & 1).  Rows past the tile's end repeat its last
     // row: their outputs are never stored.  The loads are buffer loads (byte
     // offsets from x or H, the K-step in the scalar offset); the hardware
     // returns zeros for any offset past the buffer's extent.
     const __amdgpu_buffer_rsrc_t arsrc = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint16_t*>(GU ? a.x : a.Hin), 0, (int)(GU ? a.x_bytes : a.h_bytes), 0x00020000);
-    uint32_t avo[4];
+    uint32_t avo[4];                              // (LA are used)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        int r = 32 * w + 8 * i + (lane >> 3);
+    for (int i = 0; i < LA; ++i) {
+        int r = 8 * (LA * wave + i) + (lane >> 3);
         r = r < rows_valid ? r : rows_valid - 1;
         const int p = row0 + r;
-        const int c = (lane & 7) ^ (lane >> 3) ^ (i & 1);
-        const uint32_t row = GU ? (uint32_t)(a.perm[p] / a.k) * (uint32_t)a.d : (uint32_t)p * (uint32_t)a.f;
+        const int c = (lane & 7) ^ (lane >> 3) ^ ((LA * wave + i) & 1);
+        uint32_t row;
+        if constexpr (GU && !LORA) row = (uint32_t)(a.perm[p] / a.k) * (uint32_t)a.d;
+        else row = (uint32_t)p * (uint32_t)K;
         avo[i] = (row + (uint32_t)c * 8u) * 2u;
     }
     const int KT = K / kBK;        // even: K is a multiple of 128
     auto load_a = [&](int kt, int stage) {
         const int ks = kt < KT ? kt : KT - 1;       // past the end: reload the last step (never read)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < LA; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                arsrc, (__attribute__((address_space(3))) void*)(&As[stage][(4 * w + i) * 512]), 16, avo[i],
+                arsrc, (__attribute__((address_space(3))) void*)(&As[stage][(LA * wave + i) * 512]), 16, avo[i],
                 ks * kBK * 2, 0, 0);
     };
 
-    // The tile's MI = ceil(rows_valid / 32) row blocks are all that is
+    // The wave's MI = ceil(its valid rows / 32) row blocks are all that is
     // computed: a short last tile of an expert (its few leftover rows) costs
     // MI / 4 of a full tile's MFMAs.
     auto body = [&](auto mi_count) {
@@ -257,15 +379,16 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_kernel(GemmArgs a) {
         // A operand of MFMA step ks for the MI row blocks, from buffer `stage`
         const int m = lane & 31;
         const int fm = (m & 7) ^ ((m >> 3) & 1);
+        const int rm = WM == 1 ? 0 : wm * 32 * MMAX;          // the wave's first row
         auto read_a = [&](bf16x8_t (&af)[MI], int stage, int ks) {
             const int c = FR::a_koff(ks, g) >> 3;
 #pragma unroll
             for (int mi = 0; mi < MI; ++mi)
-                af[mi] = *reinterpret_cast<const bf16x8_t*>(&As[stage][(mi * 32 + m) * kBK + ((c ^ fm) << 3)]);
+                af[mi] = *reinterpret_cast<const bf16x8_t*>(&As[stage][(rm + mi * 32 + m) * kBK + ((c ^ fm) << 3)]);
         };
         bf16x8_t af[2][MI];
         // A(0) has landed once only A(1) and A(2) may be outstanding
-        vm_wait<8>();
+        vm_wait<2 * LA>();
         __builtin_amdgcn_s_barrier();
         read_a(af[0], 0, 0);
 
@@ -282,24 +405,61 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_kernel(GemmArgs a) {
         // scheduling barriers: the compiler would otherwise sink every prefetch
         // below the last MFMA.
         constexpr int RP = 2 * (LBK - 1);             // refills issued before A(kt + 3)
+        // Block-FP8 beside adapters: the codes are multiplied as they are (exact in
+        // bf16) and the accumulators are kept in units of the current block's
+        // scale, rescaled when the next 128 K begin; the grouped form rounds code
+        // times scale to bf16 instead.  A unit stays at 2^-90 or above, so that
+        // rescaling cannot overflow: smaller scales keep a factor 2^-36 in the
+        // codes (exact), and zero or subnormal ones leave the unit and put the
+        // codes below everything.
+        constexpr bool UNITS = LORA && FMT == FT_FMT_FP8_B128;
+        float unit[2] = {0x1p-90f, 0x1p-90f}, conv[2] = {1.0f, 1.0f};
+        auto begin_block = [&](const typename FR::SRaw (&bss)[2]) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float s = __uint_as_float(__builtin_amdgcn_readfirstlane((int)bss[i]));
+                const float mag = fabsf(s);
+                if (mag < 0x1p-126f) {
+                    conv[i] = 0x1p-126f;
+                    continue;
+                }
+                conv[i] = mag < 0x1p-90f ? 0x1p-36f : 1.0f;
+                const float u = mag < 0x1p-90f ? s * 0x1p36f : s;
+                const float r = unit[i] / u;
+                unit[i] = u;
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[mi][i][v] *= r;
+            }
+        };
         auto kstep = [&](int kt, int stage, u32x4_t (&brs)[2][LBK], typename FR::SRaw (&bss)[2]) {
+            if constexpr (UNITS) {
+                if ((kt & 1) == 0) begin_block(bss);
+            }
             const int kw = kt + 2 < KT ? kt + 2 : KT - 1;     // weights refilled for two steps ahead
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
                 if (ks < 3) {
                     read_a(af[(ks + 1) & 1], stage, ks + 1);
                 } else {
-                    if (kt >= 2) vm_wait<2 * NB + 4>();
-                    else if (kt == 1) vm_wait<NB + 4 + RP>();
-                    else vm_wait<4 + RP>();
+                    if (kt >= 2) vm_wait<2 * NB + LA>();
+                    else if (kt == 1) vm_wait<NB + LA + RP>();
+                    else vm_wait<LA + RP>();
                     __builtin_amdgcn_s_barrier();
                     __builtin_amdgcn_sched_barrier(0);
                     load_a(kt + 3, (stage + 3) % kStages);
                     __builtin_amdgcn_sched_barrier(0);
                     read_a(af[0], (stage + 1) % kStages, 0);
                 }
-                const bf16x8_t b0 = b_frag<FMT>(brs[0], ks, bss[0]);
-                const bf16x8_t b1 = b_frag<FMT>(brs[1], ks, bss[1]);
+                bf16x8_t b0, b1;
+                if constexpr (UNITS) {
+                    b0 = b_frag_codes(brs[0], ks, conv[0]);
+                    b1 = b_frag_codes(brs[1], ks, conv[1]);
+                } else {
+                    b0 = b_frag<FMT>(brs[0], ks, bss[0]);
+                    b1 = b_frag<FMT>(brs[1], ks, bss[1]);
+                }
 #pragma unroll
                 for (int mi = 0; mi < MI; ++mi) {
                     acc[mi][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b0, af[ks & 1][mi], acc[mi][0], 0, 0, 0);
@@ -341,6 +501,16 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_kernel(GemmArgs a) {
         vm_wait<0>();
         __builtin_amdgcn_s_barrier();
 
+        if constexpr (UNITS) {
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[mi][i][v] *= unit[i];
+        }
+        if constexpr (LORA) lora_rows<GU, MI>(acc, a, row0 + rm, max(rows_valid - rm, 0), pn, lane);
+
         // Epilogue.  The MFMAs compute C^T (weights as the A operand), so lane l
         // holds row mi*32 + l%32 and, per group q, the four consecutive columns
         // 8q + 4(l/32) .. +3 of each 32-column panel.  The tile goes through LDS
@@ -348,9 +518,9 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_kernel(GemmArgs a) {
         // instruction writes whole contiguous row segments.
         if (GU) {
             // h = silu(g) * u, the whole 128 x 128 bf16 tile, rows padded by 16 bytes
-            constexpr int LDH = kBN / 2 + 8;
+            constexpr int LDH = BN / 2 + 8;
             uint16_t* Hs = &As[0][0];
-            static_assert(kBM * LDH <= kStages * kBM * kBK, "h tile must fit the A buffers");
+            static_assert(BM * LDH <= kStages * BM * kBK, "h tile must fit the A buffers");
 #pragma unroll
             for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
@@ -361,23 +531,25 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_kernel(GemmArgs a) {
                     uint2 o;
                     o.x = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{h[0], h[1]}, bf16x2_t));
                     o.y = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{h[2], h[3]}, bf16x2_t));
-                    *reinterpret_cast<uint2*>(&Hs[(mi * 32 + m) * LDH + 32 * w + 8 * q + 4 * g]) = o;
+                    *reinterpret_cast<uint2*>(&Hs[(rm + mi * 32 + m) * LDH + 32 * w + 8 * q + 4 * g]) = o;
                 }
             __syncthreads();
-            // 16 lanes per 256-byte row, 16 rows per pass
+            // LR lanes per row (16 for 256 bytes), whole rows per pass
+            constexpr int LR = BN / 16, RPP = kGemmThreads / LR;
+            constexpr int ROWS = WM == 1 ? MI * 32 : BM;
 #pragma unroll
-            for (int it = 0; it < MI * 2; ++it) {
-                const int r = it * 16 + (tid >> 4), c = (tid & 15) * 8;
+            for (int it = 0; it < ROWS / RPP; ++it) {
+                const int r = it * RPP + tid / LR, c = (tid % LR) * 8;
                 if (r < rows_valid)
-                    *reinterpret_cast<u32x4_t*>(a.Hout + (int64_t)(row0 + r) * a.f + nt * (kBN / 2) + c) =
+                    *reinterpret_cast<u32x4_t*>(a.Hout + (int64_t)(row0 + r) * a.f + nt * (BN / 2) + c) =
                         *reinterpret_cast<const u32x4_t*>(&Hs[r * LDH + c]);
             }
         } else {
             // per wave: 32 rows x 64 bf16 columns at a time, rows padded by 16 bytes
             constexpr int LDY = 64 + 8;
-            uint16_t* Ys = &As[0][0] + w * 32 * LDY;
-            const bool col_ok = nt * kBN + 64 * w < a.d;
-            static_assert(4 * 32 * LDY <= kStages * kBM * kBK, "y tiles must fit the A buffers");
+            uint16_t* Ys = &As[0][0] + wave * 32 * LDY;
+            const bool col_ok = nt * BN + 64 * w < a.d;
+            static_assert(4 * 32 * LDY <= kStages * BM * kBK, "y tiles must fit the A buffers");
 #pragma unroll
             for (int mi = 0; mi < MI; ++mi) {
 #pragma unroll
@@ -385,6 +557,17 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_kernel(GemmArgs a) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint2 o;
+                        if constexpr (LORA) {
+                            if (a.base) {
+                                const int r = min(rm + mi * 32 + m, rows_valid - 1);
+                                const uint2 bv = *reinterpret_cast<const uint2*>(
+                                    a.base + (int64_t)(row0 + r) * a.d + pn[ni] * 32 + 8 * q + 4 * g);
+                                acc[mi][ni][4 * q] += bf16lo(bv.x);
+                                acc[mi][ni][4 * q + 1] += bf16hi(bv.x);
+                                acc[mi][ni][4 * q + 2] += bf16lo(bv.y);
+                                acc[mi][ni][4 * q + 3] += bf16hi(bv.y);
+                            }
+                        }
                         o.x = __builtin_bit_cast(uint32_t, __builtin_convertvector(
                                   f32x2_t{acc[mi][ni][4 * q], acc[mi][ni][4 * q + 1]}, bf16x2_t));
                         o.y = __builtin_bit_cast(uint32_t, __builtin_convertvector(
@@ -399,9 +582,9 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_kernel(GemmArgs a) {
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
                     const int rr = it * 8 + (lane >> 3), c = (lane & 7) * 8;
-                    const int r = mi * 32 + rr;
+                    const int r = rm + mi * 32 + rr;
                     if (r < rows_valid && col_ok)
-                        *reinterpret_cast<u32x4_t*>(a.Y + (int64_t)(row0 + r) * a.d + nt * kBN + 64 * w + c) =
+                        *reinterpret_cast<u32x4_t*>(a.Y + (int64_t)(row0 + r) * a.d + nt * BN + 64 * w + c) =
                             *reinterpret_cast<const u32x4_t*>(&Ys[rr * LDY + c]);
                 }
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -410,21 +593,25 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_kernel(GemmArgs a) {
             }
         }
     };
-    const int nmi = (rows_valid + 31) >> 5;
-    if (nmi >= 4) body(std::integral_constant<int, 4>{});
-    else if (nmi == 3) body(std::integral_constant<int, 3>{});
-    else if (nmi == 2) body(std::integral_constant<int, 2>{});
-    else body(std::integral_constant<int, 1>{});
+    if constexpr (WM == 1) {
+        const int nmi = (rows_valid + 31) >> 5;
+        if (nmi >= 4) body(std::integral_constant<int, 4>{});
+        else if (nmi == 3) body(std::integral_constant<int, 3>{});
+        else if (nmi == 2) body(std::integral_constant<int, 2>{});
+        else body(std::integral_constant<int, 1>{});
+    } else {
+        body(std::integral_constant<int, MMAX>{});     // (a wave past the rows computes on the last one)
+    }
 }
 
 template <int FMT>
 hipError_t launch_fmt(const GemmArgs& a, int64_t max_tiles, Timing* tm, hipStream_t st) {
     const int64_t g1 = max_tiles * (a.f / (kBN / 2)), g2 = max_tiles * ((a.d + kBN - 1) / kBN);
     TimedLaunch t1 = timing_launch(tm, FT_K_GEMM_GU);
-    hipExtLaunchKernelGGL((gemm_kernel<FMT, true>), dim3((unsigned)g1), dim3(kGemmThreads), 0, st, t1.start, t1.stop,
+    hipExtLaunchKernelGGL((gemm_kernel<FMT, true, GemmArgs, 1>), dim3((unsigned)g1), dim3(kGemmThreads), 0, st, t1.start, t1.stop,
                           0, a);
     TimedLaunch t2 = timing_launch(tm, FT_K_GEMM_DOWN);
-    hipExtLaunchKernelGGL((gemm_kernel<FMT, false>), dim3((unsigned)g2), dim3(kGemmThreads), 0, st, t2.start,
+    hipExtLaunchKernelGGL((gemm_kernel<FMT, false, GemmArgs, 1>), dim3((unsigned)g2), dim3(kGemmThreads), 0, st, t2.start,
                           t2.stop, 0, a);
     return hipGetLastError();
 }
@@ -469,6 +656,34 @@ hipError_t launch_gemm(ft_cache* c, const uint16_t* x, int T, hipStream_t st) {
         case FT_FMT_MXFP4_B32: return launch_fmt<FT_FMT_MXFP4_B32>(a, max_tiles, c->timing, st);
     }
     return hipErrorInvalidValue;
+}
+
+// The half tile while the full one would give the 256 CUs less than a workgroup each.
+template <int FMT, bool GU>
+void launch_lora_fmt(const LoraGemmArgs& a, hipStream_t st) {
+    const int cols = GU ? 2 * a.f : a.d;
+    const int64_t full = (int64_t)((a.T + kBM - 1) / kBM) * ((cols + kBN - 1) / kBN);
+    const bool half = full < 256;
+    const int bm = half ? kBM / 2 : kBM, bn = half ? kBN / 2 : kBN;
+    const dim3 grid((unsigned)(((a.T + bm - 1) / bm) * ((cols + bn - 1) / bn)));
+    if (half) hipLaunchKernelGGL((gemm_kernel<FMT, GU, LoraGemmArgs, 2>), grid, dim3(kGemmThreads), 0, st, a);
+    else hipLaunchKernelGGL((gemm_kernel<FMT, GU, LoraGemmArgs, 1>), grid, dim3(kGemmThreads), 0, st, a);
+}
+
+template <int FMT>
+void launch_lora_fmt(const LoraGemmArgs& a, bool gu, hipStream_t st) {
+    if (gu) launch_lora_fmt<FMT, true>(a, st);
+    else launch_lora_fmt<FMT, false>(a, st);
+}
+
+hipError_t launch_lora_gemm(int fmt, bool gu, const LoraGemmArgs& a, hipStream_t st) {
+    switch (fmt) {
+        case FT_FMT_BF16: launch_lora_fmt<FT_FMT_BF16>(a, gu, st); break;
+        case FT_FMT_FP8_B128: launch_lora_fmt<FT_FMT_FP8_B128>(a, gu, st); break;
+        case FT_FMT_MXFP4_B32: launch_lora_fmt<FT_FMT_MXFP4_B32>(a, gu, st); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
 }
 
 }  // namespace ftmoe

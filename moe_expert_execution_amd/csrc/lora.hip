@@ -349,6 +349,15 @@ void launch_project_nx(const ProjectArgs& a, hipStream_t st) {
         hipLaunchKernelGGL((lora_project_kernel<FMT, NM, PL, 2>), grid, dim3(kThreads), lds_bytes(a.T), st, a);
 }
 
+// Prompts: from this many tokens on the 128-row GEMM tiles are faster than
+// streaming the weights once per 32 tokens.  They reach rows by 32-bit
+// offsets and move outputs in 16-byte pieces; other calls stream.
+constexpr int kGemmTokens = 256;
+bool gemm_fits(int T, int K, const void* y, const void* base) {
+    return T >= kGemmTokens && (int64_t)T * K * 2 < (1ll << 32) && (reinterpret_cast<uintptr_t>(y) & 15) == 0 &&
+           (reinterpret_cast<uintptr_t>(base) & 15) == 0;
+}
+
 template <int NM, int PL>
 hipError_t launch_project(int fmt, const ProjectArgs& a, hipStream_t st) {
     switch (fmt) {
@@ -445,6 +454,23 @@ hipError_t launch_lora_project(const MatrixView& m, const LoraView* lora, const 
         a.vlo[0] = s.vlo[0];
         o = 2 * plane;
     }
+    if (gemm_fits(T, m.K, y, base)) {
+        LoraGemmArgs g = {};
+        g.Hin = x;
+        g.Y = y;
+        g.T = T;
+        g.d = m.n;
+        g.f = m.K;
+        g.h_bytes = (uint32_t)((int64_t)T * m.K * 2);
+        g.codes[0] = m.codes;
+        g.scales[0] = m.scales;
+        g.lora[0] = a.lora[0];
+        g.vhi[0] = a.vhi[0];
+        g.vlo[0] = a.vlo[0];
+        g.adapter = adapter;
+        g.base = base;
+        return launch_lora_gemm(m.fmt, false, g, st);
+    }
     a.part = reinterpret_cast<float*>(mem + o);
     return launch_project<1, 1>(m.fmt, a, st);
 }
@@ -483,6 +509,30 @@ hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const 
     hipError_t e;
     if (n > 0 && (e = launch_shrink(s, n, st)) != hipSuccess) return e;
 
+    const bool gemm = gemm_fits(T, sh.d_model > sh.d_ff ? sh.d_model : sh.d_ff, y, base);
+    LoraGemmArgs gm = {};
+    if (gemm) {
+        gm.x = x;
+        gm.Hin = gm.Hout = hhi;
+        gm.Y = y;
+        gm.T = T;
+        gm.d = sh.d_model;
+        gm.f = sh.d_ff;
+        gm.x_bytes = (uint32_t)((int64_t)T * sh.d_model * 2);
+        gm.h_bytes = (uint32_t)((int64_t)T * sh.d_ff * 2);
+        gm.codes[0] = rec + rl.off_gate;
+        gm.codes[1] = rec + rl.off_up;
+        gm.scales[0] = rec + rl.off_sg;
+        gm.scales[1] = rec + rl.off_su;
+        for (int i = 0; i < 2; ++i) {
+            gm.lora[i] = gu[i] ? *gu[i] : LoraView();
+            gm.vhi[i] = v_hi(i);
+            gm.vlo[i] = v_lo(i);
+        }
+        gm.adapter = adapter;
+        if ((e = launch_lora_gemm(sh.fmt, true, gm, st)) != hipSuccess) return e;
+    }
+
     ProjectArgs a = {};
     a.codes[0] = rec + rl.off_gate;
     a.codes[1] = rec + rl.off_up;
@@ -503,7 +553,7 @@ hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const 
     a.counters = reinterpret_cast<uint32_t*>(ws->mem);
     a.hhi = hhi;
     a.hlo = hlo;
-    if ((e = launch_project<2, 1>(sh.fmt, a, st)) != hipSuccess) return e;
+    if (!gemm && (e = launch_project<2, 1>(sh.fmt, a, st)) != hipSuccess) return e;
 
     if (down && down->count > 0) {
         ShrinkArgs d = {};
@@ -513,11 +563,20 @@ hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const 
         d.vlo[0] = v_lo(2);
         d.adapter = adapter;
         d.xhi = hhi;
-        d.xlo = hlo;
+        d.xlo = gemm ? nullptr : hlo;
         d.T = T;
         d.K = sh.d_ff;
         d.panels = down->max_rank / 16;
         if ((e = launch_shrink(d, 1, st)) != hipSuccess) return e;
+    }
+    if (gemm) {
+        gm.codes[0] = rec + rl.off_down;
+        gm.scales[0] = rec + rl.off_sd;
+        gm.lora[0] = down ? *down : LoraView();
+        gm.vhi[0] = v_hi(2);
+        gm.vlo[0] = v_lo(2);
+        gm.base = base;
+        return launch_lora_gemm(sh.fmt, false, gm, st);
     }
     ProjectArgs c = {};
     c.codes[0] = rec + rl.off_down;

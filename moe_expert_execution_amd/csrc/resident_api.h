@@ -56,6 +56,26 @@ struct MatrixView {
     const uint8_t* codes;
     const uint8_t* scales;
 };
+// The prompt-length products (gemm.hip): GU reads x [T x d] and writes h = silu(.) * (.)
+// [T x f] in bf16 from the matrices codes[0], codes[1]; otherwise reads Hin [T x f] and
+// writes Y [T x d] from codes[0].
+struct LoraGemmArgs {
+    const uint16_t* x;
+    const uint16_t* Hin;
+    uint16_t* Hout;
+    uint16_t* Y;
+    int T, d, f;
+    uint32_t x_bytes, h_bytes;         // extents of x and Hin, below 4 GiB
+    const uint8_t* codes[2];
+    const uint8_t* scales[2];
+    LoraView lora[2];
+    const uint16_t* vhi[2];
+    const uint16_t* vlo[2];
+    const int32_t* adapter;
+    const uint16_t* base;
+};
+hipError_t launch_lora_gemm(int fmt, bool gu, const LoraGemmArgs& a, hipStream_t st);
+
 size_t lora_project_call_bytes(int n, int K, int max_rank, int T);
 size_t lora_expert_call_bytes(const ft_shape& s, int max_rank, int T);
 size_t lora_project_workspace(int n, int K, int max_rank, int max_tokens);
