@@ -16,160 +16,184 @@ namespace {
 
 using namespace rs;
 
-// ---- the adapters of a tile of 32 tokens ------------------------------------------
+// ---- the adapters of a tile -----------------------------------------------------------
 
-// Calls body(i, a) for the distinct adapters a of a tile, in the order of
-// their first token; `id` is the lane's token's adapter, -1 for none (lanes l
-// and l + 32 hold the same token).  The loop is the same in every lane.
-template <typename F>
-__device__ __forceinline__ void each_adapter(int id, F&& body) {
-    uint32_t left = (uint32_t)__ballot(id >= 0);
-    for (int i = 0; left; ++i) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-        body(i, a);
-        left &= ~(uint32_t)__ballot(id == a);
-    }
+// DEPTH steps in flight: load(b, i) fills buffer b for step i, work(b, i) uses it.
+template <int DEPTH, typename L, typename W>
+__device__ __forceinline__ void pipelined(int n, L&& load, W&& work) {
+#pragma unroll
+    for (int b = 0; b < DEPTH; ++b)
+        if (b < n) load(b, b);
+    for (int i = 0; i < n; i += DEPTH)
+#pragma unroll
+        for (int b = 0; b < DEPTH; ++b)
+            if (i + b < n) {
+                work(b, i + b);
+                if (i + b + DEPTH < n) load(b, i + b + DEPTH);
+            }
 }
 
-// The lane's token's adapter; ids outside the pool name none.
+// The adapter of token t0 + lane % N; ids outside the pool name none (-1).
+template <int N>
 __device__ __forceinline__ int tile_adapter(const int32_t* adapter, int t0, int T, int count, int lane) {
-    const int t = t0 + (lane & 31);
+    const int t = t0 + (lane & (N - 1));
     const int id = t < T ? adapter[t] : -1;
     return (uint32_t)id < (uint32_t)count ? id : -1;
 }
 
+// A tile's adapters as steps of RS ranks, in the order of their first token.
+struct Step {
+    int a, r0, rank;
+    float scale;
+};
+constexpr int kMaxSteps = kTile * kMaxRank / 16;
+constexpr int kMaxFusedSteps = 16;        // 16-rank steps per pool that a product's launch takes along
+constexpr int kMaxParts = 4;              // parts of K of a shrink launch
+
+// One wave writes the steps of the pool for the tile's 32 tokens; returns
+// their number in *n.
+template <int RS>
+__device__ __forceinline__ void list_steps(Step* steps, int* n, const LoraView& lo, int id, int lane) {
+    int rank = 0;
+    float scale = 0.0f;
+    if (lo.count > 0 && lo.count <= 64) {      // the whole pool's ranks and scales at once, not behind the ids
+        const int c = min(lane, lo.count - 1);
+        const int r = lo.rank[c];
+        const float sc = lo.scale[c];
+        rank = __shfl(r, id & 63, 64);
+        scale = __shfl(sc, id & 63, 64);
+    } else if (id >= 0) {
+        rank = lo.rank[id];
+        scale = lo.scale[id];
+    }
+    rank = id >= 0 ? min(max(rank, 0), lo.max_rank) : 0;
+    bool first = id >= 0 && lane < kTile;
+#pragma unroll
+    for (int o = 1; o < kTile; ++o) {
+        const int other = __shfl(id, lane - o, 64);
+        first = first && (o > lane || other != id);
+    }
+    const int mine = first ? (rank + RS - 1) / RS : 0;
+    int at = mine;
+#pragma unroll
+    for (int o = 1; o < kTile; o <<= 1) {
+        const int v = __shfl_up(at, o, 64);
+        if (lane >= o) at += v;
+    }
+    if (lane == kTile - 1) *n = at;
+    at -= mine;
+    for (int q = 0; q < mine; ++q) steps[at + q] = Step{id, q * RS, rank, scale};
+}
+
 struct ShrinkArgs {
     LoraView lora[2];
-    uint16_t* vhi[2];      // [T][R] v as two bf16 planes
+    uint16_t* vhi[2];      // [T][R] v as two bf16 planes (prompts), or
     uint16_t* vlo[2];
+    float* vpart[2];       // [parts][T][R] its sums over the parts of K
     const int32_t* adapter;
     const uint16_t* xhi;
     const uint16_t* xlo;   // second plane of x (PL = 2)
     int T, K, panels;      // rank panels of 16 per projection
+    int parts;             // parts of K
 };
 
-// Workgroup (tile of 32 tokens, stride over the tile's adapters, projection
-// and 16 ranks): v for every token of the adapter; the waves split K.  Both
-// operands are row-major: of 128 K a lane takes 32 consecutive ones, so the
-// four lanes of a row use its 256 bytes.
-template <int PL>
+constexpr int kSpan = 64;             // tokens of a shrink workgroup, one per lane
+
+// Workgroup (span of 64 tokens, stride over the span's adapters, projection,
+// 16 ranks and part of K): v for every token of the adapter, gathered from the
+// span as columns; the waves split the part.  Both operands are row-major: of 128 K a lane
+// takes 32 consecutive ones, so the four lanes of a row use its 256 bytes.
+template <int PL, int NX>
 __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(ShrinkArgs s) {
     extern __shared__ __attribute__((aligned(16))) float red[];
+    __shared__ uint8_t cols[kWaves][kSpan];         // (a copy per wave: no barrier)
+    constexpr int CW = NX * kCols;                  // columns of a pass
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-    const int t0 = blockIdx.x * kTile, nt = min(kTile, s.T - t0);
-    const int proj = blockIdx.z / s.panels, r0 = (blockIdx.z - proj * s.panels) * 16;
+    const int t0 = blockIdx.x * kSpan;
+    const int part = blockIdx.z % s.parts, pp = blockIdx.z / s.parts;
+    const int proj = pp / s.panels, r0 = (pp - proj * s.panels) * 16;
     const LoraView lo = s.lora[proj];
     const int R = lo.max_rank;
     if (r0 >= R) return;
-    const int id = tile_adapter(s.adapter, t0, s.T, lo.count, lane);
+    const int id = tile_adapter<kSpan>(s.adapter, t0, s.T, lo.count, lane);
+    int ranks = 0;
+    float scales = 0.0f;
+    if (id >= 0) {
+        ranks = min(max(lo.rank[id], 0), R);
+        scales = lo.scale[id];
+    }
     const int units = s.K / kUnit;
-    const int u0 = wid * units / kWaves, u1 = (wid + 1) * units / kWaves;
-    int64_t xo[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) xo[i] = (int64_t)(t0 + min(i * kCols + (lane & 15), nt - 1)) * s.K;
-    const int nx = nt > kCols ? 2 : 1;
-    each_adapter(id, [&](int i, int a) {
-        if (i % (int)gridDim.y != (int)blockIdx.y) return;
-        const int rank = min(max(lo.rank[a], 0), R);
-        if (r0 >= rank) return;           // the expand reads v in steps of 16 up to the rank
+    const int me = part * kWaves + wid, all = s.parts * kWaves;
+    const int u0 = me * units / all, u1 = (me + 1) * units / all;
+    uint64_t left = __ballot(id >= 0);
+    for (int i = 0; left; ++i) {
+        const int src = __builtin_ctzll(left);
+        const int a = __builtin_amdgcn_readlane(id, src);
+        const uint64_t hit = __ballot(id == a);
+        left &= ~hit;
+        if (i % (int)gridDim.y != (int)blockIdx.y) continue;
+        const int rank = __builtin_amdgcn_readlane(ranks, src);
+        if (r0 >= rank) continue;         // the expand reads v in steps of 16 up to the rank
+        const float scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scales), src));
+        if (id == a) cols[wid][__popcll(hit & ((1ull << lane) - 1))] = (uint8_t)lane;
+        const int nc = __popcll(hit);
         const uint16_t* arow = lo.a + ((int64_t)a * R + min(r0 + (lane & 15), rank - 1)) * s.K;
-        f32x4_t acc[2] = {f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}};
-        XUnit au[2], x[2][2][PL];
-        auto load = [&](int b, int u) {
-            load_x<FT_FMT_MXFP4_B32>(au[b], arow, u, lane);
+        for (int c0 = 0; c0 < nc; c0 += CW) {
+            const int n = min(CW, nc - c0);
+            int64_t xo[NX];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-                if (q < nx) {
-                    load_x<FT_FMT_MXFP4_B32>(x[b][q][0], s.xhi + xo[q], u, lane);
-                    if constexpr (PL == 2) load_x<FT_FMT_MXFP4_B32>(x[b][q][PL - 1], s.xlo + xo[q], u, lane);
+            for (int q = 0; q < NX; ++q)
+                xo[q] = (int64_t)(t0 + cols[wid][c0 + min(q * kCols + (lane & 15), n - 1)]) * s.K;
+            f32x4_t acc[NX];
+#pragma unroll
+            for (int q = 0; q < NX; ++q) acc[q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            XUnit au[2], x[2][NX][PL];
+            pipelined<2>(
+                u1 - u0,
+                [&](int b, int u) {
+                    load_x<FT_FMT_MXFP4_B32>(au[b], arow, u0 + u, lane);
+#pragma unroll
+                    for (int q = 0; q < NX; ++q)
+                        if (q == 0 || q * kCols < n) {
+                            load_x<FT_FMT_MXFP4_B32>(x[b][q][0], s.xhi + xo[q], u0 + u, lane);
+                            if constexpr (PL == 2) load_x<FT_FMT_MXFP4_B32>(x[b][q][PL - 1], s.xlo + xo[q], u0 + u, lane);
+                        }
+                },
+                [&](int b, int) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+#pragma unroll
+                        for (int q = 0; q < NX; ++q)
+                            if (q == 0 || q * kCols < n)
+#pragma unroll
+                                for (int p = 0; p < PL; ++p)
+                                    acc[q] = mma(__builtin_bit_cast(bf16x8_t, au[b].v[v]), x[b][q][p].v[v], acc[q]);
+                });
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < NX; ++q) {
+                const int m = q * kCols + (lane & 15);
+                if (m < n) *reinterpret_cast<f32x4_t*>(red + (wid * n + m) * 20 + 4 * (lane >> 4)) = acc[q];
+            }
+            __syncthreads();
+            for (int q = tid; q < n * 16; q += kThreads) {
+                const int m = q >> 4, r = r0 + (q & 15);
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) v += red[(w * n + m) * 20 + (q & 15)];
+                v = r < rank ? scale * v : 0.0f;
+                const int64_t o = (int64_t)(t0 + cols[wid][c0 + m]) * R + r;
+                if (s.vpart[proj]) {
+                    s.vpart[proj][(int64_t)part * s.T * R + o] = v;
+                } else {
+                    uint16_t h, l;
+                    split_bf16(v, h, l);              // 16 significant bits
+                    s.vhi[proj][o] = h;
+                    s.vlo[proj][o] = l;
                 }
-        };
-        auto step = [&](int b) {
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (q < nx)
-#pragma unroll
-                        for (int p = 0; p < PL; ++p)
-                            acc[q] = mma(__builtin_bit_cast(bf16x8_t, au[b].v[v]), x[b][q][p].v[v], acc[q]);
-        };
-        if (u0 < u1) load(0, u0);
-        for (int u = u0; u < u1; u += 2) {
-            if (u + 1 < u1) load(1, u + 1);
-            step(0);
-            if (u + 1 < u1) {
-                if (u + 2 < u1) load(0, u + 2);
-                step(1);
             }
-        }
-        // 16 ranks of up to 32 tokens: one place per thread
-        __syncthreads();
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int m = q * kCols + (lane & 15);
-            if (m < nt) *reinterpret_cast<f32x4_t*>(red + (wid * nt + m) * 20 + 4 * (lane >> 4)) = acc[q];
-        }
-        __syncthreads();
-        const int t = tid >> 4, n = r0 + (tid & 15);
-        if (t < nt && s.adapter[t0 + t] == a) {
-            float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) v += red[(w * nt + t) * 20 + (tid & 15)];
-            // v in 16 significant bits; zero past the adapter's rank
-            uint16_t h, l;
-            split_bf16(n < rank ? lo.scale[a] * v : 0.0f, h, l);
-            const int64_t o = (int64_t)(t0 + t) * R + n;
-            s.vhi[proj][o] = h;
-            s.vlo[proj][o] = l;
-        }
-    });
-}
-
-// acc += v B_a^T for row panel p of B [n x R] and the 16 tokens `id` (the
-// lane's column's adapter) and `t` (its token); the other tokens' products
-// are selected away (an adapter's infinities and NaN stay with its own
-// requests), and ranks past the adapter's own are masked out of B, whatever
-// the pool holds there.
-__device__ __forceinline__ void expand(Acc& acc, const LoraView& lo, const uint16_t* vhi, const uint16_t* vlo, int n,
-                                       int p, int a, int id, int t, int lane) {
-    if (__ballot(id == a) == 0) return;
-    const int R = lo.max_rank, g = lane >> 4;
-    const int rank = min(max(lo.rank[a], 0), R);
-    const uint16_t* brow = lo.b + ((int64_t)a * n + p * 32 + (lane & 15)) * R + g * 8;
-    const int64_t vo = (int64_t)t * R + g * 8;
-    const u32x4_t none = u32x4_t{0u, 0u, 0u, 0u};
-    Acc sum = zero_acc();
-    for (int k0 = 0; k0 < rank; k0 += 32) {
-        u32x4_t b[2] = {none, none}, h = none, l = none;
-        const int left = rank - k0 - g * 8;          // ranks of this lane's eight that exist
-        if (left > 0) {
-            b[0] = *reinterpret_cast<const u32x4_t*>(brow + k0);
-            b[1] = *reinterpret_cast<const u32x4_t*>(brow + 16 * R + k0);
-            if (id == a) {
-                h = *reinterpret_cast<const u32x4_t*>(vhi + vo + k0);
-                l = *reinterpret_cast<const u32x4_t*>(vlo + vo + k0);
-            }
-        }
-        if (left < 8) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t keep = left >= 2 * j + 2 ? 0xFFFFFFFFu : left == 2 * j + 1 ? 0xFFFFu : 0u;
-                b[0][j] &= keep;
-                b[1][j] &= keep;
-            }
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, b[q]);
-            sum.h[q] = mma(bf, h, sum.h[q]);
-            sum.h[q] = mma(bf, l, sum.h[q]);
         }
     }
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc.h[q][v] = id == a ? acc.h[q][v] + sum.h[q][v] : acc.h[q][v];
 }
 
 // ---- the projections -----------------------------------------------------------------
@@ -178,90 +202,317 @@ struct ProjectArgs {
     const uint8_t* codes[2];
     const uint8_t* scales[2];
     LoraView lora[2];          // count 0: no adapters
-    const uint16_t* vhi[2];
-    const uint16_t* vlo[2];
+    const float* v[2];         // v of the shrink launch [vparts][T][R] (null: computed here)
+    int vparts;
     const int32_t* adapter;
     const uint16_t* xhi;
     const uint16_t* xlo;       // second plane of x (PL = 2)
-    int T, n, K, splits;
-    float* part;               // [splits][NM][T][n]
-    uint32_t* counters;        // one per (panel, tile) with several splits
+    int T, n, K;
+    int splits;                // workgroups of a (panel, tile) that split K
+    int lsplits;               // and, per matrix, that take its adapters (FUSED)
+    float* part;               // [splits + lsplits][NM][T][n] (more than one workgroup in all)
+    uint32_t* counters;        // one per (panel, tile)
     const uint16_t* base;      // NM = 1
     uint16_t* y;               // NM = 1: [T][n] bf16
     uint16_t* hhi;             // NM = 2: h = silu(first) * second as two planes [T][n]
     uint16_t* hlo;
 };
 
-// Workgroup (row panel, split of K, tile of 32 tokens): the waves and splits
-// divide K evenly and the tile's adapters in turn; sums in wave order, then
-// in split order by the last workgroup of the (panel, tile).  NM matrices
-// share x; PL planes of x add up.
-template <int FMT, int NM, int PL, int NX>
+// The lane's 16-bit pieces of `w` (two per dword) from position `left` on are cleared.
+template <typename V>
+__device__ __forceinline__ void keep_ranks(V& w, int left) {
+    constexpr int N = sizeof(V) / 4;
+#pragma unroll
+    for (int j = 0; j < N; ++j) w[j] &= left >= 2 * j + 2 ? 0xFFFFFFFFu : left == 2 * j + 1 ? 0xFFFFu : 0u;
+}
+
+// v of a tile's tokens in LDS, as two bf16 planes of rows R + 8 apart: the sum
+// of the shrink launch's parts, in 16 significant bits.  Tokens without an
+// adapter and ranks that no step reaches hold anything.
+__device__ __forceinline__ int v_row(int R) { return R + 8; }
+__device__ __forceinline__ void stage_v(uint16_t* vs, const float* v, int vparts, int T, int R, int t0, int nt, int tid) {
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    const int64_t plane = (int64_t)T * R;
+    for (int i = tid; i < nt * (R / 4); i += kThreads) {
+        const int m = i / (R / 4), k = (i - m * (R / 4)) * 4;
+        const float* src = v + (int64_t)(t0 + m) * R + k;
+        f32x4_t z = *reinterpret_cast<const f32x4_t*>(src);
+        for (int j = 1; j < vparts; ++j) {
+            const f32x4_t o = *reinterpret_cast<const f32x4_t*>(src + j * plane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] += o[e];
+        }
+        uint16_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_bf16(z[e], h[e], l[e]);
+        uint16_t* d = vs + m * v_row(R) + k;
+        *reinterpret_cast<u32x2_t*>(d) = u32x2_t{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+        *reinterpret_cast<u32x2_t*>(d + kTile * v_row(R)) = u32x2_t{l[0] | ((uint32_t)l[1] << 16), l[2] | ((uint32_t)l[3] << 16)};
+    }
+}
+
+// The B operand pairs of the steps me, me + parts, ... of 32 ranks for row
+// panel p of B [n x R].
+struct BStep {
+    u32x4_t b[2];
+};
+__device__ __forceinline__ void load_b(BStep& o, const LoraView& lo, int n, int p, const Step st, int lane) {
+    const int k = st.r0 + (lane >> 4) * 8;
+    o.b[0] = o.b[1] = u32x4_t{0u, 0u, 0u, 0u};
+    if (k < st.rank) {
+        const uint16_t* row = lo.b + ((int64_t)st.a * n + p * 32 + (lane & 15)) * lo.max_rank + k;
+        o.b[0] = *reinterpret_cast<const u32x4_t*>(row);
+        o.b[1] = *reinterpret_cast<const u32x4_t*>(row + 16 * lo.max_rank);
+    }
+}
+
+// acc += v B_a^T for one step.  `col` is the lane's columns' adapters; the
+// other tokens' products are selected away (an adapter's infinities and NaN
+// stay with its own requests), and ranks past the adapter's own are masked
+// out of B, whatever the pool holds there.
+template <int NX>
+__device__ __forceinline__ void expand(Acc (&acc)[NX], const BStep& bs, const Step st, const uint16_t* vs, int R,
+                                       const int (&col)[NX], int lane) {
+    const u32x4_t none = u32x4_t{0u, 0u, 0u, 0u};
+    const int k = st.r0 + (lane >> 4) * 8, left = st.rank - k;      // ranks of this lane's eight that exist
+    u32x4_t w[2] = {bs.b[0], bs.b[1]};
+    keep_ranks(w[0], left);
+    keep_ranks(w[1], left);
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+        if (__ballot(col[x] == st.a) == 0) continue;
+        u32x4_t h = none, l = none;
+        if (left > 0 && col[x] == st.a) {
+            const uint16_t* r = vs + (x * kCols + (lane & 15)) * v_row(R) + k;
+            h = *reinterpret_cast<const u32x4_t*>(r);
+            l = *reinterpret_cast<const u32x4_t*>(r + kTile * v_row(R));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, w[e]);
+            f32x4_t s = mma(bf, h, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+            s = mma(bf, l, s);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[x].h[e][c] = col[x] == st.a ? acc[x].h[e][c] + s[c] : acc[x].h[e][c];
+        }
+    }
+}
+
+// The adapters without a launch of their own: v B_a^T is linear in v and v in
+// the parts of K, so a wave takes v over its own units of K, 16 ranks at a
+// time, and multiplies it by B at once; the sums of the waves and workgroups
+// are those of the projection itself.  The 16 x 16 sums of x A_a^T (rows: ranks,
+// columns: tokens) are the B operand of the 16 x 16 x 16 product as they
+// stand.
+template <int PL, int NX>
+__device__ __forceinline__ void adapt(Acc (&acc)[NX], const LoraView& lo, const uint16_t* xhi, const uint16_t* xlo, int K,
+                                      int n, int p, const Step* steps, int ns, int u0, int u1, const int (&col)[NX],
+                                      const int (&t)[NX], int lane) {
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+    typedef short s16x4_t __attribute__((ext_vector_type(4)));
+    const int nu = u1 - u0, R = lo.max_rank, g = lane >> 4;
+    f32x4_t v[NX];
+#pragma unroll
+    for (int x = 0; x < NX; ++x) v[x] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int D = NX * PL == 1 ? 4 : NX == 1 ? 3 : 2;
+    XUnit au[D], xu[D][NX][PL];
+    u32x2_t b[D][2];
+    int ls = 0, lu = 0, ws = 0, wu = 0;         // (step, unit) of the next load and of the work
+    pipelined<D>(
+        ns * nu,
+        [&](int q, int) {
+            const Step st = steps[ls];
+            load_x<FT_FMT_MXFP4_B32>(au[q], lo.a + ((int64_t)st.a * R + min(st.r0 + (lane & 15), st.rank - 1)) * K, u0 + lu,
+                                     lane);
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                load_x<FT_FMT_MXFP4_B32>(xu[q][x][0], xhi + (int64_t)t[x] * K, u0 + lu, lane);
+                if constexpr (PL == 2) load_x<FT_FMT_MXFP4_B32>(xu[q][x][PL - 1], xlo + (int64_t)t[x] * K, u0 + lu, lane);
+            }
+            if (++lu == nu) {
+                const uint16_t* row = lo.b + ((int64_t)st.a * n + p * 32 + (lane & 15)) * R + st.r0 + 4 * g;
+                b[q][0] = *reinterpret_cast<const u32x2_t*>(row);
+                b[q][1] = *reinterpret_cast<const u32x2_t*>(row + 16 * R);
+                lu = 0;
+                ++ls;
+            }
+        },
+        [&](int q, int) {
+            const Step st = steps[ws];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int x = 0; x < NX; ++x)
+#pragma unroll
+                    for (int pl = 0; pl < PL; ++pl)
+                        v[x] = mma(__builtin_bit_cast(bf16x8_t, au[q].v[e]), xu[q][x][pl].v[e], v[x]);
+            if (++wu < nu) return;
+            wu = 0;
+            ++ws;
+            const int left = st.rank - st.r0 - 4 * g;      // ranks of this lane's four that exist
+            u32x2_t w[2] = {b[q][0], b[q][1]};
+            keep_ranks(w[0], left);
+            keep_ranks(w[1], left);
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                // v in 16 significant bits; zero past the adapter's rank
+                f32x4_t z, r;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[e] = e < left ? st.scale * v[x][e] : 0.0f;
+                const bf16x4_t h = __builtin_convertvector(z, bf16x4_t);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float hf = (float)h[e];
+                    r[e] = fabsf(hf) < INFINITY ? z[e] - hf : 0.0f;
+                }
+                const bf16x4_t l = __builtin_convertvector(r, bf16x4_t);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f32x4_t s = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                    const s16x4_t bw = __builtin_bit_cast(s16x4_t, w[e]);
+                    s = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(bw, __builtin_bit_cast(s16x4_t, h), s, 0, 0, 0);
+                    s = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(bw, __builtin_bit_cast(s16x4_t, l), s, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[x].h[e][i] = col[x] == st.a ? acc[x].h[e][i] + s[i] : acc[x].h[e][i];
+                }
+                v[x] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+        });
+}
+
+// Workgroups of a row panel and tile of 32 tokens: `splits` that stream the
+// panel, their waves dividing K.  The adapters, FUSED: lsplits workgroups more
+// per matrix take them, dividing K as well; they run beside the stream, not in
+// its way (listing a tile's adapters and following their addresses takes
+// several dependent loads).  Otherwise the streaming waves divide the steps of
+// 32 ranks, the first of them loaded before the stream is multiplied.  Sums in
+// wave order, then in workgroup order by the last workgroup of the (panel,
+// tile).  NM matrices share x; PL planes of x add up.
+template <int FMT, int NM, int PL, int NX, bool FUSED>
 __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a) {
     extern __shared__ __attribute__((aligned(16))) float red[];
     __shared__ uint32_t flag;
+    __shared__ Step steps[FUSED ? 1 : NM][FUSED ? kMaxFusedSteps : kMaxSteps / 2];
+    __shared__ int n_steps[NM];
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
     const int p = blockIdx.x, split = blockIdx.y, t0 = blockIdx.z * kTile;
     const int nt = min(kTile, a.T - t0), nx = nt > kCols ? 2 : 1;
-    const int units = a.K / kUnit, parts = a.splits * kWaves, me = split * kWaves + wid;
-    const int u0 = me * units / parts, u1 = (me + 1) * units / parts;
+    const int units = a.K / kUnit;
     int t[NX];
 #pragma unroll
     for (int i = 0; i < NX; ++i) t[i] = t0 + min(i * kCols + (lane & 15), nt - 1);
 
-    PanelRef pr[NM];
     Acc acc[NM][NX];
 #pragma unroll
-    for (int m = 0; m < NM; ++m) {
-        pr[m] = panel_ref<FMT>(a.codes[m], a.scales[m], a.K, p);
+    for (int m = 0; m < NM; ++m)
 #pragma unroll
         for (int i = 0; i < NX; ++i) acc[m][i] = zero_acc();
-    }
-    WUnit<FMT> w[2][NM];
-    XUnit x[2][NX][PL];
-    auto load = [&](int b, int u) {
+    const bool adapters = FUSED && split >= a.splits;
+    const int am = adapters ? (split - a.splits) % NM : 0;      // the matrix of an adapter workgroup
+    if (!adapters) {
+        const int parts = a.splits * kWaves, me = split * kWaves + wid;
+        const int u0 = me * units / parts, nu = (me + 1) * units / parts - u0;
+        PanelRef pr[NM];
 #pragma unroll
-        for (int m = 0; m < NM; ++m) load_unit<FMT>(w[b][m], pr[m], u, lane);
+        for (int m = 0; m < NM; ++m) pr[m] = panel_ref<FMT>(a.codes[m], a.scales[m], a.K, p);
+        WUnit<FMT> w[2][NM];
+        XUnit x[2][NX][PL];
+        auto load = [&](int b, int u) {
 #pragma unroll
-        for (int i = 0; i < NX; ++i)
-            if (i < nx) {
-                load_x<FMT>(x[b][i][0], a.xhi + (int64_t)t[i] * a.K, u, lane);
-                if constexpr (PL == 2) load_x<FMT>(x[b][i][PL - 1], a.xlo + (int64_t)t[i] * a.K, u, lane);
+            for (int m = 0; m < NM; ++m) load_unit<FMT>(w[b][m], pr[m], u0 + u, lane);
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                if (i < nx) {
+                    load_x<FMT>(x[b][i][0], a.xhi + (int64_t)t[i] * a.K, u0 + u, lane);
+                    if constexpr (PL == 2) load_x<FMT>(x[b][i][PL - 1], a.xlo + (int64_t)t[i] * a.K, u0 + u, lane);
+                }
+        };
+        auto work = [&](int b) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m) mma_unit<FMT, NX, PL>(acc[m], w[b][m], x[b], nx);
+        };
+        if (nu > 0) load(0, 0);
+        uint16_t* vs[NM];
+        int col[NM][NX], mine[NM];       // the columns' adapters; the wave's steps
+        BStep first[NM];
+        if constexpr (!FUSED) {
+            uint16_t* at = reinterpret_cast<uint16_t*>(red + kWaves * min(a.T, kTile) * kRedRow);
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                vs[m] = at;
+                mine[m] = 0;
+                const LoraView& lo = a.lora[m];
+                if (lo.count == 0) continue;
+                at += 2 * kTile * v_row(lo.max_rank);
+                const int id = tile_adapter<kTile>(a.adapter, t0, a.T, lo.count, lane);
+                if (wid == m) list_steps<32>(steps[m], &n_steps[m], lo, id, lane);
+                stage_v(vs[m], a.v[m], a.vparts, a.T, lo.max_rank, t0, nt, tid);
+#pragma unroll
+                for (int i = 0; i < NX; ++i) col[m][i] = __shfl(id, i * kCols + (lane & 15), 64);
             }
-    };
-    auto step = [&](int b) {
+            if (a.lora[0].count > 0 || a.lora[NM - 1].count > 0) {
+                __syncthreads();
 #pragma unroll
-        for (int m = 0; m < NM; ++m) mma_unit<FMT, NX, PL>(acc[m], w[b][m], x[b], nx);
-    };
-    if (u0 < u1) load(0, u0);
-    for (int u = u0; u < u1; u += 2) {
-        if (u + 1 < u1) load(1, u + 1);
-        step(0);
-        if (u + 1 < u1) {
-            if (u + 2 < u1) load(0, u + 2);
-            step(1);
+                for (int m = 0; m < NM; ++m)
+                    if (a.lora[m].count > 0) {
+                        const int ns = n_steps[m];
+                        mine[m] = ns > me ? (ns - me - 1) / parts + 1 : 0;
+                        if (mine[m] > 0) load_b(first[m], a.lora[m], a.n, p, steps[m][me], lane);
+                    }
+            }
         }
+        for (int u = 0; u < nu; u += 2) {
+            if (u + 1 < nu) load(1, u + 1);
+            work(0);
+            if (u + 1 < nu) {
+                if (u + 2 < nu) load(0, u + 2);
+                work(1);
+            }
+        }
+        if constexpr (!FUSED) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                if (mine[m] == 0) continue;
+                const LoraView& lo = a.lora[m];
+                constexpr int D = 4;
+                BStep bs[D];
+                expand<NX>(acc[m], first[m], steps[m][me], vs[m], lo.max_rank, col[m], lane);
+                pipelined<D>(
+                    mine[m] - 1,
+                    [&](int q, int i) { load_b(bs[q], lo, a.n, p, steps[m][me + (i + 1) * parts], lane); },
+                    [&](int q, int i) {
+                        expand<NX>(acc[m], bs[q], steps[m][me + (i + 1) * parts], vs[m], lo.max_rank, col[m], lane);
+                    });
+            }
+        }
+    } else {
+        const LoraView& lo = a.lora[am];
+        const int sub = (split - a.splits) / NM, parts = a.lsplits * kWaves, me = sub * kWaves + wid;
+        const int id = tile_adapter<kTile>(a.adapter, t0, a.T, lo.count, lane);
+        if (wid == 0) list_steps<16>(steps[0], n_steps, lo, id, lane);
+        int col[NX];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) col[i] = __shfl(id, i * kCols + (lane & 15), 64);
+        __syncthreads();
+        Acc la[NX];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) la[i] = zero_acc();
+        adapt<PL, NX>(la, lo, a.xhi, a.xlo, a.K, a.n, p, steps[0], n_steps[0], me * units / parts, (me + 1) * units / parts,
+                      col, t, lane);
+#pragma unroll
+        for (int i = 0; i < NX; ++i) acc[0][i] = la[i];
     }
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-        if (a.lora[m].count > 0) {
-            const int id = tile_adapter(a.adapter, t0, a.T, a.lora[m].count, lane);
-            int col[NX];                 // the columns' adapters
-#pragma unroll
-            for (int i = 0; i < NX; ++i) col[i] = __shfl(id, i * kCols + (lane & 15), 64);
-            each_adapter(id, [&](int i, int ad) {
-                if (i % parts != me) return;
-#pragma unroll
-                for (int q = 0; q < NX; ++q)
-                    expand(acc[m][q], a.lora[m], a.vhi[m], a.vlo[m], a.n, p, ad, col[q], t[q], lane);
-            });
-        }
 
+    // an adapter workgroup's sums are those of its matrix alone, in place 0
     constexpr int PT = kPlaces;
     float s[NM][PT];
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
-        if (m > 0) __syncthreads();
+        if (m > 0) {
+            if (adapters) break;
+            __syncthreads();
+        }
 #pragma unroll
         for (int i = 0; i < NX; ++i) put_acc(red, acc[m][i], i, wid, nt, lane);
         __syncthreads();
@@ -269,21 +520,25 @@ __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a
     }
     auto place = [&](int q) { return (int64_t)(t0 + ((tid + q * kThreads) >> 5)) * a.n + p * 32 + (tid & 31); };
     auto valid = [&](int q) { return ((tid + q * kThreads) >> 5) < nt; };
-    if (a.splits > 1) {
+    if (gridDim.y > 1) {
         const int64_t plane = (int64_t)a.T * a.n;
+        const int row = adapters ? a.splits + (split - a.splits) / NM : split;
 #pragma unroll
         for (int q = 0; q < PT; ++q)
             if (valid(q))
 #pragma unroll
-                for (int m = 0; m < NM; ++m) put_agent(a.part + (split * NM + m) * plane + place(q), s[m][q]);
-        if (!last_arrival(a.counters + blockIdx.z * gridDim.x + p, a.splits, &flag)) return;
+                for (int m = 0; m < NM; ++m)
+                    if (m == 0 || !adapters) put_agent(a.part + (row * NM + (adapters ? am : m)) * plane + place(q), s[m][q]);
+        if (!last_arrival(a.counters + blockIdx.z * gridDim.x + p, gridDim.y, &flag)) return;
+        const int rows = a.splits + a.lsplits;
 #pragma unroll
         for (int q = 0; q < PT; ++q)
             if (valid(q))
 #pragma unroll
                 for (int m = 0; m < NM; ++m) {
                     float v = 0.0f;
-                    for (int i = 0; i < a.splits; ++i) v += get_agent(a.part + (i * NM + m) * plane + place(q));
+#pragma unroll 4
+                    for (int i = 0; i < rows; ++i) v += get_agent(a.part + (i * NM + m) * plane + place(q));
                     s[m][q] = v;
                 }
     }
@@ -309,44 +564,88 @@ __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a
 
 constexpr size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Splits of K: enough workgroups for the card's 256 compute units, and no
-// more than leaves every wave a unit.
-int project_splits(int n, int K, int T) {
-    const int64_t wgs = (int64_t)(n / 32) * ((T + kTile - 1) / kTile);
-    int64_t s = 256 / wgs;
-    const int64_t most = (K / kUnit + kWaves - 1) / kWaves;
-    if (s > most) s = most;
-    return s < 1 ? 1 : (int)s;
+// How a call's product and its adapters are divided.
+struct Split {
+    int splits;        // workgroups of a (panel, tile) that stream it
+    bool adapted;      // it has adapters:
+    bool fused;        // lsplits workgroups per matrix compute v and take them, or
+    int lsplits;
+    int vparts;        // a shrink launch computes v in this many parts of K
+};
+
+// `nm` matrices [n x K]; `adapters`, `rank`: the most a tile of the call can
+// name, and the largest max_rank (0: no adapters).
+Split split_of(int nm, int n, int K, int T, int adapters, int rank) {
+    const int64_t panels = n / 32, tiles = (T + kTile - 1) / kTile;
+    const int units = K / kUnit, most = (units + kWaves - 1) / kWaves;
+    Split s;
+    // enough workgroups for the card's 256 compute units, no more than leaves every wave a unit
+    int64_t w = 256 / (panels * tiles);
+    w = w > most ? most : w;
+    s.splits = w < 1 ? 1 : (int)w;
+    s.lsplits = 0;
+    s.adapted = s.fused = false;
+    s.vparts = 1;
+    if (adapters <= 0 || rank <= 0) return s;
+    s.adapted = true;
+    if (adapters > T) adapters = T;
+    if (adapters > kTile) adapters = kTile;
+    // Without a launch for v every row panel reads the adapters' A once more (from
+    // L2): taken while that is at most 24 MB in all, some 2 us of it, and while the
+    // adapters' workgroups fit the card beside the stream's.
+    const int64_t steps = (int64_t)adapters * (rank / 16), per = 256 / (panels * tiles);
+    s.fused = T <= kTile && steps <= kMaxFusedSteps && panels * steps * 32 * K <= (24ll << 20) && per >= 1 + nm;
+    if (s.fused) {
+        if (s.splits > per - nm) s.splits = (int)(per - nm);
+        int64_t l = (per - s.splits) / nm;
+        l = l > most ? most : l;
+        s.lsplits = l < 1 ? 1 : l > 4 ? 4 : (int)l;
+    } else {
+        const int64_t spans = (T + kSpan - 1) / kSpan;
+        int64_t parts = 256 / (spans * adapters * (rank / 16));
+        parts = parts > most ? most : parts;
+        s.vparts = parts < 1 ? 1 : parts > kMaxParts ? kMaxParts : (int)parts;
+    }
+    return s;
 }
 
-size_t part_bytes(int nm, int n, int K, int T) {
-    const int s = project_splits(n, K, T);
-    return s > 1 ? align256((size_t)s * nm * T * n * sizeof(float)) : 0;
+size_t part_bytes(int nm, int n, int T, const Split& s) {
+    const int rows = s.splits + s.lsplits;
+    return rows > 1 ? align256((size_t)rows * nm * T * n * sizeof(float)) : 0;
 }
 
-size_t lds_bytes(int T) { return (size_t)kWaves * (T < kTile ? T : kTile) * kRedRow * sizeof(float); }
+// the waves' sums, and v of the matrices' adapters where the product expands them
+template <bool FUSED>
+size_t lds_bytes(const ProjectArgs& a) {
+    size_t n = (size_t)kWaves * (a.T < kTile ? a.T : kTile) * kRedRow * sizeof(float);
+    for (const LoraView& l : a.lora)
+        if (!FUSED && l.count > 0) n += (size_t)2 * kTile * (l.max_rank + 8) * sizeof(uint16_t);
+    return n;
+}
 
 hipError_t launch_shrink(const ShrinkArgs& s, int projections, hipStream_t st) {
-    const int tiles = (s.T + kTile - 1) / kTile;
+    const int spans = (s.T + kSpan - 1) / kSpan;
     int most = 0;
     for (int i = 0; i < projections; ++i) most = s.lora[i].count > most ? s.lora[i].count : most;
-    // a workgroup per adapter of a tile while tiles are few; prompts have few adapters per tile
+    // a workgroup per adapter of a span while spans are few; prompts have few adapters per span
     int gy = most < kTile ? most : kTile;
     if (gy > s.T) gy = s.T;
-    if (tiles >= 32 && gy > 4) gy = 4;
-    const dim3 grid(tiles, gy, projections * s.panels);
-    if (s.xlo) hipLaunchKernelGGL(lora_shrink_kernel<2>, grid, dim3(kThreads), lds_bytes(s.T), st, s);
-    else hipLaunchKernelGGL(lora_shrink_kernel<1>, grid, dim3(kThreads), lds_bytes(s.T), st, s);
+    if (spans >= 16 && gy > 2) gy = 2;
+    const dim3 grid(spans, gy, projections * s.panels * s.parts);
+    const int cols = s.xlo ? 2 * kCols : 4 * kCols;
+    const size_t lds = (size_t)kWaves * (s.T < cols ? s.T : cols) * 20 * sizeof(float);
+    if (s.xlo) hipLaunchKernelGGL((lora_shrink_kernel<2, 2>), grid, dim3(kThreads), lds, st, s);
+    else hipLaunchKernelGGL((lora_shrink_kernel<1, 4>), grid, dim3(kThreads), lds, st, s);
     return hipGetLastError();
 }
 
-template <int FMT, int NM, int PL>
+template <int FMT, int NM, int PL, bool FUSED>
 void launch_project_nx(const ProjectArgs& a, hipStream_t st) {
-    const dim3 grid(a.n / 32, a.splits, (a.T + kTile - 1) / kTile);
+    const dim3 grid(a.n / 32, a.splits + a.lsplits * NM, (a.T + kTile - 1) / kTile);
     if (a.T <= kCols)
-        hipLaunchKernelGGL((lora_project_kernel<FMT, NM, PL, 1>), grid, dim3(kThreads), lds_bytes(a.T), st, a);
+        hipLaunchKernelGGL((lora_project_kernel<FMT, NM, PL, 1, FUSED>), grid, dim3(kThreads), lds_bytes<FUSED>(a), st, a);
     else
-        hipLaunchKernelGGL((lora_project_kernel<FMT, NM, PL, 2>), grid, dim3(kThreads), lds_bytes(a.T), st, a);
+        hipLaunchKernelGGL((lora_project_kernel<FMT, NM, PL, 2, FUSED>), grid, dim3(kThreads), lds_bytes<FUSED>(a), st, a);
 }
 
 // Prompts: from this many tokens on the 128-row GEMM tiles are faster than
@@ -358,32 +657,49 @@ bool gemm_fits(int T, int K, const void* y, const void* base) {
            (reinterpret_cast<uintptr_t>(base) & 15) == 0;
 }
 
-template <int NM, int PL>
-hipError_t launch_project(int fmt, const ProjectArgs& a, hipStream_t st) {
+template <int NM, int PL, bool FUSED>
+hipError_t launch_project_as(int fmt, const ProjectArgs& a, hipStream_t st) {
     switch (fmt) {
-        case FT_FMT_BF16: launch_project_nx<FT_FMT_BF16, NM, PL>(a, st); break;
-        case FT_FMT_FP8_B128: launch_project_nx<FT_FMT_FP8_B128, NM, PL>(a, st); break;
-        case FT_FMT_MXFP4_B32: launch_project_nx<FT_FMT_MXFP4_B32, NM, PL>(a, st); break;
+        case FT_FMT_BF16: launch_project_nx<FT_FMT_BF16, NM, PL, FUSED>(a, st); break;
+        case FT_FMT_FP8_B128: launch_project_nx<FT_FMT_FP8_B128, NM, PL, FUSED>(a, st); break;
+        case FT_FMT_MXFP4_B32: launch_project_nx<FT_FMT_MXFP4_B32, NM, PL, FUSED>(a, st); break;
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
 }
+template <int NM, int PL>
+hipError_t launch_project(int fmt, const ProjectArgs& a, bool fuse, hipStream_t st) {
+    return fuse ? launch_project_as<NM, PL, true>(fmt, a, st) : launch_project_as<NM, PL, false>(fmt, a, st);
+}
 
+int pool_adapters(const LoraView* l) { return l && l->count > 0 ? l->count : 0; }
+int pool_rank(const LoraView* l) { return l && l->count > 0 ? l->max_rank : 0; }
+
+// v of one projection: bf16 planes [T][R] for the GEMM, else fp32 parts
+size_t v_bytes(int T, int rank, int parts) {
+    const size_t two = 2 * align256((size_t)T * rank * 2), f32 = align256((size_t)parts * T * rank * sizeof(float));
+    return two > f32 ? two : f32;
+}
+
+// Workspace of a call: v of its projections, h, the partial sums.  The sizes
+// are those of the most adapters a tile can name, so they hold for any pools
+// of up to max_rank.
 struct ExpertBuffers {
     size_t v[3], h, part, total;
 };
-// v of a projection: two planes [T][R]; h: two planes [T][f]
 ExpertBuffers expert_buffers(const ft_shape& s, int max_rank, int T) {
     ExpertBuffers b;
     size_t o = 0;
     for (int i = 0; i < 3; ++i) {
         b.v[i] = o;
-        o += 2 * align256((size_t)T * max_rank * 2);
+        o += v_bytes(T, max_rank, kMaxParts);
     }
     b.h = o;
     o += 2 * align256((size_t)T * s.d_ff * 2);
     b.part = o;
-    const size_t p1 = part_bytes(2, s.d_ff, s.d_model, T), p2 = part_bytes(1, s.d_model, s.d_ff, T);
+    Split gu = split_of(2, s.d_ff, s.d_model, T, 0, 0), dn = split_of(1, s.d_model, s.d_ff, T, 0, 0);
+    gu.lsplits = dn.lsplits = max_rank > 0 ? 4 : 0;
+    const size_t p1 = part_bytes(2, s.d_ff, T, gu), p2 = part_bytes(1, s.d_model, T, dn);
     b.total = o + (p1 > p2 ? p1 : p2);
     return b;
 }
@@ -391,7 +707,9 @@ ExpertBuffers expert_buffers(const ft_shape& s, int max_rank, int T) {
 }  // namespace
 
 size_t lora_project_call_bytes(int n, int K, int max_rank, int T) {
-    return part_bytes(1, n, K, T) + 2 * align256((size_t)T * max_rank * 2);
+    Split s = split_of(1, n, K, T, 0, 0);
+    s.lsplits = max_rank > 0 ? 4 : 0;
+    return part_bytes(1, n, T, s) + v_bytes(T, max_rank, kMaxParts);
 }
 size_t lora_expert_call_bytes(const ft_shape& s, int max_rank, int T) { return expert_buffers(s, max_rank, T).total; }
 
@@ -418,42 +736,73 @@ size_t lora_expert_workspace(const ft_shape& s, int max_rank, int max_tokens) {
     return most;
 }
 
+namespace {
+
+// The shrink launch of up to two projections that read the same x, into
+// `planes` (two bf16 planes, for the GEMM) or fp32 parts at v[i].
+hipError_t shrink(const LoraView* const* pools, uint8_t* const* v, int n, const int32_t* adapter, const uint16_t* xhi,
+                  const uint16_t* xlo, int T, int K, bool planes, int parts, hipStream_t st) {
+    ShrinkArgs s = {};
+    s.adapter = adapter;
+    s.xhi = xhi;
+    s.xlo = xlo;
+    s.T = T;
+    s.K = K;
+    s.parts = parts;
+    int m = 0;
+    for (int i = 0; i < n; ++i) {
+        if (pool_adapters(pools[i]) == 0) continue;
+        s.lora[m] = *pools[i];
+        if (planes) {
+            s.vhi[m] = reinterpret_cast<uint16_t*>(v[i]);
+            s.vlo[m] = reinterpret_cast<uint16_t*>(v[i] + align256((size_t)T * pools[i]->max_rank * 2));
+        } else {
+            s.vpart[m] = reinterpret_cast<float*>(v[i]);
+        }
+        s.panels = pools[i]->max_rank / 16 > s.panels ? pools[i]->max_rank / 16 : s.panels;
+        ++m;
+    }
+    return m > 0 ? launch_shrink(s, m, st) : hipSuccess;
+}
+
+// The pools, planes and adapters of a GEMM's NM matrices
+void gemm_pools(LoraGemmArgs& g, const LoraView* const* pools, uint8_t* const* v, int n) {
+    for (int i = 0; i < n; ++i) {
+        g.lora[i] = pool_adapters(pools[i]) > 0 ? *pools[i] : LoraView();
+        g.vhi[i] = reinterpret_cast<const uint16_t*>(v[i]);
+        g.vlo[i] = reinterpret_cast<const uint16_t*>(v[i] + align256((size_t)g.T * g.lora[i].max_rank * 2));
+    }
+}
+
+// NM matrices [n x K] on T tokens with their pools: the shrink launch where it
+// is needed, then the product.  `a` holds the matrices, x, outputs, part.
+template <int NM, int PL>
+hipError_t product(int fmt, ProjectArgs& a, const LoraView* const* pools, uint8_t* const* v, hipStream_t st) {
+    int adapters = 0, rank = 0;
+    for (int i = 0; i < NM; ++i) {
+        if (pool_adapters(pools[i]) > adapters) adapters = pool_adapters(pools[i]);
+        if (pool_rank(pools[i]) > rank) rank = pool_rank(pools[i]);
+        if (pool_adapters(pools[i]) > 0) a.lora[i] = *pools[i];
+        a.v[i] = reinterpret_cast<const float*>(v[i]);
+    }
+    const Split s = split_of(NM, a.n, a.K, a.T, adapters, rank);
+    a.splits = s.splits;
+    a.lsplits = s.lsplits;
+    a.vparts = s.vparts;
+    if (s.adapted && !s.fused) {
+        const hipError_t e = shrink(pools, v, NM, a.adapter, a.xhi, a.xlo, a.T, a.K, false, s.vparts, st);
+        if (e != hipSuccess) return e;
+    }
+    return launch_project<NM, PL>(fmt, a, s.fused, st);
+}
+
+}  // namespace
+
 hipError_t launch_lora_project(const MatrixView& m, const LoraView* lora, const int32_t* adapter, const uint16_t* x,
                                int T, const uint16_t* base, uint16_t* y, ft_workspace* ws, hipStream_t st) {
     uint8_t* mem = ws->mem + kCounterBytes;
-    ProjectArgs a = {};
-    a.codes[0] = m.codes;
-    a.scales[0] = m.scales;
-    a.lora[0] = lora ? *lora : LoraView();
-    a.lora[1] = LoraView();
-    a.adapter = adapter;
-    a.xhi = x;
-    a.T = T;
-    a.n = m.n;
-    a.K = m.K;
-    a.splits = project_splits(m.n, m.K, T);
-    a.counters = reinterpret_cast<uint32_t*>(ws->mem);
-    a.base = base;
-    a.y = y;
-    size_t o = 0;
-    if (a.lora[0].count > 0) {
-        const size_t plane = align256((size_t)T * lora->max_rank * 2);
-        ShrinkArgs s = {};
-        s.lora[0] = *lora;
-        s.lora[1] = LoraView();
-        s.vhi[0] = reinterpret_cast<uint16_t*>(mem);
-        s.vlo[0] = reinterpret_cast<uint16_t*>(mem + plane);
-        s.adapter = adapter;
-        s.xhi = x;
-        s.T = T;
-        s.K = m.K;
-        s.panels = lora->max_rank / 16;
-        hipError_t e = launch_shrink(s, 1, st);
-        if (e != hipSuccess) return e;
-        a.vhi[0] = s.vhi[0];
-        a.vlo[0] = s.vlo[0];
-        o = 2 * plane;
-    }
+    const LoraView* pools[1] = {lora};
+    uint8_t* v[1] = {mem};
     if (gemm_fits(T, m.K, y, base)) {
         LoraGemmArgs g = {};
         g.Hin = x;
@@ -464,139 +813,93 @@ hipError_t launch_lora_project(const MatrixView& m, const LoraView* lora, const 
         g.h_bytes = (uint32_t)((int64_t)T * m.K * 2);
         g.codes[0] = m.codes;
         g.scales[0] = m.scales;
-        g.lora[0] = a.lora[0];
-        g.vhi[0] = a.vhi[0];
-        g.vlo[0] = a.vlo[0];
         g.adapter = adapter;
         g.base = base;
-        return launch_lora_gemm(m.fmt, false, g, st);
+        gemm_pools(g, pools, v, 1);
+        const hipError_t e = shrink(pools, v, 1, adapter, x, nullptr, T, m.K, true, 1, st);
+        return e != hipSuccess ? e : launch_lora_gemm(m.fmt, false, g, st);
     }
-    a.part = reinterpret_cast<float*>(mem + o);
-    return launch_project<1, 1>(m.fmt, a, st);
+    ProjectArgs a = {};
+    a.codes[0] = m.codes;
+    a.scales[0] = m.scales;
+    a.adapter = adapter;
+    a.xhi = x;
+    a.T = T;
+    a.n = m.n;
+    a.K = m.K;
+    a.part = reinterpret_cast<float*>(mem + v_bytes(T, pool_rank(lora), kMaxParts));
+    a.counters = reinterpret_cast<uint32_t*>(ws->mem);
+    a.base = base;
+    a.y = y;
+    return product<1, 1>(m.fmt, a, pools, v, st);
 }
 
 hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const uint8_t* rec, const LoraView* gate,
                               const LoraView* up, const LoraView* down, const int32_t* adapter, const uint16_t* x,
                               int T, const uint16_t* base, uint16_t* y, ft_workspace* ws, hipStream_t st) {
     uint8_t* mem = ws->mem + kCounterBytes;
+    const LoraView* pools[3] = {gate, up, down};
     int R = 0;
-    for (const LoraView* l : {gate, up, down})
-        if (l && l->max_rank > R) R = l->max_rank;
+    for (const LoraView* l : pools) R = pool_rank(l) > R ? pool_rank(l) : R;
     const ExpertBuffers b = expert_buffers(sh, R, T);
-    auto v_hi = [&](int i) { return reinterpret_cast<uint16_t*>(mem + b.v[i]); };
-    auto v_lo = [&](int i) { return reinterpret_cast<uint16_t*>(mem + b.v[i] + align256((size_t)T * R * 2)); };
+    uint8_t* v[3] = {mem + b.v[0], mem + b.v[1], mem + b.v[2]};
     uint16_t* hhi = reinterpret_cast<uint16_t*>(mem + b.h);
     uint16_t* hlo = reinterpret_cast<uint16_t*>(mem + b.h + align256((size_t)T * sh.d_ff * 2));
-
-    // one launch for the adapters of gate and up, where either has any
-    ShrinkArgs s = {};
-    int n = 0;
-    s.adapter = adapter;
-    s.xhi = x;
-    s.T = T;
-    s.K = sh.d_model;
-    s.lora[0] = s.lora[1] = LoraView();
-    const LoraView* gu[2] = {gate, up};
-    for (int i = 0; i < 2; ++i)
-        if (gu[i] && gu[i]->count > 0) {
-            s.lora[n] = *gu[i];
-            s.vhi[n] = v_hi(i);
-            s.vlo[n] = v_lo(i);
-            const int p = gu[i]->max_rank / 16;
-            s.panels = p > s.panels ? p : s.panels;
-            ++n;
-        }
     hipError_t e;
-    if (n > 0 && (e = launch_shrink(s, n, st)) != hipSuccess) return e;
-
-    const bool gemm = gemm_fits(T, sh.d_model > sh.d_ff ? sh.d_model : sh.d_ff, y, base);
-    LoraGemmArgs gm = {};
-    if (gemm) {
-        gm.x = x;
-        gm.Hin = gm.Hout = hhi;
-        gm.Y = y;
-        gm.T = T;
-        gm.d = sh.d_model;
-        gm.f = sh.d_ff;
-        gm.x_bytes = (uint32_t)((int64_t)T * sh.d_model * 2);
-        gm.h_bytes = (uint32_t)((int64_t)T * sh.d_ff * 2);
-        gm.codes[0] = rec + rl.off_gate;
-        gm.codes[1] = rec + rl.off_up;
-        gm.scales[0] = rec + rl.off_sg;
-        gm.scales[1] = rec + rl.off_su;
-        for (int i = 0; i < 2; ++i) {
-            gm.lora[i] = gu[i] ? *gu[i] : LoraView();
-            gm.vhi[i] = v_hi(i);
-            gm.vlo[i] = v_lo(i);
-        }
-        gm.adapter = adapter;
-        if ((e = launch_lora_gemm(sh.fmt, true, gm, st)) != hipSuccess) return e;
+    if (gemm_fits(T, sh.d_model > sh.d_ff ? sh.d_model : sh.d_ff, y, base)) {
+        LoraGemmArgs g = {};
+        g.x = x;
+        g.Hin = g.Hout = hhi;
+        g.Y = y;
+        g.T = T;
+        g.d = sh.d_model;
+        g.f = sh.d_ff;
+        g.x_bytes = (uint32_t)((int64_t)T * sh.d_model * 2);
+        g.h_bytes = (uint32_t)((int64_t)T * sh.d_ff * 2);
+        g.codes[0] = rec + rl.off_gate;
+        g.codes[1] = rec + rl.off_up;
+        g.scales[0] = rec + rl.off_sg;
+        g.scales[1] = rec + rl.off_su;
+        g.adapter = adapter;
+        gemm_pools(g, pools, v, 2);
+        if ((e = shrink(pools, v, 2, adapter, x, nullptr, T, sh.d_model, true, 1, st)) != hipSuccess) return e;
+        if ((e = launch_lora_gemm(sh.fmt, true, g, st)) != hipSuccess) return e;
+        g.codes[0] = rec + rl.off_down;
+        g.scales[0] = rec + rl.off_sd;
+        g.base = base;
+        gemm_pools(g, pools + 2, v + 2, 1);
+        if ((e = shrink(pools + 2, v + 2, 1, adapter, hhi, nullptr, T, sh.d_ff, true, 1, st)) != hipSuccess) return e;
+        return launch_lora_gemm(sh.fmt, false, g, st);
     }
-
     ProjectArgs a = {};
     a.codes[0] = rec + rl.off_gate;
     a.codes[1] = rec + rl.off_up;
     a.scales[0] = rec + rl.off_sg;
     a.scales[1] = rec + rl.off_su;
-    for (int i = 0; i < 2; ++i) {
-        a.lora[i] = gu[i] ? *gu[i] : LoraView();
-        a.vhi[i] = v_hi(i);
-        a.vlo[i] = v_lo(i);
-    }
     a.adapter = adapter;
     a.xhi = x;
     a.T = T;
     a.n = sh.d_ff;
     a.K = sh.d_model;
-    a.splits = project_splits(a.n, a.K, T);
     a.part = reinterpret_cast<float*>(mem + b.part);
     a.counters = reinterpret_cast<uint32_t*>(ws->mem);
     a.hhi = hhi;
     a.hlo = hlo;
-    if (!gemm && (e = launch_project<2, 1>(sh.fmt, a, st)) != hipSuccess) return e;
-
-    if (down && down->count > 0) {
-        ShrinkArgs d = {};
-        d.lora[0] = *down;
-        d.lora[1] = LoraView();
-        d.vhi[0] = v_hi(2);
-        d.vlo[0] = v_lo(2);
-        d.adapter = adapter;
-        d.xhi = hhi;
-        d.xlo = gemm ? nullptr : hlo;
-        d.T = T;
-        d.K = sh.d_ff;
-        d.panels = down->max_rank / 16;
-        if ((e = launch_shrink(d, 1, st)) != hipSuccess) return e;
-    }
-    if (gemm) {
-        gm.codes[0] = rec + rl.off_down;
-        gm.scales[0] = rec + rl.off_sd;
-        gm.lora[0] = down ? *down : LoraView();
-        gm.vhi[0] = v_hi(2);
-        gm.vlo[0] = v_lo(2);
-        gm.base = base;
-        return launch_lora_gemm(sh.fmt, false, gm, st);
-    }
+    if ((e = product<2, 1>(sh.fmt, a, pools, v, st)) != hipSuccess) return e;
     ProjectArgs c = {};
     c.codes[0] = rec + rl.off_down;
     c.scales[0] = rec + rl.off_sd;
-    c.lora[0] = down ? *down : LoraView();
-    c.lora[1] = LoraView();
-    c.vhi[0] = v_hi(2);
-    c.vlo[0] = v_lo(2);
     c.adapter = adapter;
     c.xhi = hhi;
     c.xlo = hlo;
     c.T = T;
     c.n = sh.d_model;
     c.K = sh.d_ff;
-    c.splits = project_splits(c.n, c.K, T);
     c.part = a.part;
     c.counters = a.counters;
     c.base = base;
     c.y = y;
-    return launch_project<1, 2>(sh.fmt, c, st);
+    return product<1, 2>(sh.fmt, c, pools + 2, v + 2, st);
 }
 
 }  // namespace ftmoe
