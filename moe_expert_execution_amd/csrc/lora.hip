@@ -18,21 +18,6 @@ using namespace rs;
 
 // ---- the adapters of a tile -----------------------------------------------------------
 
-// DEPTH steps in flight: load(b, i) fills buffer b for step i, work(b, i) uses it.
-template <int DEPTH, typename L, typename W>
-__device__ __forceinline__ void pipelined(int n, L&& load, W&& work) {
-#pragma unroll
-    for (int b = 0; b < DEPTH; ++b)
-        if (b < n) load(b, b);
-    for (int i = 0; i < n; i += DEPTH)
-#pragma unroll
-        for (int b = 0; b < DEPTH; ++b)
-            if (i + b < n) {
-                work(b, i + b);
-                if (i + b + DEPTH < n) load(b, i + b + DEPTH);
-            }
-}
-
 // The adapter of token t0 + lane % N; ids outside the pool name none (-1).
 template <int N>
 __device__ __forceinline__ int tile_adapter(const int32_t* adapter, int t0, int T, int count, int lane) {

@@ -19,15 +19,22 @@ using namespace rs;
 
 // ---- routing ----------------------------------------------------------------------
 
-constexpr int kRouteTokens = 16;          // tokens of one matrix-core tile
-constexpr int kRouteExperts = 64;         // experts of one workgroup
+constexpr int kRouteTokens = 4;           // tokens of one routing workgroup
+constexpr int kRouteExperts = 64;         // experts of one routing workgroup
 
-// Rows of the router one wave takes.  A slice (a workgroup's 8 waves) ends in
-// one fp64 partial logit per token and expert, which the group's last
-// workgroup reads back, so longer slices are taken as tokens grow.
-inline int route_rows(int T) { return T <= 2 ? 32 : T <= 8 ? 64 : 128; }
-inline int route_slices(int d, int T) {
-    const int per = kWaves * route_rows(T);
+// Rows of the router one wave takes: short slices while the workgroups fit the
+// card twice over, so that the loads are all in flight at once.  Groups of 4
+// tokens, not the 16 of a matrix-core tile: a group's last workgroup sums and
+// selects for all its tokens, and at 16 tokens that took longer than the
+// product (24 us against 11 at 16 tokens, d = 2,048 and 128 experts).
+inline int route_rows(int d, int E, int T) {
+    const int64_t groups = (int64_t)((E + kRouteExperts - 1) / kRouteExperts) * ((T + kRouteTokens - 1) / kRouteTokens);
+    int rows = 32;
+    while (rows < 128 && groups * (d / (kWaves * rows)) > 512) rows *= 2;
+    return rows;
+}
+inline int route_slices(int d, int E, int T) {
+    const int per = kWaves * route_rows(d, E, T);
     return (d + per - 1) / per;
 }
 
@@ -104,12 +111,12 @@ __device__ __forceinline__ void select_experts(const double* z, int E, int k, in
     }
 }
 
-// Workgroup (slice of d, 64 experts, 16 tokens): partial logits on the fp64
+// Workgroup (slice of d, 64 experts, 4 tokens): partial logits on the fp64
 // matrix cores (bf16 products are exact in fp64, sums are fp64).  Per 32 rows
 // lane group g = l / 16 takes rows 8 g .. 8 g + 7, so MFMA step s contracts
 // rows 8 g + s; column c = l % 16 of tile n is expert 4 c + n, so one 8-byte
 // load gives a lane its four tiles' weights of a row, and one 16-byte load its
-// token's 8 activations.  The waves' sums are added in order, the tile's
+// token's 8 activations.  The waves' sums are added in order, the group's
 // last workgroup adds the slices in order and selects, one wave per token.
 __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
     extern __shared__ __attribute__((aligned(16))) double zred[];
@@ -127,37 +134,44 @@ __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
 #pragma unroll
     for (int n = 0; n < 4; ++n) acc[n] = f64x4{0.0, 0.0, 0.0, 0.0};
     const uint16_t* xrow = a.x + (int64_t)(t0 + min(c, nt - 1)) * a.d + 8 * g;
-    for (int kk = k0; kk < k1; kk += 32) {
-        const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(xrow + kk);
-        u32x2_t wv[8];
+    constexpr int D = 2;
+    u32x4_t xv[D];
+    u32x2_t wv[D][8];
+    auto load = [&](int b, int i) {
+        const int kk = k0 + 32 * i;
+        xv[b] = *reinterpret_cast<const u32x4_t*>(xrow + kk);
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
             const uint16_t* p = a.wr + (int64_t)(kk + 8 * g + s) * a.E + e4;
-            wv[s] = u32x2_t{0u, 0u};
+            wv[b][s] = u32x2_t{0u, 0u};
             if (vec) {
-                if (e4 < a.E) wv[s] = *reinterpret_cast<const u32x2_t*>(p);
+                if (e4 < a.E) wv[b][s] = *reinterpret_cast<const u32x2_t*>(p);
             } else {
                 uint32_t h[4];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) h[n] = e4 + n < a.E ? p[n] : 0u;
-                wv[s] = u32x2_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+                wv[b][s] = u32x2_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
             }
         }
+    };
+    auto work = [&](int b, int) {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-            const uint32_t xw = xv[s >> 1];
+            const uint32_t xw = xv[b][s >> 1];
             const double av = (double)((s & 1) ? bf16hi(xw) : bf16lo(xw));
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const uint32_t u = wv[s][n >> 1];
+                const uint32_t u = wv[b][s][n >> 1];
                 const double bv = (double)((n & 1) ? bf16hi(u) : bf16lo(u));
                 acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64(av, bv, acc[n], 0, 0, 0);
             }
         }
-    }
+    };
+    pipelined<D>(max(k1 - k0, 0) / 32, load, work);
     // accumulator element v of lane l: token 4 v + l / 16, expert 4 (l % 16) + n
+    static_assert(kRouteTokens <= 4, "tokens 0..3 are element 0 of their lanes");
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
+    for (int v = 0; v < 1; ++v) {
         const int t = 4 * v + g;
         if (t < nt)
 #pragma unroll
@@ -527,15 +541,28 @@ int down_panels(const ft_shape& s, int T) {
     return s.fmt == FT_FMT_MXFP4_B32 && (int64_t)T * s.top_k >= 32 ? 2 : 1;
 }
 
-// Splits of the tiles' axis: enough workgroups for the card, and no more than
-// leaves each wave a unit when every route has an expert of its own.
+// Splits of the tiles' axis.  A compute unit holds one workgroup, so the launch
+// takes ceil(workgroups / 256) rounds of a split's share each; more splits even
+// that out (224 panels of d = 7,168 in pairs: 3 splits take 2 rounds of a third
+// each, 9 take 4 of a ninth), and each costs its partial sums, written and read
+// once.  The times are estimates at 25 GB/s per workgroup and 4 TB/s; no more
+// splits than leave each wave a unit when every route has an expert of its own.
 int down_splits(const ft_shape& s, int T) {
-    const int wgs = s.d_model / 32 / down_panels(s, T);
-    const int64_t units = (int64_t)(T * s.top_k < s.experts ? T * s.top_k : s.experts) * (s.d_ff / kUnit);
-    int64_t n = (256 + wgs - 1) / wgs;
-    const int64_t most = (units + kWaves - 1) / kWaves;
-    if (n > most) n = most;
-    return n < 1 ? 1 : (int)n;
+    const int np = down_panels(s, T), wgs = s.d_model / 32 / np;
+    const int64_t R = (int64_t)T * s.top_k, tiles = R < s.experts ? R : s.experts;
+    const int64_t units = tiles * (s.d_ff / kUnit);
+    const double unit_bytes = s.fmt == FT_FMT_BF16 ? 8192 : s.fmt == FT_FMT_FP8_B128 ? 4096 : 2176;
+    const double stream = units * np * unit_bytes / 25e3, join = (double)T * s.d_model * 8 / 4e6;     // us
+    int best = 1;
+    double least = 1e30;
+    for (int n = 1; n <= 16 && (n == 1 || (int64_t)(n - 1) * kWaves < units); ++n) {
+        const double t = (double)((wgs * n + 255) / 256) * stream / n + (n > 1 ? 2.0 + n * join : 0.0);
+        if (t < least) {
+            least = t;
+            best = n;
+        }
+    }
+    return best;
 }
 
 constexpr size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -547,7 +574,7 @@ LayerBuffers layer_buffers(const ft_shape& s, int T) {
     LayerBuffers b;
     const size_t R = (size_t)T * s.top_k;
     b.logits = 0;
-    b.hhi = align256((size_t)route_slices(s.d_model, T) * T * s.experts * sizeof(double));
+    b.hhi = align256((size_t)route_slices(s.d_model, s.experts, T) * T * s.experts * sizeof(double));
     b.hlo = b.hhi + align256(R * s.d_ff * 2);
     b.part = b.hlo + align256(R * s.d_ff * 2);
     b.total = b.part + align256((size_t)down_splits(s, T) * T * s.d_model * sizeof(float));
@@ -618,8 +645,8 @@ hipError_t launch_layer(const ft_shape& s, const LayerArgs& la, ft_workspace* ws
     r.d = s.d_model;
     r.E = s.experts;
     r.k = s.top_k;
-    r.rows = route_rows(la.T);
-    r.slices = route_slices(s.d_model, la.T);
+    r.rows = route_rows(s.d_model, s.experts, la.T);
+    r.slices = route_slices(s.d_model, s.experts, la.T);
     r.part = reinterpret_cast<double*>(m + b.logits);
     r.counters = counters;
     r.ids = la.ids;

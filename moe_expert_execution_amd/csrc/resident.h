@@ -219,6 +219,21 @@ __device__ __forceinline__ void sum_waves(float (&out)[kPlaces], const float* re
     }
 }
 
+// DEPTH steps in flight: load(b, i) fills buffer b for step i, work(b, i) uses it.
+template <int DEPTH, typename L, typename W>
+__device__ __forceinline__ void pipelined(int n, L&& load, W&& work) {
+#pragma unroll
+    for (int b = 0; b < DEPTH; ++b)
+        if (b < n) load(b, b);
+    for (int i = 0; i < n; i += DEPTH)
+#pragma unroll
+        for (int b = 0; b < DEPTH; ++b)
+            if (i + b < n) {
+                work(b, i + b);
+                if (i + b + DEPTH < n) load(b, i + b + DEPTH);
+            }
+}
+
 // ---- hand-over between workgroups of one launch --------------------------------
 // Partial sums that another workgroup of the same launch reads go through
 // agent-scope stores and loads: those bypass the XCD's L2, which other XCDs do
