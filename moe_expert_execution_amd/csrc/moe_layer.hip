@@ -17,16 +17,24 @@ namespace {
 
 using namespace rs;
 
+// The hand-over counters of the experts' launch (below); the routing launch
+// before it clears them.
+constexpr int kShards = 8, kShardStep = 32;
+constexpr int kDrawn = 0, kDone = kShards * kShardStep;              // words of `hand`
+constexpr int kHandWords = 2 * kShards * kShardStep;
+constexpr uint32_t kMaxPolls = 1u << 22;      // seconds: only a workspace used by two calls at once gets there
+constexpr int kHandAt = 4096;                 // their place among the workspace's counters (after one per row panel)
+
 // ---- routing ----------------------------------------------------------------------
 
-constexpr int kRouteTokens = 4;           // tokens of one routing workgroup
+constexpr int kRouteTokens = 8;           // tokens of one routing workgroup
 constexpr int kRouteExperts = 64;         // experts of one routing workgroup
 
 // Rows of the router one wave takes: short slices while the workgroups fit the
-// card twice over, so that the loads are all in flight at once.  Groups of 4
+// card twice over, so that the loads are all in flight at once.  Groups of 8
 // tokens, not the 16 of a matrix-core tile: a group's last workgroup sums and
-// selects for all its tokens, and at 16 tokens that took longer than the
-// product (24 us against 11 at 16 tokens, d = 2,048 and 128 experts).
+// selects for all its tokens, one a wave (with 16 that took longer than the
+// product); groups of 4 double the product, which bounds 64 tokens.
 inline int route_rows(int d, int E, int T) {
     const int64_t groups = (int64_t)((E + kRouteExperts - 1) / kRouteExperts) * ((T + kRouteTokens - 1) / kRouteTokens);
     int rows = 32;
@@ -43,75 +51,91 @@ struct RouteArgs {
     const uint16_t* wr;
     int T, d, E, k, rows, slices;
     double* part;          // [slices][T][E]
-    uint32_t* counters;    // one per token tile
+    uint32_t* counters;    // one per token group
+    uint32_t* hand;        // the next launch's hand-over counters
     int32_t* ids;
     float* w;
 };
 
-// The largest of the 64 lanes' values, in every lane.
+// The largest of the 64 lanes' values.
 template <int CTRL>
-__device__ __forceinline__ uint64_t dpp_max(uint64_t v) {
-    const uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
-    const uint32_t l2 = (uint32_t)__builtin_amdgcn_update_dpp((int)lo, (int)lo, CTRL, 0xF, 0xF, false);
-    const uint32_t h2 = (uint32_t)__builtin_amdgcn_update_dpp((int)hi, (int)hi, CTRL, 0xF, 0xF, false);
-    const uint64_t o = ((uint64_t)h2 << 32) | l2;
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
     return o > v ? o : v;
 }
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     v = dpp_max<0x111>(v);        // row_shr 1, 2, 4, 8: the largest of each 16 lanes in its last
     v = dpp_max<0x112>(v);
     v = dpp_max<0x114>(v);
     v = dpp_max<0x118>(v);
     v = dpp_max<0x142>(v);        // row_bcast 15, 31: across the four rows, in lane 63
     v = dpp_max<0x143>(v);
-    return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), 63) << 32) |
-           (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// One wave picks the k largest of a token's E logits z (LDS), ties to the
-// lower expert, and writes ids and the softmax of the chosen.  The order is
-// that of 64-bit keys rising with the logit (-0 equals +0); a NaN ranks as
-// minus infinity, so there are always k experts to take.
+// One wave picks the k largest of a token's E <= 64 V logits z (LDS), ties to
+// the lower expert, and writes ids and the softmax of the chosen.  The order is
+// that of 64-bit keys rising with the logit (-0 equals +0), found by their high
+// words first; a NaN ranks as minus infinity, so there are always k experts to
+// take.
+template <int V>
 __device__ __forceinline__ void select_experts(const double* z, int E, int k, int lane, int32_t* ids, float* w) {
-    constexpr int V = kMaxRouteExperts / 64;
-    uint64_t key[V];
+    uint32_t hi[V], lo[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int e = lane + 64 * j;
-        key[j] = 0;
+        hi[j] = lo[j] = 0;
         if (e < E) {
             const double v = z[e] == z[e] ? z[e] + 0.0 : -INFINITY;
-            const uint64_t b = (uint64_t)__double_as_longlong(v);
-            key[j] = (b >> 63) ? ~b : b | (1ull << 63);
+            uint64_t b = (uint64_t)__double_as_longlong(v);
+            b = (b >> 63) ? ~b : b | (1ull << 63);
+            hi[j] = (uint32_t)(b >> 32);
+            lo[j] = (uint32_t)b;
         }
     }
     int mine = 0;                  // lane r keeps the r-th expert
     for (int r = 0; r < k; ++r) {
-        uint64_t m = key[0];
+        uint32_t m = hi[0];
 #pragma unroll
-        for (int j = 1; j < V; ++j) m = key[j] > m ? key[j] : m;
+        for (int j = 1; j < V; ++j) m = hi[j] > m ? hi[j] : m;
         m = wave_max(m);
-        int e = -1;
+        uint64_t b[V];
+        int n = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint64_t b = __ballot(key[j] == m);
-            if (e < 0 && b) e = 64 * j + __builtin_ctzll(b);
+            b[j] = __ballot(hi[j] == m);
+            n += __popcll(b[j]);
         }
+        if (n > 1) {               // equal high words: the largest low word, then the lowest expert
+            uint32_t l = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) l = hi[j] == m && lo[j] > l ? lo[j] : l;
+            l = wave_max(l);
+#pragma unroll
+            for (int j = 0; j < V; ++j) b[j] = __ballot(hi[j] == m && lo[j] == l);
+        }
+        int e = -1;
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (lane + 64 * j == e) key[j] = 0;
+            if (e < 0 && b[j]) e = 64 * j + __builtin_ctzll(b[j]);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (lane + 64 * j == e) hi[j] = lo[j] = 0;
         if (lane == r) mine = e;
     }
+    const double ex = exp(z[mine] - z[__builtin_amdgcn_readfirstlane(mine)]);
+    const uint64_t eb = (uint64_t)__double_as_longlong(ex);
+    double sum = 0.0;
+    for (int r = 0; r < k; ++r)
+        sum += __longlong_as_double((long long)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(eb >> 32), r) << 32) |
+                                                (uint32_t)__builtin_amdgcn_readlane((int)eb, r)));
     if (lane < k) {
-        const double ex = exp(z[mine] - z[__builtin_amdgcn_readfirstlane(mine)]);
-        double sum = 0.0;
-        for (int r = 0; r < k; ++r) sum += __shfl(ex, r, 64);
         ids[lane] = mine;
         w[lane] = (float)(ex / sum);
     }
 }
 
-// Workgroup (slice of d, 64 experts, 4 tokens): partial logits on the fp64
+// Workgroup (slice of d, 64 experts, 8 tokens): partial logits on the fp64
 // matrix cores (bf16 products are exact in fp64, sums are fp64).  Per 32 rows
 // lane group g = l / 16 takes rows 8 g .. 8 g + 7, so MFMA step s contracts
 // rows 8 g + s; column c = l % 16 of tile n is expert 4 c + n, so one 8-byte
@@ -127,6 +151,8 @@ __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
     const int g = lane >> 4, c = lane & 15;
     const int slice = blockIdx.x, e0 = blockIdx.y * kRouteExperts, t0 = blockIdx.z * kRouteTokens;
     const int nt = min(kRouteTokens, a.T - t0);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+        for (int i = tid; i < kHandWords; i += kThreads) a.hand[i] = 0;
     const int k0 = (slice * kWaves + wid) * a.rows, k1 = min(a.d, k0 + a.rows);
     const int e4 = e0 + 4 * c;
     const bool vec = (a.E & 3) == 0;      // rows of the router aligned for 8-byte loads
@@ -169,9 +195,8 @@ __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
     };
     pipelined<D>(max(k1 - k0, 0) / 32, load, work);
     // accumulator element v of lane l: token 4 v + l / 16, expert 4 (l % 16) + n
-    static_assert(kRouteTokens <= 4, "tokens 0..3 are element 0 of their lanes");
 #pragma unroll
-    for (int v = 0; v < 1; ++v) {
+    for (int v = 0; v < kRouteTokens / 4; ++v) {
         const int t = 4 * v + g;
         if (t < nt)
 #pragma unroll
@@ -197,8 +222,14 @@ __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
         zred[i] = s;
     }
     __syncthreads();
-    for (int t = wid; t < nt; t += kWaves)
-        select_experts(zred + t * a.E, a.E, a.k, lane, a.ids + (int64_t)(t0 + t) * a.k, a.w + (int64_t)(t0 + t) * a.k);
+    static_assert(kRouteTokens <= kWaves, "a token a wave");
+    if (wid < nt) {
+        const double* z = zred + wid * a.E;
+        const int64_t o = (int64_t)(t0 + wid) * a.k;
+        if (a.E <= 64) select_experts<1>(z, a.E, a.k, lane, a.ids + o, a.w + o);
+        else if (a.E <= 128) select_experts<2>(z, a.E, a.k, lane, a.ids + o, a.w + o);
+        else select_experts<4>(z, a.E, a.k, lane, a.ids + o, a.w + o);
+    }
 }
 
 // ---- the routed experts --------------------------------------------------------------
@@ -217,8 +248,14 @@ struct ExpertArgs {
     uint16_t* hhi;         // [T k][f] h as two bf16 planes
     uint16_t* hlo;
     float* part;           // [splits][T][d] (splits > 1)
-    uint32_t* counters;    // one per row panel of WdT
+    uint32_t* counters;    // one per workgroup of row panels of WdT
+    uint32_t* hand;        // the launch's hand-over counters, zero at its start
     int T, E, k, d, f, splits;
+};
+
+// A tile: at most kTile routes of one expert.
+struct Tile {
+    int e, first, nt;      // expert, first place in Groups::route, count
 };
 
 // The call's routes grouped by expert, in LDS.  A token names an expert at most
@@ -227,16 +264,29 @@ struct ExpertArgs {
 struct Groups {
     unsigned long long mask[kMaxRouteExperts];   // tokens routed to the expert
     int start[kMaxRouteExperts];                 // first of its routes in `route`
-    int tile0[kMaxRouteExperts];                 // first tile of an expert
-    int n_tiles;                                 // tiles of at most kTile routes of one expert, by expert
-    uint16_t expert[kMaxTiles];                  // a tile's expert
+    int n_tiles;
+    uint32_t tile[kMaxTiles];                    // by expert: e | first << 8 | nt << 18
     uint16_t route[kMaxRoutes];                  // routes t k + j by expert
+
+    __device__ __forceinline__ Tile at(int i) const {
+        const uint32_t v = __builtin_amdgcn_readfirstlane(tile[i]);
+        return Tile{(int)(v & 255), (int)((v >> 8) & 1023), (int)(v >> 18)};
+    }
 };
 
 // Every thread of the workgroup calls it.
-__device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int R, int E, int k) {
+__device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int T, int E, int k) {
     constexpr int PT = kMaxRoutes / kThreads;
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x, lane = tid & 63, R = T * k;
+    if (T == 1) {                         // a tile per route
+        if (tid < k) {
+            g.tile[tid] = (uint32_t)ids[tid] | ((uint32_t)tid << 8) | (1u << 18);
+            g.route[tid] = (uint16_t)tid;
+        }
+        if (tid == 0) g.n_tiles = k;
+        __syncthreads();
+        return;
+    }
     for (int e = tid; e < E; e += kThreads) g.mask[e] = 0;
     __syncthreads();
     int id[PT], tok[PT];
@@ -267,9 +317,11 @@ __device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int 
                 }
             }
             if (c > 0) {
-                g.start[e] = base + sc - c;
-                g.tile0[e] = tiles + st - tl;
-                for (int q = 0; q < tl; ++q) g.expert[tiles + st - tl + q] = (uint16_t)e;
+                const int first = base + sc - c;
+                g.start[e] = first;
+                for (int q = 0; q < tl; ++q)
+                    g.tile[tiles + st - tl + q] = (uint32_t)e | ((uint32_t)(first + q * kTile) << 8) |
+                                                  ((uint32_t)min(kTile, c - q * kTile) << 18);
             }
             base += __shfl(sc, 63, 64);
             tiles += __shfl(st, 63, 64);
@@ -285,33 +337,96 @@ __device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int 
     __syncthreads();
 }
 
-// A tile's routes: expert, first place in Groups::route, count.
-struct Tile {
-    int e, first, nt;
-};
-__device__ __forceinline__ Tile tile_of(const Groups& g, int tile) {
-    Tile t;
-    t.e = __builtin_amdgcn_readfirstlane(g.expert[tile]);
-    const int off = (tile - g.tile0[t.e]) * kTile;
-    t.first = __builtin_amdgcn_readfirstlane(g.start[t.e] + off);
-    t.nt = __builtin_amdgcn_readfirstlane(min(kTile, (int)__popcll(g.mask[t.e]) - off));
-    return t;
+// ---- the hand-over from gate/up to down inside a launch ---------------------------------
+//
+// h of every route is needed by every down workgroup, so those wait until all
+// gate/up work is done.  The wait always ends, whatever part of the grid is
+// running and whatever else runs on the device: gate/up work is bound to
+// numbers, not to workgroups.  A workgroup draws the number of its own shard
+// when it starts; one that waits also looks for numbers that nobody has drawn
+// (their workgroups may not have started, and may not start before this one
+// ends) and does their work itself.  So when a workgroup waits with nothing
+// left to draw, every number is in the hands of a running workgroup that does
+// not wait.  Counters lie 128 bytes apart in kShards shards: 256 arrivals on
+// one address take 3 us, on eight of them a third of one.
+
+// Numbers of a shard in a grid of n.
+__device__ __forceinline__ uint32_t shard_size(int shard, int n) { return (uint32_t)((n - shard + kShards - 1) / kShards); }
+
+__device__ __forceinline__ uint32_t draw(uint32_t* hand, int shard) {
+    return __hip_atomic_fetch_add(hand + kDrawn + shard * kShardStep, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Gate/up and SwiGLU: workgroups take items (tile, 32 neurons); the waves split
-// K = d.  The next unit's loads are in flight while one is multiplied, across
-// items too, so the stream does not stop for an item's sums.
-template <int FMT, int NX>
-__global__ void __launch_bounds__(kThreads, 2) layer_gateup_kernel(ExpertArgs a) {
-    extern __shared__ __attribute__((aligned(16))) float red[];
-    __shared__ Groups g;
+// One wave: waits until all numbers are done (returns -1), or returns a number
+// that it has drawn for an absent workgroup (>= 0), or gives up (-2).
+__device__ __forceinline__ int wait_done(uint32_t* hand, int n, int lane) {
+    const int shard = lane & (kShards - 1);
+    const uint32_t size = shard_size(shard, n);
+    for (uint32_t i = 0; i < kMaxPolls; ++i) {
+        const uint32_t drawn = __hip_atomic_load(hand + kDrawn + shard * kShardStep, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint32_t done = __hip_atomic_load(hand + kDone + shard * kShardStep, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (__ballot(done < size) == 0) return -1;
+        const uint64_t open = __ballot(drawn < size);
+        if (open) {
+            const int s = __builtin_ctzll(open) & (kShards - 1);
+            uint32_t v = 0;
+            if (lane == 0) v = draw(hand, s);
+            v = __builtin_amdgcn_readfirstlane(v);
+            if (v < shard_size(s, n)) return (int)v * kShards + s;
+        }
+        __builtin_amdgcn_s_sleep(1);
+    }
+    return -2;
+}
+
+// The waves' sums of a tile's gate and up panels p, SwiGLU, h.
+template <int NX>
+__device__ __forceinline__ void store_h(const ExpertArgs& a, const Groups& g, float* red, const Tile& t, int p, Acc (&ag)[NX],
+                                        Acc (&au)[NX]) {
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-    group_routes(g, a.ids, a.T * a.k, a.E, a.k);
+    const int half = kWaves * t.nt * kRedRow;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+        put_acc(red, ag[i], i, wid, t.nt, lane);
+        put_acc(red + half, au[i], i, wid, t.nt, lane);
+        ag[i] = au[i] = zero_acc();
+    }
+    __syncthreads();
+    float gs[kPlaces], us[kPlaces];
+    sum_waves(gs, red, t.nt, tid);
+    sum_waves(us, red + half, t.nt, tid);
+#pragma unroll
+    for (int i = 0; i < kPlaces; ++i) {
+        const int m = (tid + i * kThreads) >> 5;
+        // h in 16 significant bits: its rounding stays far below that of y.  Two
+        // neurons a store, past the L2 that other XCDs do not see: the even
+        // lane's for the high halves, the odd lane's for the low ones.
+        uint16_t h, l;
+        split_bf16(silu(gs[i]) * us[i], h, l);
+        const uint32_t mine = (uint32_t)h | ((uint32_t)l << 16);
+        const uint32_t other = (uint32_t)__shfl_xor((int)mine, 1, 64);
+        if (m < t.nt) {
+            const bool odd = tid & 1;
+            const int64_t o = (int64_t)g.route[t.first + m] * a.f + p * 32 + (tid & 30);
+            const uint32_t v = odd ? (other >> 16) | (mine & 0xFFFF0000u) : (mine & 0xFFFFu) | (other << 16);
+            __hip_atomic_store(reinterpret_cast<uint32_t*>((odd ? a.hlo : a.hhi) + o), v, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+}
+
+// Gate/up and SwiGLU: number v does the items (tile, 32 neurons) v, v + grid,
+// ...; the waves split K = d.  The next unit's loads are in flight while one is
+// multiplied, across items too, so the stream does not stop for an item's
+// sums.
+template <int FMT, int NX>
+__device__ __forceinline__ void layer_gateup(const ExpertArgs& a, const Groups& g, float* red, const int first_item) {
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, grid = gridDim.x;
     const int panels = a.f >> 5, items = g.n_tiles * panels;
     const int units = a.d / kUnit;
     const int u0 = wid * units / kWaves, nu = (wid + 1) * units / kWaves - u0;
-    const int steps = max(nu, 1);         // a wave without units (d < 1024) loads one and leaves it
-
+    const int steps = max(nu, 1);     // a wave without units (d < 1024) loads one and leaves it
     struct Cursor {
         int item, step;
         Tile t;
@@ -322,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 2) layer_gateup_kernel(ExpertArgs a)
         c.item = item;
         c.step = 0;
         const int tile = item / panels, p = item - tile * panels;
-        c.t = tile_of(g, tile);
+        c.t = g.at(tile);
         const uint8_t* rec = a.rec + (int64_t)c.t.e * a.stride;
         c.pg = panel_ref<FMT>(rec + a.off_gate, rec + a.off_sg, a.d, p);
         c.pu = panel_ref<FMT>(rec + a.off_up, rec + a.off_su, a.d, p);
@@ -333,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 2) layer_gateup_kernel(ExpertArgs a)
     };
     WUnit<FMT> wg[2], wu[2];
     XUnit xu[2][NX][1];
-    Cursor ld;                            // the next unit to load
+    Cursor ld;                        // the next unit to load
     auto load = [&](int b) {
         const int u = min(u0 + ld.step, units - 1);
         load_unit<FMT>(wg[b], ld.pg, u, lane);
@@ -341,14 +456,14 @@ __global__ void __launch_bounds__(kThreads, 2) layer_gateup_kernel(ExpertArgs a)
 #pragma unroll
         for (int i = 0; i < NX; ++i)
             if (i == 0 || ld.t.nt > i * kCols) load_x<FMT>(xu[b][i][0], ld.x[i], u, lane);
-        if (++ld.step == steps && ld.item + (int)gridDim.x < items) enter(ld, ld.item + gridDim.x);
+        if (++ld.step == steps && ld.item + grid < items) enter(ld, ld.item + grid);
     };
     Acc ag[NX], au[NX];
-    int item = blockIdx.x, step = 0;
+    int item = first_item, step = 0;
     if (item >= items) return;
     enter(ld, item);
     load(0);
-    Tile t = tile_of(g, item / panels);
+    Tile t = g.at(item / panels);
 #pragma unroll
     for (int i = 0; i < NX; ++i) ag[i] = au[i] = zero_acc();
     // one step: unit `step` of `item`; after the item's last one its sums; true at the end
@@ -359,38 +474,15 @@ __global__ void __launch_bounds__(kThreads, 2) layer_gateup_kernel(ExpertArgs a)
             mma_unit<FMT, NX, 1>(au, wu[b], xu[b], nx);
         }
         if (++step < steps) return false;
-        const int half = kWaves * t.nt * kRedRow;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            put_acc(red, ag[i], i, wid, t.nt, lane);
-            put_acc(red + half, au[i], i, wid, t.nt, lane);
-            ag[i] = au[i] = zero_acc();
-        }
-        __syncthreads();
-        float gs[kPlaces], us[kPlaces];
-        sum_waves(gs, red, t.nt, tid);
-        sum_waves(us, red + half, t.nt, tid);
-        const int p = item % panels;
-#pragma unroll
-        for (int i = 0; i < kPlaces; ++i) {
-            const int m = (tid + i * kThreads) >> 5;
-            if (m >= t.nt) break;
-            // h in 16 significant bits: its rounding stays far below that of y
-            uint16_t h, l;
-            split_bf16(silu(gs[i]) * us[i], h, l);
-            const int64_t o = (int64_t)g.route[t.first + m] * a.f + p * 32 + (tid & 31);
-            a.hhi[o] = h;
-            a.hlo[o] = l;
-        }
-        item += gridDim.x;
+        store_h<NX>(a, g, red, t, item % panels, ag, au);
+        item += grid;
         if (item >= items) return true;
         step = 0;
-        t = tile_of(g, item / panels);
+        t = g.at(item / panels);
         return false;
     };
     // whether a step follows the current one
-    auto more = [&]() { return step + 1 < steps || item + (int)gridDim.x < items; };
+    auto more = [&]() { return step + 1 < steps || item + grid < items; };
     for (;;) {
         if (more()) load(1);
         if (advance(0)) return;
@@ -399,139 +491,272 @@ __global__ void __launch_bounds__(kThreads, 2) layer_gateup_kernel(ExpertArgs a)
     }
 }
 
-// Down and combine: workgroup (NP row panels of WdT, split).  The tiles' K = f
-// units form one axis, divided evenly over the splits and their waves.  A
-// wave sums a tile's units with the tile's routes as columns, then adds w
-// times the sum to its own [token][row] sums in LDS: a token's sums see the
-// tiles in order, whatever else the tile holds, and a column past the tile's
-// routes goes nowhere.  The waves' sums are added in order, and with several
-// splits the panels' last workgroup adds the splits in order, so y does not
-// depend on timing.
+// The same, one load at a time: the part of an absent workgroup, which is hardly
+// ever done, without the registers of a pipeline.  The same sums in the same
+// order.
+template <int FMT, int NX>
+__device__ __forceinline__ void layer_gateup_absent(const ExpertArgs& a, const Groups& g, float* red, const int first_item) {
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+    const int panels = a.f >> 5, items = g.n_tiles * panels, units = a.d / kUnit;
+    const int u0 = wid * units / kWaves, u1 = (wid + 1) * units / kWaves;
+#pragma unroll 1
+    for (int item = first_item; item < items; item += gridDim.x) {
+        const int p = item % panels;
+        const Tile t = g.at(item / panels);
+        const uint8_t* rec = a.rec + (int64_t)t.e * a.stride;
+        const PanelRef pg = panel_ref<FMT>(rec + a.off_gate, rec + a.off_sg, a.d, p);
+        const PanelRef pu = panel_ref<FMT>(rec + a.off_up, rec + a.off_su, a.d, p);
+        Acc ag[NX], au[NX];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) ag[i] = au[i] = zero_acc();
+#pragma unroll 1
+        for (int u = u0; u < u1; ++u) {
+            WUnit<FMT> w;
+            XUnit x[NX][1];
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                load_x<FMT>(x[i][0], a.x + (int64_t)(g.route[t.first + min(i * kCols + (lane & 15), t.nt - 1)] / a.k) * a.d, u,
+                            lane);
+            load_unit<FMT>(w, pg, u, lane);
+            mma_unit<FMT, NX, 1>(ag, w, x, NX);
+            load_unit<FMT>(w, pu, u, lane);
+            mma_unit<FMT, NX, 1>(au, w, x, NX);
+        }
+        store_h<NX>(a, g, red, t, p, ag, au);
+    }
+}
+
+// A number's h is on its way past the L2 before the number counts as done.
+__device__ __forceinline__ void number_done(uint32_t* hand, int number) {
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        __hip_atomic_fetch_add(hand + kDone + (number % kShards) * kShardStep, 1u, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+}
+
 template <int NP>
 constexpr int sum_row() { return 32 * NP + 4; }      // floats of a token's sums in LDS, padded
 
-template <int FMT, int NX, int NP>
-__global__ void __launch_bounds__(kThreads, 2) layer_down_kernel(ExpertArgs a) {
-    extern __shared__ __attribute__((aligned(16))) float sums[];     // [kWaves][T][sum_row]
+// Down and combine: items (NP row panels of WdT, split) go round the
+// workgroups.  The tiles' K = f units form one axis, divided evenly over the
+// splits and their waves.  A wave sums a tile's units with the tile's routes as
+// columns, then adds w times the sum to its own [token][row] sums in LDS: a
+// token's sums see the tiles in order, whatever else the tile holds, and a
+// column past the tile's routes goes nowhere.  The waves' sums are added in
+// order, and with several splits the panels' last workgroup adds the splits in
+// order, so y does not depend on timing.  wait(again) is called once, before h
+// is first read, with the first unit of weights on its way; where it has used
+// the registers meanwhile it calls again().  It returns whether h is there.
+template <int FMT, int NX, int NP, typename Wait>
+__device__ __forceinline__ void layer_down(const ExpertArgs& a, const Groups& g, const float* wr, float* red, uint32_t* flag,
+                                           Wait&& wait) {
+    constexpr int SR = sum_row<NP>();
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, grid = gridDim.x;
+    const int dwg = a.d / 32 / NP, ditems = dwg * a.splits;
+    const int uf = a.f / kUnit, units = g.n_tiles * uf;
+    bool there = true;
+    for (int item = blockIdx.x; item < ditems; item += grid) {
+        const int p0 = (item % dwg) * NP, split = item / dwg;
+        const int part = split * kWaves + wid, parts = a.splits * kWaves;
+        const int u0 = (int)((int64_t)part * units / parts), u1 = (int)((int64_t)(part + 1) * units / parts);
+        struct Cursor {
+            int tile, kk;
+            Tile t;
+            PanelRef pd[NP];
+            int64_t h[NX];
+        };
+        auto enter = [&](Cursor& c, int tile) {
+            c.tile = tile;
+            c.kk = 0;
+            c.t = g.at(tile);
+            const uint8_t* rec = a.rec + (int64_t)c.t.e * a.stride;
+#pragma unroll
+            for (int n = 0; n < NP; ++n) c.pd[n] = panel_ref<FMT>(rec + a.off_down, rec + a.off_sd, a.f, p0 + n);
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                c.h[i] = (int64_t)g.route[c.t.first + min(i * kCols + (lane & 15), c.t.nt - 1)] * a.f;
+        };
+        WUnit<FMT> wd[2][NP];
+        XUnit hu[2][NX][2];
+        Cursor ld;                            // the next unit to load
+        auto load_w = [&](int b) {
+#pragma unroll
+            for (int n = 0; n < NP; ++n) load_unit<FMT>(wd[b][n], ld.pd[n], ld.kk, lane);
+        };
+        auto load_h = [&](int b) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                if (i == 0 || ld.t.nt > i * kCols) {
+                    load_x<FMT>(hu[b][i][0], a.hhi + ld.h[i], ld.kk, lane);
+                    load_x<FMT>(hu[b][i][1], a.hlo + ld.h[i], ld.kk, lane);
+                }
+            if (++ld.kk == uf && ld.tile + 1 < g.n_tiles) enter(ld, ld.tile + 1);
+        };
+        auto first_w = [&]() {
+            if (u0 < u1) {
+                enter(ld, u0 / uf);
+                ld.kk = u0 % uf;
+                load_w(0);
+            }
+        };
+        first_w();
+        if (item == (int)blockIdx.x) there = wait(first_w);
+        float* mine = red + wid * a.T * SR;
+        for (int i = lane * 4; i < a.T * SR; i += 256) *reinterpret_cast<f32x4_t*>(mine + i) = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        if (u0 < u1) {
+            Acc acc[NP][NX];
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+#pragma unroll
+                for (int i = 0; i < NX; ++i) acc[n][i] = zero_acc();
+            int u = u0, tile = u0 / uf, kk = u0 - tile * uf;
+            load_h(0);
+            Tile t = g.at(tile);
+            auto advance = [&](int b) -> bool {
+                const int nx = t.nt > kCols ? 2 : 1;
+#pragma unroll
+                for (int n = 0; n < NP; ++n) mma_unit<FMT, NX, 2>(acc[n], wd[b][n], hu[b], nx);
+                const bool last = ++u == u1;
+                if (++kk < uf && !last) return false;
+#pragma unroll
+                for (int i = 0; i < NX; ++i) {
+                    const int m = i * kCols + (lane & 15);
+                    if (m < t.nt) {
+                        const int r = g.route[t.first + m];
+                        const float w = wr[r];
+                        float* s = mine + (r / a.k) * SR + 4 * (lane >> 4);
+#pragma unroll
+                        for (int n = 0; n < NP; ++n)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                f32x4_t* q = reinterpret_cast<f32x4_t*>(s + 32 * n + 16 * h);
+                                f32x4_t v = *q;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) v[e] = fmaf(w, acc[n][i].h[h][e], v[e]);
+                                *q = v;
+                            }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) acc[n][i] = zero_acc();
+                }
+                if (last) return true;
+                kk = 0;
+                t = g.at(++tile);
+                return false;
+            };
+            auto next = [&](int b) {
+                if (u + 1 < u1) {
+                    load_w(b);
+                    load_h(b);
+                }
+            };
+            for (;;) {
+                next(1);
+                if (advance(0)) break;
+                next(0);
+                if (advance(1)) break;
+            }
+        }
+        __syncthreads();
+        auto emit = [&](int t, int n, float v) {
+            const int64_t o = (int64_t)t * a.d + p0 * 32 + n;
+            if (a.base) v += __uint_as_float((uint32_t)a.base[o] << 16);
+            a.y[o] = there ? f32_to_bf16_rne(v) : 0x7FC0;
+        };
+        constexpr int C = 32 * NP;
+        for (int i = tid; i < a.T * C; i += kThreads) {
+            const int t = i / C, n = i % C;
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) s += red[(w * a.T + t) * SR + n];
+            if (a.splits == 1) emit(t, n, s);
+            else put_agent(a.part + ((int64_t)split * a.T + t) * a.d + p0 * 32 + n, s);
+        }
+        if (a.splits > 1 && last_arrival(a.counters + item % dwg, a.splits, flag)) {
+            for (int i = tid; i < a.T * C; i += kThreads) {
+                const int t = i / C, n = i % C;
+                float s = 0.0f;
+#pragma unroll 4
+                for (int q = 0; q < a.splits; ++q) s += get_agent(a.part + ((int64_t)q * a.T + t) * a.d + p0 * 32 + n);
+                emit(t, n, s);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Up to 16 tokens: the routed experts and the combine in one launch.  A launch
+// between gate/up and down costs 2.4 us and empties the card twice; here a
+// workgroup without gate/up work, or done with it, has its down weights under
+// way while it waits.
+template <int FMT, int NP>
+__global__ void __launch_bounds__(kThreads, 2) layer_experts_kernel(ExpertArgs a) {
+    extern __shared__ __attribute__((aligned(16))) float red[];     // the waves' sums of either half
     __shared__ Groups g;
     __shared__ float wr[kMaxRoutes];
     __shared__ uint32_t flag;
-    constexpr int SR = sum_row<NP>();
+    __shared__ int number;
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+    const int grid = gridDim.x;
+    if (tid == 0) {
+        const int shard = blockIdx.x % kShards;
+        const uint32_t v = draw(a.hand, shard);
+        number = v < shard_size(shard, grid) ? (int)v * kShards + shard : -1;
+    }
     for (int r = tid; r < a.T * a.k; r += kThreads) wr[r] = a.w[r];
-    float* mine = sums + wid * a.T * SR;
-    for (int i = lane * 4; i < a.T * SR; i += 256) *reinterpret_cast<f32x4_t*>(mine + i) = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    group_routes(g, a.ids, a.T * a.k, a.E, a.k);
-
-    const int p0 = blockIdx.x * NP, split = blockIdx.y;
-    const int uf = a.f / kUnit, units = g.n_tiles * uf;
-    const int part = split * kWaves + wid, parts = a.splits * kWaves;
-    const int u0 = (int)((int64_t)part * units / parts), u1 = (int)((int64_t)(part + 1) * units / parts);
-
-    struct Cursor {
-        int tile, kk;
-        Tile t;
-        PanelRef pd[NP];
-        int64_t h[NX];
-    };
-    auto enter = [&](Cursor& c, int tile) {
-        c.tile = tile;
-        c.kk = 0;
-        c.t = tile_of(g, tile);
-        const uint8_t* rec = a.rec + (int64_t)c.t.e * a.stride;
-#pragma unroll
-        for (int n = 0; n < NP; ++n) c.pd[n] = panel_ref<FMT>(rec + a.off_down, rec + a.off_sd, a.f, p0 + n);
-#pragma unroll
-        for (int i = 0; i < NX; ++i)
-            c.h[i] = (int64_t)g.route[c.t.first + min(i * kCols + (lane & 15), c.t.nt - 1)] * a.f;
-    };
-    WUnit<FMT> wd[2][NP];
-    XUnit hu[2][NX][2];
-    Cursor ld;
-    auto load = [&](int b) {
-#pragma unroll
-        for (int n = 0; n < NP; ++n) load_unit<FMT>(wd[b][n], ld.pd[n], ld.kk, lane);
-#pragma unroll
-        for (int i = 0; i < NX; ++i)
-            if (i == 0 || ld.t.nt > i * kCols) {
-                load_x<FMT>(hu[b][i][0], a.hhi + ld.h[i], ld.kk, lane);
-                load_x<FMT>(hu[b][i][1], a.hlo + ld.h[i], ld.kk, lane);
+    group_routes(g, a.ids, a.T, a.E, a.k);
+    const int mine = number;
+    if (mine >= 0) {
+        layer_gateup<FMT, 1>(a, g, red, mine);
+        number_done(a.hand, mine);
+    }
+    layer_down<FMT, 1, NP>(a, g, wr, red, &flag, [&](auto&& again) -> bool {
+        auto poll = [&]() -> int {
+            __syncthreads();
+            if (wid == 0) {
+                const int r = wait_done(a.hand, grid, lane);
+                if (lane == 0) number = r;
             }
-        if (++ld.kk == uf && ld.tile + 1 < g.n_tiles) enter(ld, ld.tile + 1);
-    };
-    if (u0 < u1) {
-        Acc acc[NP][NX];
-#pragma unroll
-        for (int n = 0; n < NP; ++n)
-#pragma unroll
-            for (int i = 0; i < NX; ++i) acc[n][i] = zero_acc();
-        int u = u0, tile = u0 / uf, kk = u0 - tile * uf;
-        enter(ld, tile);
-        ld.kk = kk;
-        load(0);
-        Tile t = tile_of(g, tile);
-        auto advance = [&](int b) -> bool {
-            const int nx = t.nt > kCols ? 2 : 1;
-#pragma unroll
-            for (int n = 0; n < NP; ++n) mma_unit<FMT, NX, 2>(acc[n], wd[b][n], hu[b], nx);
-            const bool last = ++u == u1;
-            if (++kk < uf && !last) return false;
-#pragma unroll
-            for (int i = 0; i < NX; ++i) {
-                const int m = i * kCols + (lane & 15);
-                if (m < t.nt) {
-                    const int r = g.route[t.first + m];
-                    const float w = wr[r];
-                    float* s = mine + (r / a.k) * SR + 4 * (lane >> 4);
-#pragma unroll
-                    for (int n = 0; n < NP; ++n)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            f32x4_t* q = reinterpret_cast<f32x4_t*>(s + 32 * n + 16 * h);
-                            f32x4_t v = *q;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) v[e] = fmaf(w, acc[n][i].h[h][e], v[e]);
-                            *q = v;
-                        }
-                }
-#pragma unroll
-                for (int n = 0; n < NP; ++n) acc[n][i] = zero_acc();
-            }
-            if (last) return true;
-            kk = 0;
-            t = tile_of(g, ++tile);
-            return false;
+            __syncthreads();
+            return number;
         };
-        for (;;) {
-            if (u + 1 < u1) load(1);
-            if (advance(0)) break;
-            if (u + 1 < u1) load(0);
-            if (advance(1)) break;
+        int r = poll();
+        if (r >= 0) {                         // do absent workgroups' parts first, then load again
+            do {
+                layer_gateup_absent<FMT, 1>(a, g, red, r);
+                number_done(a.hand, r);
+                r = poll();
+            } while (r >= 0);
+            again();
         }
-    }
-    __syncthreads();
-    auto emit = [&](int t, int n, float v) {
-        const int64_t o = (int64_t)t * a.d + p0 * 32 + n;
-        if (a.base) v += __uint_as_float((uint32_t)a.base[o] << 16);
-        a.y[o] = f32_to_bf16_rne(v);
-    };
-    constexpr int C = 32 * NP;
-    for (int i = tid; i < a.T * C; i += kThreads) {
-        const int t = i / C, n = i % C;
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) s += sums[(w * a.T + t) * SR + n];
-        if (a.splits == 1) emit(t, n, s);
-        else put_agent(a.part + ((int64_t)split * a.T + t) * a.d + p0 * 32 + n, s);
-    }
-    if (a.splits == 1 || !last_arrival(a.counters + blockIdx.x, a.splits, &flag)) return;
-    for (int i = tid; i < a.T * C; i += kThreads) {
-        const int t = i / C, n = i % C;
-        float s = 0.0f;
-#pragma unroll 4
-        for (int q = 0; q < a.splits; ++q) s += get_agent(a.part + ((int64_t)q * a.T + t) * a.d + p0 * 32 + n);
-        emit(t, n, s);
-    }
+        // h is read through the caches from here on: no XCD holds an older copy of it,
+        // since a launch starts with its caches invalidated and nothing of it reads h
+        // before this.  (An agent-scope fence would invalidate the XCD's L2 once per
+        // wave; the down half took 14 us more with one.)
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+        return r == -1;
+    });
+}
+
+// More tokens: two launches, whose second operand of 16 columns leaves no
+// registers for the hand-over (it is 1% of these calls and less).
+template <int FMT>
+__global__ void __launch_bounds__(kThreads, 2) layer_gateup_kernel(ExpertArgs a) {
+    extern __shared__ __attribute__((aligned(16))) float red[];
+    __shared__ Groups g;
+    group_routes(g, a.ids, a.T, a.E, a.k);
+    layer_gateup<FMT, 2>(a, g, red, blockIdx.x);
+}
+template <int FMT, int NP>
+__global__ void __launch_bounds__(kThreads, 2) layer_down_kernel(ExpertArgs a) {
+    extern __shared__ __attribute__((aligned(16))) float red[];
+    __shared__ Groups g;
+    __shared__ float wr[kMaxRoutes];
+    __shared__ uint32_t flag;
+    for (int r = threadIdx.x; r < a.T * a.k; r += kThreads) wr[r] = a.w[r];
+    group_routes(g, a.ids, a.T, a.E, a.k);
+    layer_down<FMT, 2, NP>(a, g, wr, red, &flag, [](auto&&) { return true; });
 }
 
 // Row panels per down workgroup.  The h loads beside an MXFP4 panel outweigh its
@@ -595,27 +820,29 @@ hipError_t launch_fmt(const ft_shape& s, const RouteArgs& r, const ExpertArgs& a
     const int R = a.T * a.k;
     const int tiles = (R < a.E ? R : a.E) + R / (kTile + 1);
     const int64_t items = (int64_t)tiles * (a.f / 32);
-    const dim3 gg((unsigned)(items < 256 ? items : 256));
+    const int np = down_panels(s, a.T);
+    const int64_t ditems = (int64_t)(a.d / 32 / np) * a.splits;
     const int nt = a.T < kTile ? a.T : kTile;
     const size_t glds = (size_t)2 * kWaves * nt * kRedRow * sizeof(float);
-    const bool one = a.T <= kCols;        // every tile fits one operand
-    if (one) hipLaunchKernelGGL((layer_gateup_kernel<FMT, 1>), gg, dim3(kThreads), glds, st, a);
-    else hipLaunchKernelGGL((layer_gateup_kernel<FMT, 2>), gg, dim3(kThreads), glds, st, a);
+    const size_t dlds = (size_t)kWaves * a.T * (32 * np + 4) * sizeof(float);
+    auto blocks = [](int64_t n) { return dim3((unsigned)(n < 256 ? n : 256)); };
+    if (a.T <= kCols) {                   // every tile fits one operand
+        const dim3 grid = blocks(items > ditems ? items : ditems);
+        const size_t lds = glds > dlds ? glds : dlds;
+        if (FMT == FT_FMT_MXFP4_B32 && np == 2)
+            hipLaunchKernelGGL((layer_experts_kernel<FMT, FMT == FT_FMT_MXFP4_B32 ? 2 : 1>), grid, dim3(kThreads), lds, st, a);
+        else
+            hipLaunchKernelGGL((layer_experts_kernel<FMT, 1>), grid, dim3(kThreads), lds, st, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(layer_gateup_kernel<FMT>, blocks(items), dim3(kThreads), glds, st, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-
-    const int np = down_panels(s, a.T);
-    const dim3 dg(a.d / 32 / np, a.splits);
-    const size_t dlds = (size_t)kWaves * a.T * (32 * np + 4) * sizeof(float);
-    if constexpr (FMT == FT_FMT_MXFP4_B32) {
-        if (np == 2) {
-            if (one) hipLaunchKernelGGL((layer_down_kernel<FMT, 1, 2>), dg, dim3(kThreads), dlds, st, a);
-            else hipLaunchKernelGGL((layer_down_kernel<FMT, 2, 2>), dg, dim3(kThreads), dlds, st, a);
-            return hipGetLastError();
-        }
-    }
-    if (one) hipLaunchKernelGGL((layer_down_kernel<FMT, 1, 1>), dg, dim3(kThreads), dlds, st, a);
-    else hipLaunchKernelGGL((layer_down_kernel<FMT, 2, 1>), dg, dim3(kThreads), dlds, st, a);
+    const dim3 grid((unsigned)ditems);
+    if (FMT == FT_FMT_MXFP4_B32 && np == 2)
+        hipLaunchKernelGGL((layer_down_kernel<FMT, FMT == FT_FMT_MXFP4_B32 ? 2 : 1>), grid, dim3(kThreads), dlds, st, a);
+    else
+        hipLaunchKernelGGL((layer_down_kernel<FMT, 1>), grid, dim3(kThreads), dlds, st, a);
     return hipGetLastError();
 }
 
@@ -649,6 +876,7 @@ hipError_t launch_layer(const ft_shape& s, const LayerArgs& la, ft_workspace* ws
     r.slices = route_slices(s.d_model, s.experts, la.T);
     r.part = reinterpret_cast<double*>(m + b.logits);
     r.counters = counters;
+    r.hand = counters + kHandAt;
     r.ids = la.ids;
     r.w = la.w;
     ExpertArgs a;
@@ -669,6 +897,7 @@ hipError_t launch_layer(const ft_shape& s, const LayerArgs& la, ft_workspace* ws
     a.hlo = reinterpret_cast<uint16_t*>(m + b.hlo);
     a.part = reinterpret_cast<float*>(m + b.part);
     a.counters = counters + kMaxLayerTokens;
+    a.hand = counters + kHandAt;
     a.T = la.T;
     a.E = s.experts;
     a.k = s.top_k;

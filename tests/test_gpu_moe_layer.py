@@ -233,3 +233,29 @@ def test_refusals_with_a_workspace():
         assert err.value.status == M.FT_ERR_ARG
     torch.cuda.synchronize()
     assert all((o == -7).all() for o in out)
+
+
+@pytest.mark.parametrize("T", [1, 5, 16])
+def test_one_launch_experts_share_the_card(T):
+    """Few-token calls on three streams at once, with a large product on a fourth: workgroups of each call start
+    late or after others wait, and every call gives the bits it gives alone."""
+    cfg = config("bf16", 2048, 768, 128, 8, seed=15)
+    recs = synth.bank(cfg)
+    layers = [Layer(cfg, T, recs) for _ in range(3)]
+    xs = [synth.tokens(cfg, T, 20 + i) for i in range(3)]
+    want = [l(x) for l, x in zip(layers, xs)]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    xd = [dev_u16(x) for x in xs]
+    outs = [l.outputs(T) for l in layers]
+    m = torch.randn(2048, 2048, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(30):
+        for j in range(3):
+            layers[j].enqueue(xd[j], outs[j], stream=streams[j])
+        if i % 10 == 0:
+            with torch.cuda.stream(streams[3]):
+                m = (m @ m).clamp(-1, 1)
+    torch.cuda.synchronize()
+    for j in range(3):
+        for got, ref in zip((outs[j][0].cpu().numpy(), outs[j][1].cpu().numpy(), bits(outs[j][2])), want[j]):
+            np.testing.assert_array_equal(got, ref)
