@@ -161,35 +161,57 @@ __device__ __forceinline__ void lora_rows(f32x16_t (&acc)[MI][2], const LoraGemm
                 left[mi] &= ~hit[mi];
             }
             const int rank = min(max(lo.rank[ad], 0), R);
-            for (int k0 = 0; k0 < rank; k0 += 16) {
-                const int have = rank - k0 - g * 8;      // ranks of this lane's eight that exist
+            // steps (16 ranks, part of v), the next one's loads under way while one is multiplied
+            constexpr int NB = GU ? 1 : 2;
+            u32x4_t bw[2][NB], hv[2][MI], lv[2][MI];
+            const int steps = (rank + 15) / 16 * a.vparts;
+            auto load = [&](int q, int i) {
+                const int k0 = i / a.vparts * 16, part = i % a.vparts;
 #pragma unroll
-                for (int ni = 0; ni < 2; ++ni) {
-                    if (GU && ni != pool) continue;
-                    u32x4_t bw = *reinterpret_cast<const u32x4_t*>(
-                        lo.b + ((int64_t)ad * n + pn[ni] * 32 + (lane & 31)) * R + k0 + g * 8);
+                for (int j = 0; j < NB; ++j)
+                    bw[q][j] = *reinterpret_cast<const u32x4_t*>(
+                        lo.b + ((int64_t)ad * n + pn[GU ? pool : j] * 32 + (lane & 31)) * R + k0 + g * 8);
+                const int64_t at = (int64_t)part * a.T * R + k0;
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) {
+                    hv[q][mi] = lv[q][mi] = u32x4_t{0u, 0u, 0u, 0u};
+                    if (id[mi] == ad) {
+                        hv[q][mi] = *reinterpret_cast<const u32x4_t*>(a.vhi[pool] + at + vrow[mi]);
+                        lv[q][mi] = *reinterpret_cast<const u32x4_t*>(a.vlo[pool] + at + vrow[mi]);
+                    }
+                }
+            };
+            auto work = [&](int q, int i) {
+                const int have = rank - i / a.vparts * 16 - g * 8;       // ranks of this lane's eight that exist
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    u32x4_t w = bw[q][j];
                     if (have < 8) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            bw[j] &= have >= 2 * j + 2 ? 0xFFFFFFFFu : have == 2 * j + 1 ? 0xFFFFu : 0u;
+                        for (int e = 0; e < 4; ++e) w[e] &= have >= 2 * e + 2 ? 0xFFFFFFFFu : have == 2 * e + 1 ? 0xFFFFu : 0u;
                     }
-                    const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, bw);
+                    const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, w);
 #pragma unroll
                     for (int mi = 0; mi < MI; ++mi) {
                         if (!hit[mi]) continue;
-                        u32x4_t h = u32x4_t{0u, 0u, 0u, 0u}, l = h;
-                        if (id[mi] == ad) {
-                            h = *reinterpret_cast<const u32x4_t*>(a.vhi[pool] + vrow[mi] + k0);
-                            l = *reinterpret_cast<const u32x4_t*>(a.vlo[pool] + vrow[mi] + k0);
-                        }
                         f32x16_t sum;
 #pragma unroll
                         for (int v = 0; v < 16; ++v) sum[v] = 0.0f;
-                        sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf, __builtin_bit_cast(bf16x8_t, h), sum, 0, 0, 0);
-                        sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf, __builtin_bit_cast(bf16x8_t, l), sum, 0, 0, 0);
+                        sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf, __builtin_bit_cast(bf16x8_t, hv[q][mi]), sum, 0, 0, 0);
+                        sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf, __builtin_bit_cast(bf16x8_t, lv[q][mi]), sum, 0, 0, 0);
+                        f32x16_t& c = acc[mi][GU ? pool : j];
 #pragma unroll
-                        for (int v = 0; v < 16; ++v) acc[mi][ni][v] = id[mi] == ad ? acc[mi][ni][v] + sum[v] : acc[mi][ni][v];
+                        for (int v = 0; v < 16; ++v) c[v] = id[mi] == ad ? c[v] + sum[v] : c[v];
                     }
+                }
+            };
+            if (steps > 0) load(0, 0);
+            for (int i = 0; i < steps; i += 2) {
+                if (i + 1 < steps) load(1, i + 1);
+                work(0, i);
+                if (i + 1 < steps) {
+                    if (i + 2 < steps) load(0, i + 2);
+                    work(1, i + 1);
                 }
             }
         }

@@ -72,9 +72,11 @@ __device__ __forceinline__ void list_steps(Step* steps, int* n, const LoraView& 
 
 struct ShrinkArgs {
     LoraView lora[2];
-    uint16_t* vhi[2];      // [T][R] v as two bf16 planes (prompts), or
+    uint16_t* vhi[2];      // [parts][T][R] v over the parts of K, as two bf16 planes (prompts), or
     uint16_t* vlo[2];
-    float* vpart[2];       // [parts][T][R] its sums over the parts of K
+    float* vpart[2];       // in fp32, with
+    Step* steps[2];        // the steps of 32 ranks of each tile of 32 tokens [tiles][kMaxSteps / 2]
+    int* n_steps[2];       // and their number
     const int32_t* adapter;
     const uint16_t* xhi;
     const uint16_t* xlo;   // second plane of x (PL = 2)
@@ -86,16 +88,17 @@ constexpr int kSpan = 64;             // tokens of a shrink workgroup, one per l
 
 // Workgroup (span of 64 tokens, stride over the span's adapters, projection,
 // 16 ranks and part of K): v for every token of the adapter, gathered from the
-// span as columns; the waves split the part.  Both operands are row-major: of 128 K a lane
-// takes 32 consecutive ones, so the four lanes of a row use its 256 bytes.
+// span as columns; the waves split the part.  The later adapters of a span go
+// first: most spans of a prompt have one adapter, so those workgroups mostly
+// end at once, and the others' work should not start behind it.
 template <int PL, int NX>
 __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(ShrinkArgs s) {
     extern __shared__ __attribute__((aligned(16))) float red[];
     __shared__ uint8_t cols[kWaves][kSpan];         // (a copy per wave: no barrier)
     constexpr int CW = NX * kCols;                  // columns of a pass
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-    const int t0 = blockIdx.x * kSpan;
-    const int part = blockIdx.z % s.parts, pp = blockIdx.z / s.parts;
+    const int t0 = blockIdx.x * kSpan, stride = gridDim.z, first = stride - 1 - (int)blockIdx.z;
+    const int part = blockIdx.y % s.parts, pp = blockIdx.y / s.parts;
     const int proj = pp / s.panels, r0 = (pp - proj * s.panels) * 16;
     const LoraView lo = s.lora[proj];
     const int R = lo.max_rank;
@@ -110,13 +113,19 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(ShrinkArgs s) 
     const int units = s.K / kUnit;
     const int me = part * kWaves + wid, all = s.parts * kWaves;
     const int u0 = me * units / all, u1 = (me + 1) * units / all;
+    if (s.steps[proj] && first == 0 && r0 == 0 && part == 0 && wid < kSpan / kTile) {
+        const int tile = t0 / kTile + wid;
+        if (tile * kTile < s.T)
+            list_steps<32>(s.steps[proj] + (int64_t)tile * (kMaxSteps / 2), s.n_steps[proj] + tile, lo,
+                           __shfl(id, wid * kTile + (lane & (kTile - 1)), 64), lane);
+    }
     uint64_t left = __ballot(id >= 0);
     for (int i = 0; left; ++i) {
         const int src = __builtin_ctzll(left);
         const int a = __builtin_amdgcn_readlane(id, src);
         const uint64_t hit = __ballot(id == a);
         left &= ~hit;
-        if (i % (int)gridDim.y != (int)blockIdx.y) continue;
+        if (i % stride != first) continue;
         const int rank = __builtin_amdgcn_readlane(ranks, src);
         if (r0 >= rank) continue;         // the expand reads v in steps of 16 up to the rank
         const float scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scales), src));
@@ -136,12 +145,12 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(ShrinkArgs s) 
             pipelined<2>(
                 u1 - u0,
                 [&](int b, int u) {
-                    load_x<FT_FMT_MXFP4_B32>(au[b], arow, u0 + u, lane);
+                    load_x<FT_FMT_BF16>(au[b], arow, u0 + u, lane);
 #pragma unroll
                     for (int q = 0; q < NX; ++q)
                         if (q == 0 || q * kCols < n) {
-                            load_x<FT_FMT_MXFP4_B32>(x[b][q][0], s.xhi + xo[q], u0 + u, lane);
-                            if constexpr (PL == 2) load_x<FT_FMT_MXFP4_B32>(x[b][q][PL - 1], s.xlo + xo[q], u0 + u, lane);
+                            load_x<FT_FMT_BF16>(x[b][q][0], s.xhi + xo[q], u0 + u, lane);
+                            if constexpr (PL == 2) load_x<FT_FMT_BF16>(x[b][q][PL - 1], s.xlo + xo[q], u0 + u, lane);
                         }
                 },
                 [&](int b, int) {
@@ -154,18 +163,19 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(ShrinkArgs s) 
                                 for (int p = 0; p < PL; ++p)
                                     acc[q] = mma(__builtin_bit_cast(bf16x8_t, au[b].v[v]), x[b][q][p].v[v], acc[q]);
                 });
+            constexpr int RR = 20;                   // floats of a column's ranks in LDS, padded
             __syncthreads();
 #pragma unroll
             for (int q = 0; q < NX; ++q) {
                 const int m = q * kCols + (lane & 15);
-                if (m < n) *reinterpret_cast<f32x4_t*>(red + (wid * n + m) * 20 + 4 * (lane >> 4)) = acc[q];
+                if (m < n) *reinterpret_cast<f32x4_t*>(red + (wid * n + m) * RR + 4 * (lane >> 4)) = acc[q];
             }
             __syncthreads();
             for (int q = tid; q < n * 16; q += kThreads) {
-                const int m = q >> 4, r = r0 + (q & 15);
+                const int m = q >> 4, k = q & 15, r = r0 + k;
                 float v = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kWaves; ++w) v += red[(w * n + m) * 20 + (q & 15)];
+                for (int w = 0; w < kWaves; ++w) v += red[(w * n + m) * RR + k];
                 v = r < rank ? scale * v : 0.0f;
                 const int64_t o = (int64_t)(t0 + cols[wid][c0 + m]) * R + r;
                 if (s.vpart[proj]) {
@@ -173,8 +183,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(ShrinkArgs s) 
                 } else {
                     uint16_t h, l;
                     split_bf16(v, h, l);              // 16 significant bits
-                    s.vhi[proj][o] = h;
-                    s.vlo[proj][o] = l;
+                    const int64_t at = (int64_t)part * s.T * R + o;
+                    s.vhi[proj][at] = h;
+                    s.vlo[proj][at] = l;
                 }
             }
         }
@@ -187,7 +198,9 @@ struct ProjectArgs {
     const uint8_t* codes[2];
     const uint8_t* scales[2];
     LoraView lora[2];          // count 0: no adapters
-    const float* v[2];         // v of the shrink launch [vparts][T][R] (null: computed here)
+    const float* v[2];         // of the shrink launch: v [vparts][T][R],
+    const Step* steps[2];      // and each tile's steps of 32 ranks (unless FUSED)
+    const int* n_steps[2];
     int vparts;
     const int32_t* adapter;
     const uint16_t* xhi;
@@ -221,12 +234,15 @@ __device__ __forceinline__ void stage_v(uint16_t* vs, const float* v, int vparts
     for (int i = tid; i < nt * (R / 4); i += kThreads) {
         const int m = i / (R / 4), k = (i - m * (R / 4)) * 4;
         const float* src = v + (int64_t)(t0 + m) * R + k;
-        f32x4_t z = *reinterpret_cast<const f32x4_t*>(src);
-        for (int j = 1; j < vparts; ++j) {
-            const f32x4_t o = *reinterpret_cast<const f32x4_t*>(src + j * plane);
+        f32x4_t part[kMaxParts], z = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] += o[e];
-        }
+        for (int j = 0; j < kMaxParts; ++j)
+            if (j < vparts) part[j] = *reinterpret_cast<const f32x4_t*>(src + j * plane);
+#pragma unroll
+        for (int j = 0; j < kMaxParts; ++j)
+            if (j < vparts)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[e] += part[j][e];
         uint16_t h[4], l[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split_bf16(z[e], h[e], l[e]);
@@ -284,67 +300,55 @@ __device__ __forceinline__ void expand(Acc (&acc)[NX], const BStep& bs, const St
 }
 
 // The adapters without a launch of their own: v B_a^T is linear in v and v in
-// the parts of K, so a wave takes v over its own units of K, 16 ranks at a
-// time, and multiplies it by B at once; the sums of the waves and workgroups
-// are those of the projection itself.  The 16 x 16 sums of x A_a^T (rows: ranks,
-// columns: tokens) are the B operand of the 16 x 16 x 16 product as they
-// stand.
+// the parts of K, so the pairs (16 ranks, unit of K) of a tile go round the
+// waves, which multiply their part of v by B at once; the sums of the waves
+// and workgroups are those of the projection itself.  The 16 x 16 sums of
+// x A_a^T (rows: ranks, columns: tokens) are the B operand of the 16 x 16 x 16
+// product as they stand.
 template <int PL, int NX>
 __device__ __forceinline__ void adapt(Acc (&acc)[NX], const LoraView& lo, const uint16_t* xhi, const uint16_t* xlo, int K,
-                                      int n, int p, const Step* steps, int ns, int u0, int u1, const int (&col)[NX],
+                                      int n, int p, const Step* steps, int ns, int me, int parts, const int (&col)[NX],
                                       const int (&t)[NX], int lane) {
     typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
     typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
     typedef short s16x4_t __attribute__((ext_vector_type(4)));
-    const int nu = u1 - u0, R = lo.max_rank, g = lane >> 4;
-    f32x4_t v[NX];
-#pragma unroll
-    for (int x = 0; x < NX; ++x) v[x] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const int units = K / kUnit, R = lo.max_rank, g = lane >> 4;
+    const int pairs = ns * units, mine = pairs > me ? (pairs - me - 1) / parts + 1 : 0;
     constexpr int D = NX * PL == 1 ? 4 : NX == 1 ? 3 : 2;
     XUnit au[D], xu[D][NX][PL];
     u32x2_t b[D][2];
-    int ls = 0, lu = 0, ws = 0, wu = 0;         // (step, unit) of the next load and of the work
     pipelined<D>(
-        ns * nu,
-        [&](int q, int) {
-            const Step st = steps[ls];
-            load_x<FT_FMT_MXFP4_B32>(au[q], lo.a + ((int64_t)st.a * R + min(st.r0 + (lane & 15), st.rank - 1)) * K, u0 + lu,
-                                     lane);
+        mine,
+        [&](int q, int i) {
+            const int j = me + i * parts, u = j % units;
+            const Step st = steps[j / units];
+            load_x<FT_FMT_BF16>(au[q], lo.a + ((int64_t)st.a * R + min(st.r0 + (lane & 15), st.rank - 1)) * K, u, lane);
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
-                load_x<FT_FMT_MXFP4_B32>(xu[q][x][0], xhi + (int64_t)t[x] * K, u0 + lu, lane);
-                if constexpr (PL == 2) load_x<FT_FMT_MXFP4_B32>(xu[q][x][PL - 1], xlo + (int64_t)t[x] * K, u0 + lu, lane);
+                load_x<FT_FMT_BF16>(xu[q][x][0], xhi + (int64_t)t[x] * K, u, lane);
+                if constexpr (PL == 2) load_x<FT_FMT_BF16>(xu[q][x][PL - 1], xlo + (int64_t)t[x] * K, u, lane);
             }
-            if (++lu == nu) {
-                const uint16_t* row = lo.b + ((int64_t)st.a * n + p * 32 + (lane & 15)) * R + st.r0 + 4 * g;
-                b[q][0] = *reinterpret_cast<const u32x2_t*>(row);
-                b[q][1] = *reinterpret_cast<const u32x2_t*>(row + 16 * R);
-                lu = 0;
-                ++ls;
-            }
+            const uint16_t* row = lo.b + ((int64_t)st.a * n + p * 32 + (lane & 15)) * R + st.r0 + 4 * g;
+            b[q][0] = *reinterpret_cast<const u32x2_t*>(row);
+            b[q][1] = *reinterpret_cast<const u32x2_t*>(row + 16 * R);
         },
-        [&](int q, int) {
-            const Step st = steps[ws];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int x = 0; x < NX; ++x)
-#pragma unroll
-                    for (int pl = 0; pl < PL; ++pl)
-                        v[x] = mma(__builtin_bit_cast(bf16x8_t, au[q].v[e]), xu[q][x][pl].v[e], v[x]);
-            if (++wu < nu) return;
-            wu = 0;
-            ++ws;
+        [&](int q, int i) {
+            const Step st = steps[(me + i * parts) / units];
             const int left = st.rank - st.r0 - 4 * g;      // ranks of this lane's four that exist
             u32x2_t w[2] = {b[q][0], b[q][1]};
             keep_ranks(w[0], left);
             keep_ranks(w[1], left);
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
+                f32x4_t v = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int pl = 0; pl < PL; ++pl) v = mma(__builtin_bit_cast(bf16x8_t, au[q].v[e]), xu[q][x][pl].v[e], v);
                 // v in 16 significant bits; zero past the adapter's rank
                 f32x4_t z, r;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z[e] = e < left ? st.scale * v[x][e] : 0.0f;
+                for (int e = 0; e < 4; ++e) z[e] = e < left ? st.scale * v[e] : 0.0f;
                 const bf16x4_t h = __builtin_convertvector(z, bf16x4_t);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -359,16 +363,15 @@ __device__ __forceinline__ void adapt(Acc (&acc)[NX], const LoraView& lo, const 
                     s = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(bw, __builtin_bit_cast(s16x4_t, h), s, 0, 0, 0);
                     s = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(bw, __builtin_bit_cast(s16x4_t, l), s, 0, 0, 0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[x].h[e][i] = col[x] == st.a ? acc[x].h[e][i] + s[i] : acc[x].h[e][i];
+                    for (int c = 0; c < 4; ++c) acc[x].h[e][c] = col[x] == st.a ? acc[x].h[e][c] + s[c] : acc[x].h[e][c];
                 }
-                v[x] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
             }
         });
 }
 
 // Workgroups of a row panel and tile of 32 tokens: `splits` that stream the
 // panel, their waves dividing K.  The adapters, FUSED: lsplits workgroups more
-// per matrix take them, dividing K as well; they run beside the stream, not in
+// per matrix take them; they run beside the stream, not in
 // its way (listing a tile's adapters and following their addresses takes
 // several dependent loads).  Otherwise the streaming waves divide the steps of
 // 32 ranks, the first of them loaded before the stream is multiplied.  Sums in
@@ -418,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a
             for (int m = 0; m < NM; ++m) mma_unit<FMT, NX, PL>(acc[m], w[b][m], x[b], nx);
         };
         if (nu > 0) load(0, 0);
+        if (nu > 1) load(1, 1);
         uint16_t* vs[NM];
         int col[NM][NX], mine[NM];       // the columns' adapters; the wave's steps
         BStep first[NM];
@@ -431,7 +435,8 @@ __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a
                 if (lo.count == 0) continue;
                 at += 2 * kTile * v_row(lo.max_rank);
                 const int id = tile_adapter<kTile>(a.adapter, t0, a.T, lo.count, lane);
-                if (wid == m) list_steps<32>(steps[m], &n_steps[m], lo, id, lane);
+                if (tid < kMaxSteps / 2) steps[m][tid] = a.steps[m][(int64_t)blockIdx.z * (kMaxSteps / 2) + tid];
+                if (tid == 0) n_steps[m] = a.n_steps[m][blockIdx.z];
                 stage_v(vs[m], a.v[m], a.vparts, a.T, lo.max_rank, t0, nt, tid);
 #pragma unroll
                 for (int i = 0; i < NX; ++i) col[m][i] = __shfl(id, i * kCols + (lane & 15), 64);
@@ -448,11 +453,11 @@ __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a
             }
         }
         for (int u = 0; u < nu; u += 2) {
-            if (u + 1 < nu) load(1, u + 1);
             work(0);
+            if (u + 2 < nu) load(0, u + 2);
             if (u + 1 < nu) {
-                if (u + 2 < nu) load(0, u + 2);
                 work(1);
+                if (u + 3 < nu) load(1, u + 3);
             }
         }
         if constexpr (!FUSED) {
@@ -483,8 +488,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a
         Acc la[NX];
 #pragma unroll
         for (int i = 0; i < NX; ++i) la[i] = zero_acc();
-        adapt<PL, NX>(la, lo, a.xhi, a.xlo, a.K, a.n, p, steps[0], n_steps[0], me * units / parts, (me + 1) * units / parts,
-                      col, t, lane);
+        adapt<PL, NX>(la, lo, a.xhi, a.xlo, a.K, a.n, p, steps[0], n_steps[0], me, parts, col, t, lane);
 #pragma unroll
         for (int i = 0; i < NX; ++i) acc[0][i] = la[i];
     }
@@ -582,12 +586,13 @@ Split split_of(int nm, int n, int K, int T, int adapters, int rank) {
     s.fused = T <= kTile && steps <= kMaxFusedSteps && panels * steps * 32 * K <= (24ll << 20) && per >= 1 + nm;
     if (s.fused) {
         if (s.splits > per - nm) s.splits = (int)(per - nm);
+        const int64_t pairs = steps * units, need = (pairs + kWaves - 1) / kWaves;
         int64_t l = (per - s.splits) / nm;
-        l = l > most ? most : l;
+        l = l > need ? need : l;
         s.lsplits = l < 1 ? 1 : l > 4 ? 4 : (int)l;
     } else {
         const int64_t spans = (T + kSpan - 1) / kSpan;
-        int64_t parts = 256 / (spans * adapters * (rank / 16));
+        int64_t parts = 256 / (spans * adapters * (rank / 16) * nm);
         parts = parts > most ? most : parts;
         s.vparts = parts < 1 ? 1 : parts > kMaxParts ? kMaxParts : (int)parts;
     }
@@ -616,7 +621,7 @@ hipError_t launch_shrink(const ShrinkArgs& s, int projections, hipStream_t st) {
     int gy = most < kTile ? most : kTile;
     if (gy > s.T) gy = s.T;
     if (spans >= 16 && gy > 2) gy = 2;
-    const dim3 grid(spans, gy, projections * s.panels * s.parts);
+    const dim3 grid(spans, projections * s.panels * s.parts, gy);
     const int cols = s.xlo ? 2 * kCols : 4 * kCols;
     const size_t lds = (size_t)kWaves * (s.T < cols ? s.T : cols) * 20 * sizeof(float);
     if (s.xlo) hipLaunchKernelGGL((lora_shrink_kernel<2, 2>), grid, dim3(kThreads), lds, st, s);
@@ -633,12 +638,18 @@ void launch_project_nx(const ProjectArgs& a, hipStream_t st) {
         hipLaunchKernelGGL((lora_project_kernel<FMT, NM, PL, 2, FUSED>), grid, dim3(kThreads), lds_bytes<FUSED>(a), st, a);
 }
 
-// Prompts: from this many tokens on the 128-row GEMM tiles are faster than
-// streaming the weights once per 32 tokens.  They reach rows by 32-bit
-// offsets and move outputs in 16-byte pieces; other calls stream.
-constexpr int kGemmTokens = 256;
-bool gemm_fits(int T, int K, const void* y, const void* base) {
-    return T >= kGemmTokens && (int64_t)T * K * 2 < (1ll << 32) && (reinterpret_cast<uintptr_t>(y) & 15) == 0 &&
+// Prompts go through the GEMM tiles (gemm.hip).  A GEMM workgroup's time is that
+// of its K at the rate of one compute unit, however few there are (21 us for
+// K = 2,048 in bf16, 40 for 4,096 in fp8); streaming takes rounds of 256
+// workgroups of 8 to 16 us.  `rounds` and `most` were set where the two met: a
+// projection of 384 tokens takes 26 us either way at [768 x 2,048] (2 rounds),
+// 45 and 44 at [2,048 x 4,096] fp8 (3 rounds); an expert 47 and 46 at 256 tokens
+// (d = 2,048, f = 768: 3 rounds), 90 and 76 at 192 (fp8, 4,096 and 2,048: 5).
+// Up to 64 tokens always stream.  The tiles reach rows by 32-bit offsets and
+// move outputs in 16-byte pieces; other calls stream as well.
+int64_t stream_rounds(int n, int T) { return ((int64_t)(n / 32) * ((T + kTile - 1) / kTile) + 255) / 256; }
+bool gemm_fits(int T, int64_t rounds, int64_t most, int K, const void* y, const void* base) {
+    return T > 64 && rounds > most && (int64_t)T * K * 2 < (1ll << 32) && (reinterpret_cast<uintptr_t>(y) & 15) == 0 &&
            (reinterpret_cast<uintptr_t>(base) & 15) == 0;
 }
 
@@ -660,9 +671,15 @@ hipError_t launch_project(int fmt, const ProjectArgs& a, bool fuse, hipStream_t 
 int pool_adapters(const LoraView* l) { return l && l->count > 0 ? l->count : 0; }
 int pool_rank(const LoraView* l) { return l && l->count > 0 ? l->max_rank : 0; }
 
-// v of one projection: bf16 planes [T][R] for the GEMM, else fp32 parts
+// v of one projection over the parts of K: bf16 planes for the GEMM, else fp32
+size_t rank_tiles(int T) { return ((size_t)T + kTile - 1) / kTile; }
+// and the tiles' steps
+size_t list_bytes(int T) {
+    return rank_tiles(T) * (kMaxSteps / 2) * sizeof(Step) + align256(rank_tiles(T) * sizeof(int));
+}
 size_t v_bytes(int T, int rank, int parts) {
-    const size_t two = 2 * align256((size_t)T * rank * 2), f32 = align256((size_t)parts * T * rank * sizeof(float));
+    if (rank == 0) return 0;
+    const size_t two = 2 * align256((size_t)parts * T * rank * 2), f32 = align256((size_t)parts * T * rank * sizeof(float)) + list_bytes(T);
     return two > f32 ? two : f32;
 }
 
@@ -740,9 +757,12 @@ hipError_t shrink(const LoraView* const* pools, uint8_t* const* v, int n, const 
         s.lora[m] = *pools[i];
         if (planes) {
             s.vhi[m] = reinterpret_cast<uint16_t*>(v[i]);
-            s.vlo[m] = reinterpret_cast<uint16_t*>(v[i] + align256((size_t)T * pools[i]->max_rank * 2));
+            s.vlo[m] = reinterpret_cast<uint16_t*>(v[i] + align256((size_t)kMaxParts * T * pools[i]->max_rank * 2));
         } else {
             s.vpart[m] = reinterpret_cast<float*>(v[i]);
+            uint8_t* list = v[i] + align256((size_t)kMaxParts * T * pools[i]->max_rank * sizeof(float));
+            s.steps[m] = reinterpret_cast<Step*>(list);
+            s.n_steps[m] = reinterpret_cast<int*>(list + rank_tiles(T) * (kMaxSteps / 2) * sizeof(Step));
         }
         s.panels = pools[i]->max_rank / 16 > s.panels ? pools[i]->max_rank / 16 : s.panels;
         ++m;
@@ -750,12 +770,25 @@ hipError_t shrink(const LoraView* const* pools, uint8_t* const* v, int n, const 
     return m > 0 ? launch_shrink(s, m, st) : hipSuccess;
 }
 
-// The pools, planes and adapters of a GEMM's NM matrices
-void gemm_pools(LoraGemmArgs& g, const LoraView* const* pools, uint8_t* const* v, int n) {
+// The parts of K of a GEMM's shrink launch over K: a workgroup per compute unit
+// when a span of tokens names one adapter.
+int gemm_parts(const LoraView* const* pools, int n, int K, int T) {
+    int64_t wgs = 0;
+    for (int i = 0; i < n; ++i) wgs += pool_rank(pools[i]) / 16;
+    wgs *= (T + kSpan - 1) / kSpan;
+    int64_t p = wgs > 0 ? 256 / wgs : 1;
+    const int most = K / kUnit / kWaves;
+    p = p > most ? most : p;
+    return p < 1 ? 1 : p > kMaxParts ? kMaxParts : (int)p;
+}
+
+// The pools, planes and adapters of a GEMM's matrices
+void gemm_pools(LoraGemmArgs& g, const LoraView* const* pools, uint8_t* const* v, int n, int parts) {
+    g.vparts = parts;
     for (int i = 0; i < n; ++i) {
         g.lora[i] = pool_adapters(pools[i]) > 0 ? *pools[i] : LoraView();
         g.vhi[i] = reinterpret_cast<const uint16_t*>(v[i]);
-        g.vlo[i] = reinterpret_cast<const uint16_t*>(v[i] + align256((size_t)g.T * g.lora[i].max_rank * 2));
+        g.vlo[i] = reinterpret_cast<const uint16_t*>(v[i] + align256((size_t)kMaxParts * g.T * g.lora[i].max_rank * 2));
     }
 }
 
@@ -769,6 +802,9 @@ hipError_t product(int fmt, ProjectArgs& a, const LoraView* const* pools, uint8_
         if (pool_rank(pools[i]) > rank) rank = pool_rank(pools[i]);
         if (pool_adapters(pools[i]) > 0) a.lora[i] = *pools[i];
         a.v[i] = reinterpret_cast<const float*>(v[i]);
+        const uint8_t* list = v[i] + align256((size_t)kMaxParts * a.T * pool_rank(pools[i]) * sizeof(float));
+        a.steps[i] = reinterpret_cast<const Step*>(list);
+        a.n_steps[i] = reinterpret_cast<const int*>(list + rank_tiles(a.T) * (kMaxSteps / 2) * sizeof(Step));
     }
     const Split s = split_of(NM, a.n, a.K, a.T, adapters, rank);
     a.splits = s.splits;
@@ -788,7 +824,7 @@ hipError_t launch_lora_project(const MatrixView& m, const LoraView* lora, const 
     uint8_t* mem = ws->mem + kCounterBytes;
     const LoraView* pools[1] = {lora};
     uint8_t* v[1] = {mem};
-    if (gemm_fits(T, m.K, y, base)) {
+    if (gemm_fits(T, stream_rounds(m.n, T), 2, m.K, y, base)) {
         LoraGemmArgs g = {};
         g.Hin = x;
         g.Y = y;
@@ -800,8 +836,9 @@ hipError_t launch_lora_project(const MatrixView& m, const LoraView* lora, const 
         g.scales[0] = m.scales;
         g.adapter = adapter;
         g.base = base;
-        gemm_pools(g, pools, v, 1);
-        const hipError_t e = shrink(pools, v, 1, adapter, x, nullptr, T, m.K, true, 1, st);
+        const int parts = gemm_parts(pools, 1, m.K, T);
+        gemm_pools(g, pools, v, 1, parts);
+        const hipError_t e = shrink(pools, v, 1, adapter, x, nullptr, T, m.K, true, parts, st);
         return e != hipSuccess ? e : launch_lora_gemm(m.fmt, false, g, st);
     }
     ProjectArgs a = {};
@@ -831,7 +868,8 @@ hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const 
     uint16_t* hhi = reinterpret_cast<uint16_t*>(mem + b.h);
     uint16_t* hlo = reinterpret_cast<uint16_t*>(mem + b.h + align256((size_t)T * sh.d_ff * 2));
     hipError_t e;
-    if (gemm_fits(T, sh.d_model > sh.d_ff ? sh.d_model : sh.d_ff, y, base)) {
+    if (gemm_fits(T, stream_rounds(sh.d_ff, T) + stream_rounds(sh.d_model, T), 3,
+                  sh.d_model > sh.d_ff ? sh.d_model : sh.d_ff, y, base)) {
         LoraGemmArgs g = {};
         g.x = x;
         g.Hin = g.Hout = hhi;
@@ -846,14 +884,15 @@ hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const 
         g.scales[0] = rec + rl.off_sg;
         g.scales[1] = rec + rl.off_su;
         g.adapter = adapter;
-        gemm_pools(g, pools, v, 2);
-        if ((e = shrink(pools, v, 2, adapter, x, nullptr, T, sh.d_model, true, 1, st)) != hipSuccess) return e;
+        const int gp = gemm_parts(pools, 2, sh.d_model, T), dp = gemm_parts(pools + 2, 1, sh.d_ff, T);
+        gemm_pools(g, pools, v, 2, gp);
+        if ((e = shrink(pools, v, 2, adapter, x, nullptr, T, sh.d_model, true, gp, st)) != hipSuccess) return e;
         if ((e = launch_lora_gemm(sh.fmt, true, g, st)) != hipSuccess) return e;
         g.codes[0] = rec + rl.off_down;
         g.scales[0] = rec + rl.off_sd;
         g.base = base;
-        gemm_pools(g, pools + 2, v + 2, 1);
-        if ((e = shrink(pools + 2, v + 2, 1, adapter, hhi, nullptr, T, sh.d_ff, true, 1, st)) != hipSuccess) return e;
+        gemm_pools(g, pools + 2, v + 2, 1, dp);
+        if ((e = shrink(pools + 2, v + 2, 1, adapter, hhi, nullptr, T, sh.d_ff, true, dp, st)) != hipSuccess) return e;
         return launch_lora_gemm(sh.fmt, false, g, st);
     }
     ProjectArgs a = {};

@@ -69,8 +69,9 @@ struct LoraGemmArgs {
     const uint8_t* codes[2];
     const uint8_t* scales[2];
     LoraView lora[2];
-    const uint16_t* vhi[2];
+    const uint16_t* vhi[2];            // [vparts][T][R] v over parts of K, two bf16 planes
     const uint16_t* vlo[2];
+    int vparts;
     const int32_t* adapter;
     const uint16_t* base;
 };
