@@ -639,8 +639,8 @@ void launch_project_nx(const ProjectArgs& a, hipStream_t st) {
 }
 
 // Prompts go through the GEMM tiles (gemm.hip).  A GEMM workgroup's time is that
-// of its K at the rate of one compute unit, however few there are (21 us for
-// K = 2,048 in bf16, 40 for 4,096 in fp8); streaming takes rounds of 256
+// of its K at the rate of one compute unit, however few there are (18 us for
+// K = 2,048 in bf16, 37 for 4,096 in fp8); streaming takes rounds of 256
 // workgroups of 8 to 16 us.  `rounds` and `most` were set where the two met: a
 // projection of 384 tokens takes 26 us either way at [768 x 2,048] (2 rounds),
 // 45 and 44 at [2,048 x 4,096] fp8 (3 rounds); an expert 47 and 46 at 256 tokens

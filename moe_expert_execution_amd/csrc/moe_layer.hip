@@ -140,8 +140,10 @@ __device__ __forceinline__ void select_experts(const double* z, int E, int k, in
 // lane group g = l / 16 takes rows 8 g .. 8 g + 7, so MFMA step s contracts
 // rows 8 g + s; column c = l % 16 of tile n is expert 4 c + n, so one 8-byte
 // load gives a lane its four tiles' weights of a row, and one 16-byte load its
-// token's 8 activations.  The waves' sums are added in order, the group's
-// last workgroup adds the slices in order and selects, one wave per token.
+// token's 8 activations.  The waves' sums are added in order, and the group's
+// last workgroup adds the slices in order and selects, one wave per token
+// (a single token's slices are added by the experts' launch: sending them on is
+// quicker than waiting for them here).
 __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
     extern __shared__ __attribute__((aligned(16))) double zred[];
     __shared__ uint32_t flag;
@@ -210,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
         for (int w = 0; w < kWaves; ++w) s += zred[w * nt * kRouteExperts + i];
         if (e < a.E) put_agent(a.part + ((int64_t)slice * a.T + t0 + t) * a.E + e, s);
     }
+    if (a.T == 1) return;                 // the experts' launch selects
     if (!last_arrival(a.counters + blockIdx.z, a.slices * gridDim.y, &flag)) return;
 
     const int n = nt * a.E;
@@ -238,11 +241,13 @@ constexpr int kMaxRoutes = kMaxLayerTokens * kMaxTopK;       // 1024
 constexpr int kMaxTiles = kMaxRouteExperts + kMaxRoutes / (kTile + 1);
 
 struct ExpertArgs {
+    const double* logits;  // [slices][E] of a single token (ONE)
+    int slices;
     const uint16_t* x;
     const uint8_t* rec;
     int64_t stride, off_gate, off_up, off_down, off_sg, off_su, off_sd;
-    const int32_t* ids;
-    const float* w;
+    int32_t* ids;          // (written by the ONE launch)
+    float* w;
     const uint16_t* base;
     uint16_t* y;
     uint16_t* hhi;         // [T k][f] h as two bf16 planes
@@ -278,15 +283,6 @@ struct Groups {
 __device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int T, int E, int k) {
     constexpr int PT = kMaxRoutes / kThreads;
     const int tid = threadIdx.x, lane = tid & 63, R = T * k;
-    if (T == 1) {                         // a tile per route
-        if (tid < k) {
-            g.tile[tid] = (uint32_t)ids[tid] | ((uint32_t)tid << 8) | (1u << 18);
-            g.route[tid] = (uint16_t)tid;
-        }
-        if (tid == 0) g.n_tiles = k;
-        __syncthreads();
-        return;
-    }
     for (int e = tid; e < E; e += kThreads) g.mask[e] = 0;
     __syncthreads();
     int id[PT], tok[PT];
@@ -333,6 +329,41 @@ __device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int 
     for (int i = 0; i < PT; ++i) {
         const int r = tid + i * kThreads;
         if (r < R) g.route[g.start[id[i]] + __popcll(g.mask[id[i]] & ((1ull << tok[i]) - 1))] = (uint16_t)r;
+    }
+    __syncthreads();
+}
+
+// A single token: adds its logits' slices, selects, and makes a tile of each
+// route; workgroup 0 writes the outputs.  Every thread of the workgroup calls
+// it; `z` is scratch for E logits.
+__device__ __forceinline__ void select_one(Groups& g, float* wr, double* z, const ExpertArgs& a) {
+    __shared__ int32_t ids[kMaxTopK];
+    const int tid = threadIdx.x, lane = tid & 63;
+    if (tid < a.E) {
+        double s = 0.0;
+        for (int q = 0; q < a.slices; q += 16) {
+            double v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = a.logits[(int64_t)(q + i < a.slices ? q + i : q) * a.E + tid];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s += q + i < a.slices ? v[i] : 0.0;
+        }
+        z[tid] = s;
+    }
+    __syncthreads();
+    if (tid < 64) {
+        if (a.E <= 64) select_experts<1>(z, a.E, a.k, lane, ids, wr);
+        else if (a.E <= 128) select_experts<2>(z, a.E, a.k, lane, ids, wr);
+        else select_experts<4>(z, a.E, a.k, lane, ids, wr);
+        if (lane < a.k) {
+            g.tile[lane] = (uint32_t)ids[lane] | ((uint32_t)lane << 8) | (1u << 18);
+            g.route[lane] = (uint16_t)lane;
+            if (blockIdx.x == 0) {
+                a.ids[lane] = ids[lane];
+                a.w[lane] = wr[lane];
+            }
+        }
+        if (lane == 0) g.n_tiles = a.k;
     }
     __syncthreads();
 }
@@ -690,7 +721,8 @@ __device__ __forceinline__ void layer_down(const ExpertArgs& a, const Groups& g,
 // between gate/up and down costs 2.4 us and empties the card twice; here a
 // workgroup without gate/up work, or done with it, has its down weights under
 // way while it waits.
-template <int FMT, int NP>
+// ONE: a single token, selected here.
+template <int FMT, int NP, bool ONE>
 __global__ void __launch_bounds__(kThreads, 2) layer_experts_kernel(ExpertArgs a) {
     extern __shared__ __attribute__((aligned(16))) float red[];     // the waves' sums of either half
     __shared__ Groups g;
@@ -704,8 +736,12 @@ __global__ void __launch_bounds__(kThreads, 2) layer_experts_kernel(ExpertArgs a
         const uint32_t v = draw(a.hand, shard);
         number = v < shard_size(shard, grid) ? (int)v * kShards + shard : -1;
     }
-    for (int r = tid; r < a.T * a.k; r += kThreads) wr[r] = a.w[r];
-    group_routes(g, a.ids, a.T, a.E, a.k);
+    if constexpr (ONE) {
+        select_one(g, wr, reinterpret_cast<double*>(red), a);
+    } else {
+        for (int r = tid; r < a.T * a.k; r += kThreads) wr[r] = a.w[r];
+        group_routes(g, a.ids, a.T, a.E, a.k);
+    }
     const int mine = number;
     if (mine >= 0) {
         layer_gateup<FMT, 1>(a, g, red, mine);
@@ -829,10 +865,15 @@ hipError_t launch_fmt(const ft_shape& s, const RouteArgs& r, const ExpertArgs& a
     if (a.T <= kCols) {                   // every tile fits one operand
         const dim3 grid = blocks(items > ditems ? items : ditems);
         const size_t lds = glds > dlds ? glds : dlds;
-        if (FMT == FT_FMT_MXFP4_B32 && np == 2)
-            hipLaunchKernelGGL((layer_experts_kernel<FMT, FMT == FT_FMT_MXFP4_B32 ? 2 : 1>), grid, dim3(kThreads), lds, st, a);
-        else
-            hipLaunchKernelGGL((layer_experts_kernel<FMT, 1>), grid, dim3(kThreads), lds, st, a);
+        if (a.T == 1) {
+            const size_t z = kMaxRouteExperts * sizeof(double);
+            hipLaunchKernelGGL((layer_experts_kernel<FMT, 1, true>), grid, dim3(kThreads), lds > z ? lds : z, st, a);
+        } else if (FMT == FT_FMT_MXFP4_B32 && np == 2) {
+            hipLaunchKernelGGL((layer_experts_kernel<FMT, FMT == FT_FMT_MXFP4_B32 ? 2 : 1, false>), grid, dim3(kThreads), lds,
+                               st, a);
+        } else {
+            hipLaunchKernelGGL((layer_experts_kernel<FMT, 1, false>), grid, dim3(kThreads), lds, st, a);
+        }
         return hipGetLastError();
     }
     hipLaunchKernelGGL(layer_gateup_kernel<FMT>, blocks(items), dim3(kThreads), glds, st, a);
@@ -891,6 +932,8 @@ hipError_t launch_layer(const ft_shape& s, const LayerArgs& la, ft_workspace* ws
     a.off_sd = la.rl.off_sd;
     a.ids = la.ids;
     a.w = la.w;
+    a.logits = r.part;
+    a.slices = r.slices;
     a.base = la.base;
     a.y = la.y;
     a.hhi = reinterpret_cast<uint16_t*>(m + b.hhi);
