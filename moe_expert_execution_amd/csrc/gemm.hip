@@ -430,23 +430,26 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_kernel(Args a) {
         // Block-FP8 beside adapters: the codes are multiplied as they are (exact in
         // bf16) and the accumulators are kept in units of the current block's
         // scale, rescaled when the next 128 K begin; the grouped form rounds code
-        // times scale to bf16 instead.  A unit stays at 2^-90 or above, so that
-        // rescaling cannot overflow: smaller scales keep a factor 2^-36 in the
-        // codes (exact), and zero or subnormal ones leave the unit and put the
-        // codes below everything.
+        // times scale to bf16 instead.  A unit stays within 2^-61 of the largest
+        // scale so far, so that rescaling cannot overflow: a smaller scale keeps a
+        // factor 2^-m in the codes (exact).  Zero, subnormal and still smaller ones
+        // leave the unit and put the codes below 2^-117 of it.
         constexpr bool UNITS = LORA && FMT == FT_FMT_FP8_B128;
+        // (The first unit is small enough that all-zero scales give zero.)
         float unit[2] = {0x1p-90f, 0x1p-90f}, conv[2] = {1.0f, 1.0f};
+        uint32_t top[2] = {0u, 0u};
         auto begin_block = [&](const typename FR::SRaw (&bss)[2]) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float s = __uint_as_float(__builtin_amdgcn_readfirstlane((int)bss[i]));
-                const float mag = fabsf(s);
-                if (mag < 0x1p-126f) {
+                const uint32_t sb = (uint32_t)__builtin_amdgcn_readfirstlane((int)bss[i]), mag = sb & 0x7FFFFFFFu;
+                const int m = max((int)(top[i] >> 23) - (int)(mag >> 23) - 60, 0);
+                if (mag < 0x00800000u || m > 110) {
                     conv[i] = 0x1p-126f;
                     continue;
                 }
-                conv[i] = mag < 0x1p-90f ? 0x1p-36f : 1.0f;
-                const float u = mag < 0x1p-90f ? s * 0x1p36f : s;
+                top[i] = max(top[i], mag);
+                conv[i] = __uint_as_float((uint32_t)(127 - m) << 23);
+                const float u = __uint_as_float(sb) * __uint_as_float((uint32_t)(127 + m) << 23);
                 const float r = unit[i] / u;
                 unit[i] = u;
 #pragma unroll
