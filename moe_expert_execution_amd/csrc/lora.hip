@@ -81,43 +81,52 @@ struct ShrinkArgs {
     const uint16_t* xhi;
     const uint16_t* xlo;   // second plane of x (PL = 2)
     int T, K, panels;      // rank panels of 16 per projection
+    int slots;             // projections times panels
     int parts;             // parts of K
 };
 
-constexpr int kSpan = 64;             // tokens of a shrink workgroup, one per lane
-
-// Workgroup (span of 64 tokens, stride over the span's adapters, projection,
-// 16 ranks and part of K): v for every token of the adapter, gathered from the
-// span as columns; the waves split the part.  The later adapters of a span go
-// first: most spans of a prompt have one adapter, so those workgroups mostly
-// end at once, and the others' work should not start behind it.
-template <int PL, int NX>
+// Workgroup (span of SPAN tokens, stride over the span's adapters, S slots and
+// part of K), a slot being 16 ranks of a projection: v for every token of the
+// adapter, gathered from the span as columns that the slots share; the waves
+// split the part.  The later adapters of a span go first: most spans of a prompt
+// have one adapter, so those workgroups mostly end at once, and the others' work
+// should not start behind it.
+template <int PL, int NX, int SPAN, int S>
 __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(ShrinkArgs s) {
     extern __shared__ __attribute__((aligned(16))) float red[];
-    __shared__ uint8_t cols[kWaves][kSpan];         // (a copy per wave: no barrier)
+    __shared__ uint8_t cols[kWaves][SPAN];          // (a copy per wave: no barrier)
     constexpr int CW = NX * kCols;                  // columns of a pass
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-    const int t0 = blockIdx.x * kSpan, stride = gridDim.z, first = stride - 1 - (int)blockIdx.z;
-    const int part = blockIdx.y % s.parts, pp = blockIdx.y / s.parts;
-    const int proj = pp / s.panels, r0 = (pp - proj * s.panels) * 16;
-    const LoraView lo = s.lora[proj];
-    const int R = lo.max_rank;
-    if (r0 >= R) return;
-    const int id = tile_adapter<kSpan>(s.adapter, t0, s.T, lo.count, lane);
-    int ranks = 0;
-    float scales = 0.0f;
-    if (id >= 0) {
-        ranks = min(max(lo.rank[id], 0), R);
-        scales = lo.scale[id];
+    const int t0 = blockIdx.x * SPAN, stride = gridDim.z, first = stride - 1 - (int)blockIdx.z;
+    const int part = blockIdx.y % s.parts, slot0 = blockIdx.y / s.parts * S;
+    int proj[S], r0[S], ranks[S], id = -1;          // the lane's token's adapter, and its ranks in each slot's pool
+    float scales[S];
+    const int raw = lane < SPAN && t0 + lane < s.T ? s.adapter[t0 + lane] : -1;
+#pragma unroll
+    for (int m = 0; m < S; ++m) {
+        const int slot = slot0 + m, q = slot / s.panels;
+        const bool live = slot < s.slots && (slot - q * s.panels) * 16 < s.lora[min(q, 1)].max_rank;
+        proj[m] = live ? q : 0;
+        r0[m] = live ? (slot - q * s.panels) * 16 : kMaxRank;
+        const LoraView& lo = s.lora[proj[m]];
+        ranks[m] = 0;
+        scales[m] = 0.0f;
+        if (live && (uint32_t)raw < (uint32_t)lo.count) {
+            id = raw;
+            ranks[m] = min(max(lo.rank[raw], 0), lo.max_rank);
+            scales[m] = lo.scale[raw];
+        }
     }
     const int units = s.K / kUnit;
     const int me = part * kWaves + wid, all = s.parts * kWaves;
     const int u0 = me * units / all, u1 = (me + 1) * units / all;
-    if (s.steps[proj] && first == 0 && r0 == 0 && part == 0 && wid < kSpan / kTile) {
-        const int tile = t0 / kTile + wid;
-        if (tile * kTile < s.T)
-            list_steps<32>(s.steps[proj] + (int64_t)tile * (kMaxSteps / 2), s.n_steps[proj] + tile, lo,
-                           __shfl(id, wid * kTile + (lane & (kTile - 1)), 64), lane);
+    if constexpr (S == 1) {
+        if (s.steps[proj[0]] && first == 0 && r0[0] == 0 && part == 0 && wid < SPAN / kTile) {
+            const int tile = t0 / kTile + wid;
+            if (tile * kTile < s.T)
+                list_steps<32>(s.steps[proj[0]] + (int64_t)tile * (kMaxSteps / 2), s.n_steps[proj[0]] + tile, s.lora[proj[0]],
+                               __shfl(id, wid * kTile + (lane & (kTile - 1)), 64), lane);
+        }
     }
     uint64_t left = __ballot(id >= 0);
     for (int i = 0; left; ++i) {
@@ -126,26 +135,40 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(ShrinkArgs s) 
         const uint64_t hit = __ballot(id == a);
         left &= ~hit;
         if (i % stride != first) continue;
-        const int rank = __builtin_amdgcn_readlane(ranks, src);
-        if (r0 >= rank) continue;         // the expand reads v in steps of 16 up to the rank
-        const float scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scales), src));
+        int rank[S];
+        bool on[S], any = false;          // the expand reads v in steps of 16 up to the rank
+#pragma unroll
+        for (int m = 0; m < S; ++m) {
+            rank[m] = __builtin_amdgcn_readlane(ranks[m], src);
+            on[m] = r0[m] < rank[m];
+            any = any || on[m];
+        }
+        if (!any) continue;
         if (id == a) cols[wid][__popcll(hit & ((1ull << lane) - 1))] = (uint8_t)lane;
         const int nc = __popcll(hit);
-        const uint16_t* arow = lo.a + ((int64_t)a * R + min(r0 + (lane & 15), rank - 1)) * s.K;
+        const uint16_t* arow[S];
+#pragma unroll
+        for (int m = 0; m < S; ++m)
+            arow[m] = s.lora[proj[m]].a +
+                      ((int64_t)a * s.lora[proj[m]].max_rank + min(r0[m] + (lane & 15), max(rank[m] - 1, 0))) * s.K;
         for (int c0 = 0; c0 < nc; c0 += CW) {
             const int n = min(CW, nc - c0);
             int64_t xo[NX];
 #pragma unroll
             for (int q = 0; q < NX; ++q)
                 xo[q] = (int64_t)(t0 + cols[wid][c0 + min(q * kCols + (lane & 15), n - 1)]) * s.K;
-            f32x4_t acc[NX];
+            f32x4_t acc[S][NX];
 #pragma unroll
-            for (int q = 0; q < NX; ++q) acc[q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-            XUnit au[2], x[2][NX][PL];
+            for (int m = 0; m < S; ++m)
+#pragma unroll
+                for (int q = 0; q < NX; ++q) acc[m][q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            XUnit au[2][S], x[2][NX][PL];
             pipelined<2>(
                 u1 - u0,
                 [&](int b, int u) {
-                    load_x<FT_FMT_BF16>(au[b], arow, u0 + u, lane);
+#pragma unroll
+                    for (int m = 0; m < S; ++m)
+                        if (S == 1 || on[m]) load_x<FT_FMT_BF16>(au[b][m], arow[m], u0 + u, lane);
 #pragma unroll
                     for (int q = 0; q < NX; ++q)
                         if (q == 0 || q * kCols < n) {
@@ -155,37 +178,47 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(ShrinkArgs s) 
                 },
                 [&](int b, int) {
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
+                    for (int m = 0; m < S; ++m)
+                        if (S == 1 || on[m])
 #pragma unroll
-                        for (int q = 0; q < NX; ++q)
-                            if (q == 0 || q * kCols < n)
+                            for (int v = 0; v < 4; ++v)
 #pragma unroll
-                                for (int p = 0; p < PL; ++p)
-                                    acc[q] = mma(__builtin_bit_cast(bf16x8_t, au[b].v[v]), x[b][q][p].v[v], acc[q]);
+                                for (int q = 0; q < NX; ++q)
+                                    if (q == 0 || q * kCols < n)
+#pragma unroll
+                                        for (int p = 0; p < PL; ++p)
+                                            acc[m][q] = mma(__builtin_bit_cast(bf16x8_t, au[b][m].v[v]), x[b][q][p].v[v], acc[m][q]);
                 });
             constexpr int RR = 20;                   // floats of a column's ranks in LDS, padded
             __syncthreads();
 #pragma unroll
             for (int q = 0; q < NX; ++q) {
-                const int m = q * kCols + (lane & 15);
-                if (m < n) *reinterpret_cast<f32x4_t*>(red + (wid * n + m) * RR + 4 * (lane >> 4)) = acc[q];
+                const int c = q * kCols + (lane & 15);
+#pragma unroll
+                for (int m = 0; m < S; ++m)
+                    if (c < n) *reinterpret_cast<f32x4_t*>(red + ((m * kWaves + wid) * n + c) * RR + 4 * (lane >> 4)) = acc[m][q];
             }
             __syncthreads();
-            for (int q = tid; q < n * 16; q += kThreads) {
-                const int m = q >> 4, k = q & 15, r = r0 + k;
-                float v = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kWaves; ++w) v += red[(w * n + m) * RR + k];
-                v = r < rank ? scale * v : 0.0f;
-                const int64_t o = (int64_t)(t0 + cols[wid][c0 + m]) * R + r;
-                if (s.vpart[proj]) {
-                    s.vpart[proj][(int64_t)part * s.T * R + o] = v;
-                } else {
-                    uint16_t h, l;
-                    split_bf16(v, h, l);              // 16 significant bits
-                    const int64_t at = (int64_t)part * s.T * R + o;
-                    s.vhi[proj][at] = h;
-                    s.vlo[proj][at] = l;
+            for (int m = 0; m < S; ++m) {
+                if (!on[m]) continue;
+                const float scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scales[m]), src));
+                const int R = s.lora[proj[m]].max_rank;
+                for (int q = tid; q < n * 16; q += kThreads) {
+                    const int c = q >> 4, k = q & 15, r = r0[m] + k;
+                    float v = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) v += red[((m * kWaves + w) * n + c) * RR + k];
+                    v = r < rank[m] ? scale * v : 0.0f;
+                    const int64_t at = ((int64_t)part * s.T + t0 + cols[wid][c0 + c]) * R + r;
+                    if (s.vpart[proj[m]]) {
+                        s.vpart[proj[m]][at] = v;
+                    } else {
+                        uint16_t h, l;
+                        split_bf16(v, h, l);              // 16 significant bits
+                        s.vhi[proj[m]][at] = h;
+                        s.vlo[proj[m]][at] = l;
+                    }
                 }
             }
         }
@@ -553,13 +586,40 @@ __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a
 
 constexpr size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// How a shrink launch goes over its tokens and slots.
+struct Shrink {
+    int span, per;         // tokens, and slots, of a workgroup
+    int parts;             // of K
+};
+
+// Short calls, whose tokens may all name adapters of their own: spans of 64
+// tokens, as the more tokens share an adapter's A the better.  A prompt's spans
+// mostly have one adapter: 32 tokens where that still leaves the workgroups one
+// round of the 256 compute units (777 tokens of K = 2,048: 6.4 us, 9.1 with 64),
+// 64 where it does not (8,192 tokens, two slots: 15.4 us, 19.4 with 32), and where
+// x exceeds the XCDs' 32 MiB of L2, so that another slot's workgroups read it from
+// beyond them, two slots to a workgroup (4,096 tokens of K = 7,168: 29 us, 40 with
+// one; 8,192 of K = 2,048: 17.3).
+Shrink shrink_of(int T, int K, int slots, int adapters, bool prompt) {
+    Shrink s;
+    const int64_t narrow = (T + kTile - 1) / kTile;
+    s.per = prompt && slots > 1 && narrow * slots >= 256 && (int64_t)T * K * 2 > (32ll << 20) ? 2 : 1;
+    s.span = prompt && (s.per == 2 || narrow * slots <= 256) ? kTile : 2 * kTile;
+    const int64_t spans = (T + s.span - 1) / s.span;
+    const int most = prompt ? K / kUnit / kWaves : (K / kUnit + kWaves - 1) / kWaves;
+    int64_t p = 256 / (spans * ((slots + s.per - 1) / s.per) * (prompt ? 1 : adapters));
+    p = p > most ? most : p;
+    s.parts = p < 1 ? 1 : p > kMaxParts ? kMaxParts : (int)p;
+    return s;
+}
+
 // How a call's product and its adapters are divided.
 struct Split {
     int splits;        // workgroups of a (panel, tile) that stream it
     bool adapted;      // it has adapters:
     bool fused;        // lsplits workgroups per matrix compute v and take them, or
     int lsplits;
-    int vparts;        // a shrink launch computes v in this many parts of K
+    Shrink shrink;     // a launch before it computes v
 };
 
 // `nm` matrices [n x K]; `adapters`, `rank`: the most a tile of the call can
@@ -574,7 +634,7 @@ Split split_of(int nm, int n, int K, int T, int adapters, int rank) {
     s.splits = w < 1 ? 1 : (int)w;
     s.lsplits = 0;
     s.adapted = s.fused = false;
-    s.vparts = 1;
+    s.shrink.parts = 1;
     if (adapters <= 0 || rank <= 0) return s;
     s.adapted = true;
     if (adapters > T) adapters = T;
@@ -591,10 +651,7 @@ Split split_of(int nm, int n, int K, int T, int adapters, int rank) {
         l = l > need ? need : l;
         s.lsplits = l < 1 ? 1 : l > 4 ? 4 : (int)l;
     } else {
-        const int64_t spans = (T + kSpan - 1) / kSpan;
-        int64_t parts = 256 / (spans * adapters * (rank / 16) * nm);
-        parts = parts > most ? most : parts;
-        s.vparts = parts < 1 ? 1 : parts > kMaxParts ? kMaxParts : (int)parts;
+        s.shrink = shrink_of(T, K, nm * (rank / 16), adapters, false);
     }
     return s;
 }
@@ -613,19 +670,21 @@ size_t lds_bytes(const ProjectArgs& a) {
     return n;
 }
 
-hipError_t launch_shrink(const ShrinkArgs& s, int projections, hipStream_t st) {
-    const int spans = (s.T + kSpan - 1) / kSpan;
-    int most = 0;
-    for (int i = 0; i < projections; ++i) most = s.lora[i].count > most ? s.lora[i].count : most;
+hipError_t launch_shrink(const ShrinkArgs& s, const Shrink& sh, hipStream_t st) {
+    const int spans = (s.T + sh.span - 1) / sh.span;
+    const int most = s.lora[0].count > s.lora[1].count ? s.lora[0].count : s.lora[1].count;
     // a workgroup per adapter of a span while spans are few; prompts have few adapters per span
     int gy = most < kTile ? most : kTile;
     if (gy > s.T) gy = s.T;
     if (spans >= 16 && gy > 2) gy = 2;
-    const dim3 grid(spans, projections * s.panels * s.parts, gy);
-    const int cols = s.xlo ? 2 * kCols : 4 * kCols;
-    const size_t lds = (size_t)kWaves * (s.T < cols ? s.T : cols) * 20 * sizeof(float);
-    if (s.xlo) hipLaunchKernelGGL((lora_shrink_kernel<2, 2>), grid, dim3(kThreads), lds, st, s);
-    else hipLaunchKernelGGL((lora_shrink_kernel<1, 4>), grid, dim3(kThreads), lds, st, s);
+    const dim3 grid(spans, (s.slots + sh.per - 1) / sh.per * s.parts, gy);
+    const int cols = s.xlo || sh.span == kTile ? 2 * kCols : 4 * kCols;
+    const size_t lds = (size_t)sh.per * kWaves * (s.T < cols ? s.T : cols) * 20 * sizeof(float);
+    const auto f = s.xlo             ? lora_shrink_kernel<2, 2, 2 * kTile, 1>
+                   : sh.span > kTile ? lora_shrink_kernel<1, 4, 2 * kTile, 1>
+                   : sh.per == 1     ? lora_shrink_kernel<1, 2, kTile, 1>
+                                     : lora_shrink_kernel<1, 2, kTile, 2>;
+    hipLaunchKernelGGL(f, grid, dim3(kThreads), lds, st, s);
     return hipGetLastError();
 }
 
@@ -743,14 +802,14 @@ namespace {
 // The shrink launch of up to two projections that read the same x, into
 // `planes` (two bf16 planes, for the GEMM) or fp32 parts at v[i].
 hipError_t shrink(const LoraView* const* pools, uint8_t* const* v, int n, const int32_t* adapter, const uint16_t* xhi,
-                  const uint16_t* xlo, int T, int K, bool planes, int parts, hipStream_t st) {
+                  const uint16_t* xlo, int T, int K, bool planes, const Shrink& sh, hipStream_t st) {
     ShrinkArgs s = {};
     s.adapter = adapter;
     s.xhi = xhi;
     s.xlo = xlo;
     s.T = T;
     s.K = K;
-    s.parts = parts;
+    s.parts = sh.parts;
     int m = 0;
     for (int i = 0; i < n; ++i) {
         if (pool_adapters(pools[i]) == 0) continue;
@@ -767,19 +826,19 @@ hipError_t shrink(const LoraView* const* pools, uint8_t* const* v, int n, const 
         s.panels = pools[i]->max_rank / 16 > s.panels ? pools[i]->max_rank / 16 : s.panels;
         ++m;
     }
-    return m > 0 ? launch_shrink(s, m, st) : hipSuccess;
+    s.slots = m * s.panels;
+    return m > 0 ? launch_shrink(s, sh, st) : hipSuccess;
 }
 
-// The parts of K of a GEMM's shrink launch over K: a workgroup per compute unit
-// when a span of tokens names one adapter.
-int gemm_parts(const LoraView* const* pools, int n, int K, int T) {
-    int64_t wgs = 0;
-    for (int i = 0; i < n; ++i) wgs += pool_rank(pools[i]) / 16;
-    wgs *= (T + kSpan - 1) / kSpan;
-    int64_t p = wgs > 0 ? 256 / wgs : 1;
-    const int most = K / kUnit / kWaves;
-    p = p > most ? most : p;
-    return p < 1 ? 1 : p > kMaxParts ? kMaxParts : (int)p;
+// The shrink launch before a GEMM over K.
+Shrink gemm_shrink(const LoraView* const* pools, int n, int K, int T) {
+    int m = 0, rank = 16;
+    for (int i = 0; i < n; ++i) {
+        if (pool_adapters(pools[i]) == 0) continue;
+        rank = pools[i]->max_rank > rank ? pools[i]->max_rank : rank;
+        ++m;
+    }
+    return shrink_of(T, K, (m > 0 ? m : 1) * (rank / 16), 1, true);
 }
 
 // The pools, planes and adapters of a GEMM's matrices
@@ -809,9 +868,9 @@ hipError_t product(int fmt, ProjectArgs& a, const LoraView* const* pools, uint8_
     const Split s = split_of(NM, a.n, a.K, a.T, adapters, rank);
     a.splits = s.splits;
     a.lsplits = s.lsplits;
-    a.vparts = s.vparts;
+    a.vparts = s.shrink.parts;
     if (s.adapted && !s.fused) {
-        const hipError_t e = shrink(pools, v, NM, a.adapter, a.xhi, a.xlo, a.T, a.K, false, s.vparts, st);
+        const hipError_t e = shrink(pools, v, NM, a.adapter, a.xhi, a.xlo, a.T, a.K, false, s.shrink, st);
         if (e != hipSuccess) return e;
     }
     return launch_project<NM, PL>(fmt, a, s.fused, st);
@@ -836,9 +895,9 @@ hipError_t launch_lora_project(const MatrixView& m, const LoraView* lora, const 
         g.scales[0] = m.scales;
         g.adapter = adapter;
         g.base = base;
-        const int parts = gemm_parts(pools, 1, m.K, T);
-        gemm_pools(g, pools, v, 1, parts);
-        const hipError_t e = shrink(pools, v, 1, adapter, x, nullptr, T, m.K, true, parts, st);
+        const Shrink sk = gemm_shrink(pools, 1, m.K, T);
+        gemm_pools(g, pools, v, 1, sk.parts);
+        const hipError_t e = shrink(pools, v, 1, adapter, x, nullptr, T, m.K, true, sk, st);
         return e != hipSuccess ? e : launch_lora_gemm(m.fmt, false, g, st);
     }
     ProjectArgs a = {};
@@ -884,15 +943,15 @@ hipError_t launch_lora_expert(const ft_shape& sh, const RecordLayout& rl, const 
         g.scales[0] = rec + rl.off_sg;
         g.scales[1] = rec + rl.off_su;
         g.adapter = adapter;
-        const int gp = gemm_parts(pools, 2, sh.d_model, T), dp = gemm_parts(pools + 2, 1, sh.d_ff, T);
-        gemm_pools(g, pools, v, 2, gp);
-        if ((e = shrink(pools, v, 2, adapter, x, nullptr, T, sh.d_model, true, gp, st)) != hipSuccess) return e;
+        const Shrink gs = gemm_shrink(pools, 2, sh.d_model, T), ds = gemm_shrink(pools + 2, 1, sh.d_ff, T);
+        gemm_pools(g, pools, v, 2, gs.parts);
+        if ((e = shrink(pools, v, 2, adapter, x, nullptr, T, sh.d_model, true, gs, st)) != hipSuccess) return e;
         if ((e = launch_lora_gemm(sh.fmt, true, g, st)) != hipSuccess) return e;
         g.codes[0] = rec + rl.off_down;
         g.scales[0] = rec + rl.off_sd;
         g.base = base;
-        gemm_pools(g, pools + 2, v + 2, 1, dp);
-        if ((e = shrink(pools + 2, v + 2, 1, adapter, hhi, nullptr, T, sh.d_ff, true, dp, st)) != hipSuccess) return e;
+        gemm_pools(g, pools + 2, v + 2, 1, ds.parts);
+        if ((e = shrink(pools + 2, v + 2, 1, adapter, hhi, nullptr, T, sh.d_ff, true, ds, st)) != hipSuccess) return e;
         return launch_lora_gemm(sh.fmt, false, g, st);
     }
     ProjectArgs a = {};
