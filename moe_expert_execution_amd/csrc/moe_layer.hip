@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
 // ---- the routed experts --------------------------------------------------------------
 
 constexpr int kMaxRoutes = kMaxLayerTokens * kMaxTopK;       // 1024
-constexpr int kMaxTiles = kMaxRouteExperts + kMaxRoutes / (kTile + 1);
+constexpr int kMaxTiles = kMaxRouteExperts + kMaxRoutes / (kCols + 1);
 
 struct ExpertArgs {
     const double* logits;  // [slices][E] of a single token (ONE)
@@ -258,7 +258,7 @@ struct ExpertArgs {
     int T, E, k, d, f, splits;
 };
 
-// A tile: at most kTile routes of one expert.
+// A tile: routes of one expert, as many as its kernel's operands hold.
 struct Tile {
     int e, first, nt;      // expert, first place in Groups::route, count
 };
@@ -279,7 +279,8 @@ struct Groups {
     }
 };
 
-// Every thread of the workgroup calls it.
+// Every thread of the workgroup calls it; tiles of up to W routes.
+template <int W>
 __device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int T, int E, int k) {
     constexpr int PT = kMaxRoutes / kThreads;
     const int tid = threadIdx.x, lane = tid & 63, R = T * k;
@@ -302,7 +303,7 @@ __device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int 
         for (int e0 = 0; e0 < E; e0 += 64) {
             const int e = e0 + lane;
             const int c = e < E ? __popcll(g.mask[e]) : 0;
-            const int tl = (c + kTile - 1) / kTile;
+            const int tl = (c + W - 1) / W;
             int sc = c, st = tl;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
@@ -316,8 +317,8 @@ __device__ __forceinline__ void group_routes(Groups& g, const int32_t* ids, int 
                 const int first = base + sc - c;
                 g.start[e] = first;
                 for (int q = 0; q < tl; ++q)
-                    g.tile[tiles + st - tl + q] = (uint32_t)e | ((uint32_t)(first + q * kTile) << 8) |
-                                                  ((uint32_t)min(kTile, c - q * kTile) << 18);
+                    g.tile[tiles + st - tl + q] = (uint32_t)e | ((uint32_t)(first + q * W) << 8) |
+                                                  ((uint32_t)min(W, c - q * W) << 18);
             }
             base += __shfl(sc, 63, 64);
             tiles += __shfl(st, 63, 64);
@@ -740,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 2) layer_experts_kernel(ExpertArgs a
         select_one(g, wr, reinterpret_cast<double*>(red), a);
     } else {
         for (int r = tid; r < a.T * a.k; r += kThreads) wr[r] = a.w[r];
-        group_routes(g, a.ids, a.T, a.E, a.k);
+        group_routes<kCols>(g, a.ids, a.T, a.E, a.k);
     }
     const int mine = number;
     if (mine >= 0) {
@@ -777,23 +778,30 @@ __global__ void __launch_bounds__(kThreads, 2) layer_experts_kernel(ExpertArgs a
 
 // More tokens: two launches, whose second operand of 16 columns leaves no
 // registers for the hand-over (it is 1% of these calls and less).
-template <int FMT>
+template <int FMT, int NX>
 __global__ void __launch_bounds__(kThreads, 2) layer_gateup_kernel(ExpertArgs a) {
     extern __shared__ __attribute__((aligned(16))) float red[];
     __shared__ Groups g;
-    group_routes(g, a.ids, a.T, a.E, a.k);
-    layer_gateup<FMT, 2>(a, g, red, blockIdx.x);
+    group_routes<NX * kCols>(g, a.ids, a.T, a.E, a.k);
+    layer_gateup<FMT, NX>(a, g, red, blockIdx.x);
 }
-template <int FMT, int NP>
+template <int FMT, int NX, int NP>
 __global__ void __launch_bounds__(kThreads, 2) layer_down_kernel(ExpertArgs a) {
     extern __shared__ __attribute__((aligned(16))) float red[];
     __shared__ Groups g;
     __shared__ float wr[kMaxRoutes];
     __shared__ uint32_t flag;
     for (int r = threadIdx.x; r < a.T * a.k; r += kThreads) wr[r] = a.w[r];
-    group_routes(g, a.ids, a.T, a.E, a.k);
-    layer_down<FMT, 2, NP>(a, g, wr, red, &flag, [](auto&&) { return true; });
+    group_routes<NX * kCols>(g, a.ids, a.T, a.E, a.k);
+    layer_down<FMT, NX, NP>(a, g, wr, red, &flag, [](auto&&) { return true; });
 }
+
+// Tiles of 16 routes instead of 32.  The second operand costs registers (28 spilled
+// in MXFP4's down, 21 in bf16) whether a tile fills it or not, and 16 routes hold
+// most experts of a batch: 64 tokens on 256 MXFP4 experts take 936 us and 1,080
+// with 32, 64 on 128 bf16 experts 206 and 234.  An expert with more reads its
+// weights again, so calls whose experts have more than 4 routes on average keep 32.
+bool narrow_tiles(const ft_shape& s, int T) { return (int64_t)T * s.top_k <= 4ll * s.experts; }
 
 // Row panels per down workgroup.  The h loads beside an MXFP4 panel outweigh its
 // codes fourfold, so two panels share them once there are experts enough to
@@ -854,7 +862,7 @@ hipError_t launch_fmt(const ft_shape& s, const RouteArgs& r, const ExpertArgs& a
     if (e != hipSuccess) return e;
 
     const int R = a.T * a.k;
-    const int tiles = (R < a.E ? R : a.E) + R / (kTile + 1);
+    const int tiles = (R < a.E ? R : a.E) + R / (kCols + 1);       // at most, whatever the tiles' width
     const int64_t items = (int64_t)tiles * (a.f / 32);
     const int np = down_panels(s, a.T);
     const int64_t ditems = (int64_t)(a.d / 32 / np) * a.splits;
@@ -876,14 +884,15 @@ hipError_t launch_fmt(const ft_shape& s, const RouteArgs& r, const ExpertArgs& a
         }
         return hipGetLastError();
     }
-    hipLaunchKernelGGL(layer_gateup_kernel<FMT>, blocks(items), dim3(kThreads), glds, st, a);
+    const bool narrow = narrow_tiles(s, a.T);
+    const auto gu = narrow ? layer_gateup_kernel<FMT, 1> : layer_gateup_kernel<FMT, 2>;
+    hipLaunchKernelGGL(gu, blocks(items), dim3(kThreads), glds, st, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)ditems);
-    if (FMT == FT_FMT_MXFP4_B32 && np == 2)
-        hipLaunchKernelGGL((layer_down_kernel<FMT, FMT == FT_FMT_MXFP4_B32 ? 2 : 1>), grid, dim3(kThreads), dlds, st, a);
-    else
-        hipLaunchKernelGGL((layer_down_kernel<FMT, 1>), grid, dim3(kThreads), dlds, st, a);
+    constexpr int P2 = FMT == FT_FMT_MXFP4_B32 ? 2 : 1;
+    const auto dn = narrow ? (np == 2 ? layer_down_kernel<FMT, 1, P2> : layer_down_kernel<FMT, 1, 1>)
+                           : (np == 2 ? layer_down_kernel<FMT, 2, P2> : layer_down_kernel<FMT, 2, 1>);
+    hipLaunchKernelGGL(dn, dim3((unsigned)ditems), dim3(kThreads), dlds, st, a);
     return hipGetLastError();
 }
 
