@@ -144,6 +144,12 @@ __device__ __forceinline__ void select_experts(const double* z, int E, int k, in
 // last workgroup adds the slices in order and selects, one wave per token
 // (a single token's slices are added by the experts' launch: sending them on is
 // quicker than waiting for them here).
+//
+// Latency decides it: 4.9 us at one token and 128 experts, 9.9 at 16, 12.6 at 5 and
+// 256 experts of d = 4,096 (2.1 MB of router), of which the two waits for other
+// workgroups' numbers and the selection are more than half; 28 to 33 us for 64
+// tokens, 256 experts and d = 7,168 (0.23 GFLOP: 8 TFLOP/s in fp64, half of each
+// product's rows unused).
 __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
     extern __shared__ __attribute__((aligned(16))) double zred[];
     __shared__ uint32_t flag;
@@ -451,7 +457,7 @@ __device__ __forceinline__ void store_h(const ExpertArgs& a, const Groups& g, fl
 // Gate/up and SwiGLU: number v does the items (tile, 32 neurons) v, v + grid,
 // ...; the waves split K = d.  The next unit's loads are in flight while one is
 // multiplied, across items too, so the stream does not stop for an item's
-// sums.
+// sums.  64 tokens on 256 MXFP4 experts: 3.5 GB in 580 to 640 us, 5.4 to 6.0 TB/s.
 template <int FMT, int NX>
 __device__ __forceinline__ void layer_gateup(const ExpertArgs& a, const Groups& g, float* red, const int first_item) {
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, grid = gridDim.x;
@@ -580,6 +586,8 @@ constexpr int sum_row() { return 32 * NP + 4; }      // floats of a token's sums
 // order, so y does not depend on timing.  wait(again) is called once, before h
 // is first read, with the first unit of weights on its way; where it has used
 // the registers meanwhile it calls again().  It returns whether h is there.
+// 64 tokens on 256 MXFP4 experts: 1.7 GB in 323 to 354 us, 4.9 to 5.4 TB/s, the
+// rest being the splits' four rounds of grouping, 64 tokens' sums and partial sums.
 template <int FMT, int NX, int NP, typename Wait>
 __device__ __forceinline__ void layer_down(const ExpertArgs& a, const Groups& g, const float* wr, float* red, uint32_t* flag,
                                            Wait&& wait) {
@@ -721,8 +729,14 @@ __device__ __forceinline__ void layer_down(const ExpertArgs& a, const Groups& g,
 // Up to 16 tokens: the routed experts and the combine in one launch.  A launch
 // between gate/up and down costs 2.4 us and empties the card twice; here a
 // workgroup without gate/up work, or done with it, has its down weights under
-// way while it waits.
-// ONE: a single token, selected here.
+// way while it waits (the whole call on 128 bf16 experts of 2,048 x 768: 147 us
+// with two launches, 137 in one at 16 tokens; 30.7 and 27.8 at one).
+// ONE: a single token, selected here (27.7 and 26.4 us).
+//
+// Bound by HBM: 779 MB of records and router at 16 tokens in 126 us are 6.2 TB/s,
+// what a large read reaches; 947 MB of 40 FP8 experts in 162 us 5.8 TB/s.  At one
+// token (75 MB, 21.7 us) and in small layers by latency: grouping or selection,
+// the first weights, two sums over waves, the hand-over and the sum over splits.
 template <int FMT, int NP, bool ONE>
 __global__ void __launch_bounds__(kThreads, 2) layer_experts_kernel(ExpertArgs a) {
     extern __shared__ __attribute__((aligned(16))) float red[];     // the waves' sums of either half
@@ -776,8 +790,9 @@ __global__ void __launch_bounds__(kThreads, 2) layer_experts_kernel(ExpertArgs a
     });
 }
 
-// More tokens: two launches, whose second operand of 16 columns leaves no
-// registers for the hand-over (it is 1% of these calls and less).
+// More tokens: two launches.  (In one, most of these calls gained 0 to 3%, and 64
+// tokens on 128 MXFP4 experts of d = 2,048 took 110 us instead of 96: their many
+// down items go one after the other through the workgroups that gate/up left.)
 template <int FMT, int NX>
 __global__ void __launch_bounds__(kThreads, 2) layer_gateup_kernel(ExpertArgs a) {
     extern __shared__ __attribute__((aligned(16))) float red[];
@@ -796,16 +811,19 @@ __global__ void __launch_bounds__(kThreads, 2) layer_down_kernel(ExpertArgs a) {
     layer_down<FMT, NX, NP>(a, g, wr, red, &flag, [](auto&&) { return true; });
 }
 
-// Tiles of 16 routes instead of 32.  The second operand costs registers (28 spilled
-// in MXFP4's down, 21 in bf16) whether a tile fills it or not, and 16 routes hold
-// most experts of a batch: 64 tokens on 256 MXFP4 experts take 936 us and 1,080
-// with 32, 64 on 128 bf16 experts 206 and 234.  An expert with more reads its
-// weights again, so calls whose experts have more than 4 routes on average keep 32.
-bool narrow_tiles(const ft_shape& s, int T) { return (int64_t)T * s.top_k <= 4ll * s.experts; }
+// Tiles of 16 routes instead of 32 (more than 16 tokens).  The second operand
+// costs registers (28 spilled in MXFP4's down, 21 in bf16) whether a tile fills it
+// or not: 64 tokens on 256 MXFP4 experts (2 routes each) take 930 us and 1,085
+// with 32, 64 on 128 bf16 experts (4) 199 and 235, 64 on 8 (16) 41 and 43.  An
+// expert with more than 16 routes reads its weights again, from L2 at best: with
+// 32 routes each, 8 FP8 experts take 116 us and 105 with tiles of 32, 8 MXFP4
+// experts at 64 each 188 and 174.
+bool narrow_tiles(const ft_shape& s, int T) { return (int64_t)T * s.top_k <= 16ll * s.experts; }
 
 // Row panels per down workgroup.  The h loads beside an MXFP4 panel outweigh its
 // codes fourfold, so two panels share them once there are experts enough to
-// fill the card all the same.
+// fill the card all the same (d = 7,168, 256 experts: 170 us and 180 with one at 4
+// tokens, 945 and 1,071 at 64; d = 2,048, 128 experts: 29.8 and 28.9 at 2 tokens).
 int down_panels(const ft_shape& s, int T) {
     return s.fmt == FT_FMT_MXFP4_B32 && (int64_t)T * s.top_k >= 32 ? 2 : 1;
 }
