@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import moe_expert_execution_amd as M
 from oracle import formats as OF
 from tests.gpu_util import dev, dev_u16
 from tests.resident_util import Pool, assert_within, bits, expert_with_bound, mixed_ids, project_with_bound
@@ -190,3 +191,20 @@ def test_prompts_on_two_streams():
     torch.cuda.synchronize()
     for i in range(2):
         np.testing.assert_array_equal(bits(ys[i]), want[i])
+
+
+@pytest.mark.parametrize("off", [0, 1])
+def test_most_tokens(off):
+    """The largest call, through the tiles and, with y off the 16-byte grid, through the few-token kernel."""
+    n, K, R, T = 128, 128, 16, 65535
+    pr = Project("bf16", n, K, R, T, seed=32)
+    pool = Pool(5, R, K, n, 32)
+    x, ids = x_of(T, K, 0), mixed_ids(T, 5, 32, run=3000)
+    ref, bound = project_with_bound(x, pr.W, pool, ids)
+    y = torch.full((T * n + 8,), -7, dtype=torch.int16, device="cuda")
+    pr.enqueue(pool.device(), dev_u16(x), dev(ids), y[off:])
+    torch.cuda.synchronize()
+    assert_within(OF.bf16_to_f64(bits(y[off:off + T * n].view(T, n))), ref, bound)
+    assert (y[:off] == -7).all() and (y[off + T * n:] == -7).all()
+    with pytest.raises(M.FtError, match="T must be"):
+        pr.enqueue(pool.device(), dev_u16(x), dev(ids), y, T=T + 1)
