@@ -135,6 +135,24 @@ __device__ __forceinline__ void select_experts(const double* z, int E, int k, in
     }
 }
 
+// W = 32: a + its other half's in the lower half of the wave, the same of b in the
+// upper; W = 16: in the even and odd rows of 16 lanes.
+template <int W>
+__device__ __forceinline__ double add_halves(double a, double b) {
+    const uint64_t x = (uint64_t)__double_as_longlong(a), y = (uint64_t)__double_as_longlong(b);
+    uint32_t p[2], q[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t u = (uint32_t)(x >> (32 * i)), v = (uint32_t)(y >> (32 * i));
+        const auto r = W == 32 ? __builtin_amdgcn_permlane32_swap(u, v, false, false)
+                               : __builtin_amdgcn_permlane16_swap(u, v, false, false);
+        p[i] = r[0];
+        q[i] = r[1];
+    }
+    return __longlong_as_double((long long)(p[0] | ((uint64_t)p[1] << 32))) +
+           __longlong_as_double((long long)(q[0] | ((uint64_t)q[1] << 32)));
+}
+
 // Workgroup (slice of d, 64 experts, 8 tokens): partial logits on the fp64
 // matrix cores (bf16 products are exact in fp64, sums are fp64).  Per 32 rows
 // lane group g = l / 16 takes rows 8 g .. 8 g + 7, so MFMA step s contracts
@@ -150,6 +168,11 @@ __device__ __forceinline__ void select_experts(const double* z, int E, int k, in
 // workgroups' numbers and the selection are more than half; 28 to 33 us for 64
 // tokens, 256 experts and d = 7,168 (0.23 GFLOP: 8 TFLOP/s in fp64, half of each
 // product's rows unused).
+//
+// NT: up to 8 tokens by vector FMAs instead (0: the matrix cores).  A lane sums its
+// rows and four experts for each token, and the four lane groups' sums are added
+// by exchanging halves.
+template <int NT>
 __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
     extern __shared__ __attribute__((aligned(16))) double zred[];
     __shared__ uint32_t flag;
@@ -164,16 +187,19 @@ __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
     const int k0 = (slice * kWaves + wid) * a.rows, k1 = min(a.d, k0 + a.rows);
     const int e4 = e0 + 4 * c;
     const bool vec = (a.E & 3) == 0;      // rows of the router aligned for 8-byte loads
-    f64x4 acc[4];
+    constexpr int XT = NT ? NT : 1;       // tokens a lane loads
+    f64x4 acc[NT ? NT : 4];               // [token] of the four experts, or [tile]
 #pragma unroll
-    for (int n = 0; n < 4; ++n) acc[n] = f64x4{0.0, 0.0, 0.0, 0.0};
-    const uint16_t* xrow = a.x + (int64_t)(t0 + min(c, nt - 1)) * a.d + 8 * g;
+    for (f64x4& v : acc) v = f64x4{0.0, 0.0, 0.0, 0.0};
+    const uint16_t* xrow = a.x + (int64_t)(t0 + (NT ? 0 : min(c, nt - 1))) * a.d + 8 * g;
     constexpr int D = 2;
-    u32x4_t xv[D];
+    u32x4_t xv[D][XT];
     u32x2_t wv[D][8];
     auto load = [&](int b, int i) {
         const int kk = k0 + 32 * i;
-        xv[b] = *reinterpret_cast<const u32x4_t*>(xrow + kk);
+#pragma unroll
+        for (int t = 0; t < XT; ++t)
+            if (t < nt) xv[b][t] = *reinterpret_cast<const u32x4_t*>(xrow + (int64_t)t * a.d + kk);
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
             const uint16_t* p = a.wr + (int64_t)(kk + 8 * g + s) * a.E + e4;
@@ -191,24 +217,48 @@ __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
     auto work = [&](int b, int) {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-            const uint32_t xw = xv[b][s >> 1];
-            const double av = (double)((s & 1) ? bf16hi(xw) : bf16lo(xw));
+            double wd[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const uint32_t u = wv[b][s][n >> 1];
-                const double bv = (double)((n & 1) ? bf16hi(u) : bf16lo(u));
-                acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64(av, bv, acc[n], 0, 0, 0);
+                wd[n] = (double)((n & 1) ? bf16hi(u) : bf16lo(u));
+            }
+#pragma unroll
+            for (int t = 0; t < XT; ++t) {
+                if (t >= nt) break;
+                const uint32_t xw = xv[b][t][s >> 1];
+                const double xd = (double)((s & 1) ? bf16hi(xw) : bf16lo(xw));
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    if constexpr (NT) acc[t][n] = fma(xd, wd[n], acc[t][n]);
+                    else acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64(xd, wd[n], acc[n], 0, 0, 0);
+                }
             }
         }
     };
     pipelined<D>(max(k1 - k0, 0) / 32, load, work);
-    // accumulator element v of lane l: token 4 v + l / 16, expert 4 (l % 16) + n
+    if constexpr (NT) {
+        // value i = 4 t + n: the halves of the wave keep i and i + 2 NT, then the rows i and i + NT
+        double v[4 * NT];
 #pragma unroll
-    for (int v = 0; v < kRouteTokens / 4; ++v) {
-        const int t = 4 * v + g;
-        if (t < nt)
+        for (int i = 0; i < 4 * NT; ++i) v[i] = acc[i / 4][i % 4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) zred[(wid * nt + t) * kRouteExperts + 4 * c + n] = acc[n][v];
+        for (int i = 0; i < 2 * NT; ++i) v[i] = add_halves<32>(v[i], v[i + 2 * NT]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const double z = add_halves<16>(v[i], v[i + NT]);
+            const int at = i + (g & 1) * NT + (g >> 1) * 2 * NT, t = at >> 2;
+            if (t < nt) zred[(wid * nt + t) * kRouteExperts + 4 * c + (at & 3)] = z;
+        }
+    } else {
+        // accumulator element v of lane l: token 4 v + l / 16, expert 4 (l % 16) + n
+#pragma unroll
+        for (int v = 0; v < kRouteTokens / 4; ++v) {
+            const int t = 4 * v + g;
+            if (t < nt)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) zred[(wid * nt + t) * kRouteExperts + 4 * c + n] = acc[n][v];
+        }
     }
     __syncthreads();
     for (int i = tid; i < nt * kRouteExperts; i += kThreads) {
@@ -874,7 +924,8 @@ hipError_t launch_fmt(const ft_shape& s, const RouteArgs& r, const ExpertArgs& a
     const int rt = r.T < kRouteTokens ? r.T : kRouteTokens;
     // the waves' partial logits, then whole rows
     static_assert(kWaves * kRouteExperts >= kMaxRouteExperts, "a token's logits fit its partial sums' place");
-    hipLaunchKernelGGL(layer_route_kernel, rg, dim3(kThreads), (size_t)rt * kWaves * kRouteExperts * sizeof(double), st,
+    const auto route = r.T == 1 ? layer_route_kernel<1> : r.T <= kRouteTokens ? layer_route_kernel<kRouteTokens> : layer_route_kernel<0>;
+    hipLaunchKernelGGL(route, rg, dim3(kThreads), (size_t)rt * kWaves * kRouteExperts * sizeof(double), st,
                        r);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
