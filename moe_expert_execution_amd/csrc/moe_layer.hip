@@ -163,15 +163,17 @@ __device__ __forceinline__ double add_halves(double a, double b) {
 // (a single token's slices are added by the experts' launch: sending them on is
 // quicker than waiting for them here).
 //
-// Latency decides it: 4.9 us at one token and 128 experts, 9.9 at 16, 12.6 at 5 and
-// 256 experts of d = 4,096 (2.1 MB of router), of which the two waits for other
-// workgroups' numbers and the selection are more than half; 28 to 33 us for 64
-// tokens, 256 experts and d = 7,168 (0.23 GFLOP: 8 TFLOP/s in fp64, half of each
-// product's rows unused).
-//
 // NT: up to 8 tokens by vector FMAs instead (0: the matrix cores).  A lane sums its
 // rows and four experts for each token, and the four lane groups' sums are added
-// by exchanging halves.
+// by exchanging halves.  An fp64 matrix product takes the time of 16 tokens, 2,048
+// cycles for 32 rows and 64 experts, whatever there are: one token on 128 experts
+// takes 4.1 us and 4.9 with it, on 8 experts 2.9 and 4.7; 5 tokens on 256 experts
+// of d = 4,096 12.3 and 12.6.
+//
+// Latency decides those; of the 5 tokens' time more than half is the last
+// workgroup's: the slices (164 KB to one compute unit) and the selection.  16
+// tokens on 128 experts take 9.8 us, 64 on 256 experts of d = 7,168 28 to 33 (0.23
+// GFLOP: 8 TFLOP/s in fp64, half of each product's rows unused).
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 2) layer_route_kernel(RouteArgs a) {
     extern __shared__ __attribute__((aligned(16))) double zred[];
