@@ -418,8 +418,10 @@ __device__ __forceinline__ void adapt(Acc (&acc)[NX], const LoraView& lo, const 
 // One token through [2,048 x 2,048] bf16 takes 6.5 us, 2.4 of them the launch (8.4 MB;
 // latency); 64 tokens with 32 FP8 adapters of [4,096 x 4,096] 17.8: each workgroup
 // brings 0.13 MB of weights, 0.26 of x and some 0.1 of B to its compute unit, at
-// the 40 to 80 GB/s that one draws from L2, and there is a list, a staged v and a sum
-// over waves on the way.
+// the 40 to 80 GB/s that one draws from L2: 6.4 us until the first two units, v and
+// the list are in, 4.5 for the stream's other two, 3.4 for the adapters and 1.4 for
+// the sum over waves.  (v and the list loaded before the stream, or four steps of B
+// before it: 18.4 us and no change.)
 template <int FMT, int NM, int PL, int NX, bool FUSED>
 __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a) {
     extern __shared__ __attribute__((aligned(16))) float red[];
