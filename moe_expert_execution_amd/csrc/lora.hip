@@ -416,12 +416,13 @@ __device__ __forceinline__ void adapt(Acc (&acc)[NX], const LoraView& lo, const 
 // tile).  NM matrices share x; PL planes of x add up.
 //
 // One token through [2,048 x 2,048] bf16 takes 6.5 us, 2.4 of them the launch (8.4 MB;
-// latency); 64 tokens with 32 FP8 adapters of [4,096 x 4,096] 17.8: each workgroup
+// latency); 64 tokens with 32 FP8 adapters of [4,096 x 4,096] 16.9: each workgroup
 // brings 0.13 MB of weights, 0.26 of x and some 0.1 of B to its compute unit, at
 // the 40 to 80 GB/s that one draws from L2: 6.4 us until the first two units, v and
 // the list are in, 4.5 for the stream's other two, 3.4 for the adapters and 1.4 for
-// the sum over waves.  (v and the list loaded before the stream, or four steps of B
-// before it: 18.4 us and no change.)
+// the sum over waves, with two units in flight (17.3 us; three fit where one matrix
+// and one plane of x take part).  v and the list loaded before the stream took 1 us
+// more, four steps of B before it changed nothing.
 template <int FMT, int NM, int PL, int NX, bool FUSED>
 __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a) {
     extern __shared__ __attribute__((aligned(16))) float red[];
@@ -449,8 +450,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a
         PanelRef pr[NM];
 #pragma unroll
         for (int m = 0; m < NM; ++m) pr[m] = panel_ref<FMT>(a.codes[m], a.scales[m], a.K, p);
-        WUnit<FMT> w[2][NM];
-        XUnit x[2][NX][PL];
+        constexpr int D = NM * PL == 1 ? 3 : 2;        // units in flight
+        WUnit<FMT> w[D][NM];
+        XUnit x[D][NX][PL];
         auto load = [&](int b, int u) {
 #pragma unroll
             for (int m = 0; m < NM; ++m) load_unit<FMT>(w[b][m], pr[m], u0 + u, lane);
@@ -465,8 +467,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a
 #pragma unroll
             for (int m = 0; m < NM; ++m) mma_unit<FMT, NX, PL>(acc[m], w[b][m], x[b], nx);
         };
-        if (nu > 0) load(0, 0);
-        if (nu > 1) load(1, 1);
+#pragma unroll
+        for (int b = 0; b < D; ++b)
+            if (b < nu) load(b, b);
         uint16_t* vs[NM];
         int col[NM][NX], mine[NM];       // the columns' adapters; the wave's steps
         BStep first[NM];
@@ -497,23 +500,22 @@ __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a
                     }
             }
         }
-        for (int u = 0; u < nu; u += 2) {
-            work(0);
-            if (u + 2 < nu) load(0, u + 2);
-            if (u + 1 < nu) {
-                work(1);
-                if (u + 3 < nu) load(1, u + 3);
-            }
-        }
+        for (int u = 0; u < nu; u += D)
+#pragma unroll
+            for (int b = 0; b < D; ++b)
+                if (u + b < nu) {
+                    work(b);
+                    if (u + b + D < nu) load(b, u + b + D);
+                }
         if constexpr (!FUSED) {
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
                 if (mine[m] == 0) continue;
                 const LoraView& lo = a.lora[m];
-                constexpr int D = 4;
-                BStep bs[D];
+                constexpr int BD = 4;
+                BStep bs[BD];
                 expand<NX>(acc[m], first[m], steps[m][me], vs[m], lo.max_rank, col[m], lane);
-                pipelined<D>(
+                pipelined<BD>(
                     mine[m] - 1,
                     [&](int q, int i) { load_b(bs[q], lo, a.n, p, steps[m][me + (i + 1) * parts], lane); },
                     [&](int q, int i) {
