@@ -447,7 +447,11 @@ ft_status ft_workspace_destroy(ft_workspace* ws);
  *   always name experts of the layer; its token's w and y are NaN when it is
  *   chosen or x itself is NaN.
  * Everything is enqueued on `stream`; the call may be captured into a graph.
- * Results do not depend on timing: equal inputs give equal bits.
+ * Results do not depend on timing: equal inputs give equal bits.  Up to 16
+ * tokens the workgroups of one launch wait for each other; the wait is bounded
+ * (millions of polls, seconds), and a call whose wait runs out, which takes a
+ * workspace that another call uses at the same time, ends with NaN in the
+ * columns of y that it could not finish, and no error code.
  * Errors: FT_ERR_ARG (shape, T, null or misaligned pointers, stride, a
  * workspace that is too small or of another device than the current one or
  * the stream's), FT_ERR_HIP.

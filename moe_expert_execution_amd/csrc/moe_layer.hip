@@ -22,7 +22,6 @@ using namespace rs;
 constexpr int kShards = 8, kShardStep = 32;
 constexpr int kDrawn = 0, kDone = kShards * kShardStep;              // words of `hand`
 constexpr int kHandWords = 2 * kShards * kShardStep;
-constexpr uint32_t kMaxPolls = 1u << 22;      // seconds: only a workspace used by two calls at once gets there
 constexpr int kHandAt = 4096;                 // their place among the workspace's counters (after one per row panel)
 
 // ---- routing ----------------------------------------------------------------------
@@ -313,6 +312,7 @@ struct ExpertArgs {
     float* part;           // [splits][T][d] (splits > 1)
     uint32_t* counters;    // one per workgroup of row panels of WdT
     uint32_t* hand;        // the launch's hand-over counters, zero at its start
+    uint32_t polls, low_polls;   // bounds of the hand-over's wait (ft_workspace)
     int T, E, k, d, f, splits;
 };
 
@@ -449,10 +449,10 @@ __device__ __forceinline__ uint32_t draw(uint32_t* hand, int shard) {
 
 // One wave: waits until all numbers are done (returns -1), or returns a number
 // that it has drawn for an absent workgroup (>= 0), or gives up (-2).
-__device__ __forceinline__ int wait_done(uint32_t* hand, int n, int lane) {
+__device__ __forceinline__ int wait_done(uint32_t* hand, int n, uint32_t polls, int lane) {
     const int shard = lane & (kShards - 1);
     const uint32_t size = shard_size(shard, n);
-    for (uint32_t i = 0; i < kMaxPolls; ++i) {
+    for (uint32_t i = 0; i < polls; ++i) {
         const uint32_t drawn = __hip_atomic_load(hand + kDrawn + shard * kShardStep, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         const uint32_t done = __hip_atomic_load(hand + kDone + shard * kShardStep, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         if (__ballot(done < size) == 0) return -1;
@@ -637,7 +637,9 @@ constexpr int sum_row() { return 32 * NP + 4; }      // floats of a token's sums
 // order, and with several splits the panels' last workgroup adds the splits in
 // order, so y does not depend on timing.  wait(again) is called once, before h
 // is first read, with the first unit of weights on its way; where it has used
-// the registers meanwhile it calls again().  It returns whether h is there.
+// the registers meanwhile it calls again().  It returns whether h is there: where
+// it is not, the workgroup's part of y, or its partial sums, are NaN, so that y is
+// NaN whichever workgroup adds the splits.
 // 64 tokens on 256 MXFP4 experts: 1.7 GB in 323 to 354 us, 4.9 to 5.4 TB/s, the
 // rest being the splits' four rounds of grouping, 64 tokens' sums and partial sums.
 template <int FMT, int NX, int NP, typename Wait>
@@ -754,7 +756,7 @@ __device__ __forceinline__ void layer_down(const ExpertArgs& a, const Groups& g,
         auto emit = [&](int t, int n, float v) {
             const int64_t o = (int64_t)t * a.d + p0 * 32 + n;
             if (a.base) v += __uint_as_float((uint32_t)a.base[o] << 16);
-            a.y[o] = there ? f32_to_bf16_rne(v) : 0x7FC0;
+            a.y[o] = f32_to_bf16_rne(v);
         };
         constexpr int C = 32 * NP;
         for (int i = tid; i < a.T * C; i += kThreads) {
@@ -762,6 +764,7 @@ __device__ __forceinline__ void layer_down(const ExpertArgs& a, const Groups& g,
             float s = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) s += red[(w * a.T + t) * SR + n];
+            if (!there) s = __uint_as_float(0x7FC00000u);
             if (a.splits == 1) emit(t, n, s);
             else put_agent(a.part + ((int64_t)split * a.T + t) * a.d + p0 * 32 + n, s);
         }
@@ -818,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 2) layer_experts_kernel(ExpertArgs a
         auto poll = [&]() -> int {
             __syncthreads();
             if (wid == 0) {
-                const int r = wait_done(a.hand, grid, lane);
+                const int r = wait_done(a.hand, grid, (int)blockIdx.x < grid / 2 ? a.low_polls : a.polls, lane);
                 if (lane == 0) number = r;
             }
             __syncthreads();
@@ -1021,6 +1024,8 @@ hipError_t launch_layer(const ft_shape& s, const LayerArgs& la, ft_workspace* ws
     a.part = reinterpret_cast<float*>(m + b.part);
     a.counters = counters + kMaxLayerTokens;
     a.hand = counters + kHandAt;
+    a.polls = kMaxPolls;
+    a.low_polls = ws->low_polls;
     a.T = la.T;
     a.E = s.experts;
     a.k = s.top_k;

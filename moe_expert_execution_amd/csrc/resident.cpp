@@ -1,6 +1,8 @@
 // The C ABI of the operators over resident weights (include/ftmoe.h): the
 // workspace handle, argument validation and the enqueueing calls.  No C++
 // exception crosses the boundary.
+#include <stdlib.h>
+
 #include <new>
 
 #include "resident_api.h"
@@ -122,6 +124,8 @@ ft_status ft_workspace_create(size_t bytes, ft_workspace** out) {
         return FT_ERR_HIP;
     }
     ws->bytes = bytes;
+    ws->low_polls = kMaxPolls;
+    if (const char* v = getenv("FTMOE_LAYER_WAIT_POLLS")) ws->low_polls = (uint32_t)strtoul(v, nullptr, 10);
     ws->magic = kMagic;
     *out = ws;
     return FT_OK;

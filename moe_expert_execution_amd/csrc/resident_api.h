@@ -10,6 +10,10 @@ namespace ftmoe {
 constexpr size_t kCounterBytes = 64 << 10;
 constexpr int kMaxLayerTokens = 64;       // tokens of one ft_moe_layer call
 constexpr int kMaxRouteExperts = 256;     // experts of one ft_moe_layer call
+// Polls of the wait inside ft_moe_layer's one-launch form before a workgroup gives
+// up (its part of y is NaN then): seconds, where a hand-over takes microseconds.
+// Only a workspace used by two calls at once gets there.
+constexpr uint32_t kMaxPolls = 1u << 22;
 
 }  // namespace ftmoe
 
@@ -18,6 +22,8 @@ struct ft_workspace {
     size_t bytes;        // of the buffers after the counters
     int device;
     uint64_t magic;      // set while the handle is valid
+    // for tests: the bound in the lower half of the launch's workgroups (FTMOE_LAYER_WAIT_POLLS)
+    uint32_t low_polls;
 };
 
 namespace ftmoe {
