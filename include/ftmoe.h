@@ -488,6 +488,10 @@ ft_status ft_moe_layer(const ft_shape* shape, const uint16_t* x, const uint16_t*
  * rounded to bf16).  An adapter's weights reach only the
  * tokens that name it, and a token's result does not depend on the batch
  * around it beyond the order of fp32 sums.
+ * Block-FP8 products are summed as code times x, in fp32, and then take their
+ * block's scale, so those sums have to fit fp32 (|x| up to 2^112; up to 2^80
+ * above 64 tokens).  Above 64 tokens a block whose scale is zero, subnormal or
+ * below 2^-126 of the largest scale beside it along K may count as zeros.
  * T: 0..65535 (0 enqueues nothing).  x and the weights 16-byte aligned.  base
  * may be y; apart from that y may overlap nothing.  shape of ft_lora_expert:
  * d_model, d_ff and fmt are read.  Everything is enqueued on `stream`; calls
