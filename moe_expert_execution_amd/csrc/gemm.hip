@@ -693,30 +693,28 @@ hipError_t launch_gemm(ft_cache* c, const uint16_t* x, int T, hipStream_t st) {
 // K = 2,048 in 18 us; full tiles by MFMA: 8,192 tokens through [2,048 x 2,048] in 78 us
 // are 890 TFLOP/s, the MXFP4 expert of 7,168 x 2,048 on 4,096 tokens 1,020.
 template <int FMT, bool GU>
-void launch_lora_fmt(const LoraGemmArgs& a, hipStream_t st) {
+hipError_t launch_lora_fmt(const LoraGemmArgs& a, hipStream_t st) {
     const int cols = GU ? 2 * a.f : a.d;
     const int64_t full = (int64_t)((a.T + kBM - 1) / kBM) * ((cols + kBN - 1) / kBN);
     const bool half = full < 256;
     const int bm = half ? kBM / 2 : kBM, bn = half ? kBN / 2 : kBN;
     const dim3 grid((unsigned)(((a.T + bm - 1) / bm) * ((cols + bn - 1) / bn)));
-    if (half) hipLaunchKernelGGL((gemm_kernel<FMT, GU, LoraGemmArgs, 2>), grid, dim3(kGemmThreads), 0, st, a);
-    else hipLaunchKernelGGL((gemm_kernel<FMT, GU, LoraGemmArgs, 1>), grid, dim3(kGemmThreads), 0, st, a);
+    return launch(half ? gemm_kernel<FMT, GU, LoraGemmArgs, 2> : gemm_kernel<FMT, GU, LoraGemmArgs, 1>, grid, dim3(kGemmThreads),
+                  0, st, a);
 }
 
 template <int FMT>
-void launch_lora_fmt(const LoraGemmArgs& a, bool gu, hipStream_t st) {
-    if (gu) launch_lora_fmt<FMT, true>(a, st);
-    else launch_lora_fmt<FMT, false>(a, st);
+hipError_t launch_lora_fmt(const LoraGemmArgs& a, bool gu, hipStream_t st) {
+    return gu ? launch_lora_fmt<FMT, true>(a, st) : launch_lora_fmt<FMT, false>(a, st);
 }
 
 hipError_t launch_lora_gemm(int fmt, bool gu, const LoraGemmArgs& a, hipStream_t st) {
     switch (fmt) {
-        case FT_FMT_BF16: launch_lora_fmt<FT_FMT_BF16>(a, gu, st); break;
-        case FT_FMT_FP8_B128: launch_lora_fmt<FT_FMT_FP8_B128>(a, gu, st); break;
-        case FT_FMT_MXFP4_B32: launch_lora_fmt<FT_FMT_MXFP4_B32>(a, gu, st); break;
-        default: return hipErrorInvalidValue;
+        case FT_FMT_BF16: return launch_lora_fmt<FT_FMT_BF16>(a, gu, st);
+        case FT_FMT_FP8_B128: return launch_lora_fmt<FT_FMT_FP8_B128>(a, gu, st);
+        case FT_FMT_MXFP4_B32: return launch_lora_fmt<FT_FMT_MXFP4_B32>(a, gu, st);
     }
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 
 }  // namespace ftmoe

@@ -700,17 +700,14 @@ hipError_t launch_shrink(const ShrinkArgs& s, const Shrink& sh, hipStream_t st) 
                    : sh.span > kTile ? lora_shrink_kernel<1, 4, 2 * kTile, 1>
                    : sh.per == 1     ? lora_shrink_kernel<1, 2, kTile, 1>
                                      : lora_shrink_kernel<1, 2, kTile, 2>;
-    hipLaunchKernelGGL(f, grid, dim3(kThreads), lds, st, s);
-    return hipGetLastError();
+    return launch(f, grid, dim3(kThreads), lds, st, s);
 }
 
 template <int FMT, int NM, int PL, bool FUSED>
-void launch_project_nx(const ProjectArgs& a, hipStream_t st) {
+hipError_t launch_project_nx(const ProjectArgs& a, hipStream_t st) {
     const dim3 grid(a.n / 32, a.splits + a.lsplits * NM, (a.T + kTile - 1) / kTile);
-    if (a.T <= kCols)
-        hipLaunchKernelGGL((lora_project_kernel<FMT, NM, PL, 1, FUSED>), grid, dim3(kThreads), lds_bytes<FUSED>(a), st, a);
-    else
-        hipLaunchKernelGGL((lora_project_kernel<FMT, NM, PL, 2, FUSED>), grid, dim3(kThreads), lds_bytes<FUSED>(a), st, a);
+    const auto f = a.T <= kCols ? lora_project_kernel<FMT, NM, PL, 1, FUSED> : lora_project_kernel<FMT, NM, PL, 2, FUSED>;
+    return launch(f, grid, dim3(kThreads), lds_bytes<FUSED>(a), st, a);
 }
 
 // Prompts go through the GEMM tiles (gemm.hip).  A GEMM workgroup's time is that
@@ -731,12 +728,11 @@ bool gemm_fits(int T, int64_t rounds, int64_t most, int K, const void* y, const 
 template <int NM, int PL, bool FUSED>
 hipError_t launch_project_as(int fmt, const ProjectArgs& a, hipStream_t st) {
     switch (fmt) {
-        case FT_FMT_BF16: launch_project_nx<FT_FMT_BF16, NM, PL, FUSED>(a, st); break;
-        case FT_FMT_FP8_B128: launch_project_nx<FT_FMT_FP8_B128, NM, PL, FUSED>(a, st); break;
-        case FT_FMT_MXFP4_B32: launch_project_nx<FT_FMT_MXFP4_B32, NM, PL, FUSED>(a, st); break;
-        default: return hipErrorInvalidValue;
+        case FT_FMT_BF16: return launch_project_nx<FT_FMT_BF16, NM, PL, FUSED>(a, st);
+        case FT_FMT_FP8_B128: return launch_project_nx<FT_FMT_FP8_B128, NM, PL, FUSED>(a, st);
+        case FT_FMT_MXFP4_B32: return launch_project_nx<FT_FMT_MXFP4_B32, NM, PL, FUSED>(a, st);
     }
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 template <int NM, int PL>
 hipError_t launch_project(int fmt, const ProjectArgs& a, bool fuse, hipStream_t st) {

@@ -930,9 +930,7 @@ hipError_t launch_fmt(const ft_shape& s, const RouteArgs& r, const ExpertArgs& a
     // the waves' partial logits, then whole rows
     static_assert(kWaves * kRouteExperts >= kMaxRouteExperts, "a token's logits fit its partial sums' place");
     const auto route = r.T == 1 ? layer_route_kernel<1> : r.T <= kRouteTokens ? layer_route_kernel<kRouteTokens> : layer_route_kernel<0>;
-    hipLaunchKernelGGL(route, rg, dim3(kThreads), (size_t)rt * kWaves * kRouteExperts * sizeof(double), st,
-                       r);
-    hipError_t e = hipGetLastError();
+    hipError_t e = launch(route, rg, dim3(kThreads), (size_t)rt * kWaves * kRouteExperts * sizeof(double), st, r);
     if (e != hipSuccess) return e;
 
     const int R = a.T * a.k;
@@ -949,25 +947,20 @@ hipError_t launch_fmt(const ft_shape& s, const RouteArgs& r, const ExpertArgs& a
         const size_t lds = glds > dlds ? glds : dlds;
         if (a.T == 1) {
             const size_t z = kMaxRouteExperts * sizeof(double);
-            hipLaunchKernelGGL((layer_experts_kernel<FMT, 1, true>), grid, dim3(kThreads), lds > z ? lds : z, st, a);
-        } else if (FMT == FT_FMT_MXFP4_B32 && np == 2) {
-            hipLaunchKernelGGL((layer_experts_kernel<FMT, FMT == FT_FMT_MXFP4_B32 ? 2 : 1, false>), grid, dim3(kThreads), lds,
-                               st, a);
-        } else {
-            hipLaunchKernelGGL((layer_experts_kernel<FMT, 1, false>), grid, dim3(kThreads), lds, st, a);
+            return launch(layer_experts_kernel<FMT, 1, true>, grid, dim3(kThreads), lds > z ? lds : z, st, a);
         }
-        return hipGetLastError();
+        const auto f = np == 2 ? layer_experts_kernel<FMT, FMT == FT_FMT_MXFP4_B32 ? 2 : 1, false>
+                               : layer_experts_kernel<FMT, 1, false>;
+        return launch(f, grid, dim3(kThreads), lds, st, a);
     }
     const bool narrow = narrow_tiles(s, a.T);
     const auto gu = narrow ? layer_gateup_kernel<FMT, 1> : layer_gateup_kernel<FMT, 2>;
-    hipLaunchKernelGGL(gu, blocks(items), dim3(kThreads), glds, st, a);
-    e = hipGetLastError();
+    e = launch(gu, blocks(items), dim3(kThreads), glds, st, a);
     if (e != hipSuccess) return e;
     constexpr int P2 = FMT == FT_FMT_MXFP4_B32 ? 2 : 1;
     const auto dn = narrow ? (np == 2 ? layer_down_kernel<FMT, 1, P2> : layer_down_kernel<FMT, 1, 1>)
                            : (np == 2 ? layer_down_kernel<FMT, 2, P2> : layer_down_kernel<FMT, 2, 1>);
-    hipLaunchKernelGGL(dn, dim3((unsigned)ditems), dim3(kThreads), dlds, st, a);
-    return hipGetLastError();
+    return launch(dn, dim3((unsigned)ditems), dim3(kThreads), dlds, st, a);
 }
 
 }  // namespace

@@ -28,6 +28,15 @@ struct ft_workspace {
 
 namespace ftmoe {
 
+// Launches f(a) and returns the launch's own status: hipGetLastError() after it
+// would also report, and take away, an error that an earlier call of the
+// program left behind, and the launches after this one would be left out.
+template <typename A>
+hipError_t launch(void (*f)(A), dim3 grid, dim3 block, size_t lds, hipStream_t st, const A& a) {
+    void* args[] = {const_cast<A*>(&a)};
+    return hipLaunchKernel(reinterpret_cast<const void*>(f), grid, block, args, lds, st);
+}
+
 struct LayerArgs {
     const uint16_t* x;
     const uint16_t* wr;
