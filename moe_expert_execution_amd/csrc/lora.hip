@@ -786,27 +786,26 @@ size_t lora_project_call_bytes(int n, int K, int max_rank, int T) {
 }
 size_t lora_expert_call_bytes(const ft_shape& s, int max_rank, int T) { return expert_buffers(s, max_rank, T).total; }
 
-// The largest need of any call of up to max_tokens tokens: the partial sums
-// shrink when a call's tiles alone fill the card, so every tile count up to
-// that point is looked at.
-size_t lora_project_workspace(int n, int K, int max_rank, int max_tokens) {
-    size_t most = 0;
-    for (int T = 1;; T = T + kTile < max_tokens ? (T / kTile + 1) * kTile : max_tokens) {
-        const size_t b = lora_project_call_bytes(n, K, max_rank, T);
+// The largest need of any call of up to max_tokens tokens.  A call's need grows
+// with its tokens while the number of tiles stays, and may shrink from one number
+// to the next, as the partial sums do when the tiles alone fill the card: so the
+// last token count of each number is looked at.
+template <typename F>
+size_t largest_need(int max_tokens, F&& call_bytes) {
+    size_t most = call_bytes(max_tokens);
+    for (int T = kTile; T < max_tokens; T += kTile) {
+        const size_t b = call_bytes(T);
         most = b > most ? b : most;
-        if (T >= max_tokens) break;
     }
     return most;
 }
 
+size_t lora_project_workspace(int n, int K, int max_rank, int max_tokens) {
+    return largest_need(max_tokens, [&](int T) { return lora_project_call_bytes(n, K, max_rank, T); });
+}
+
 size_t lora_expert_workspace(const ft_shape& s, int max_rank, int max_tokens) {
-    size_t most = 0;
-    for (int T = 1;; T = T + kTile < max_tokens ? (T / kTile + 1) * kTile : max_tokens) {
-        const size_t b = lora_expert_call_bytes(s, max_rank, T);
-        most = b > most ? b : most;
-        if (T >= max_tokens) break;
-    }
-    return most;
+    return largest_need(max_tokens, [&](int T) { return lora_expert_call_bytes(s, max_rank, T); });
 }
 
 namespace {

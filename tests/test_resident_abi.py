@@ -131,3 +131,19 @@ def test_lora_workspace_covers_fewer_tokens():
     assert all(b >= a > 0 for a, b in zip(sizes, sizes[1:]))
     assert M.ft_lora_expert_workspace(s, 8, 4) == 0 and M.ft_lora_expert_workspace(s, 16, 0) == 0
     assert M.ft_lora_project_workspace(M.matrix(100, 128, "bf16", 16), 16, 4) == 0
+
+
+@pytest.mark.parametrize("rank", [0, 16, 128])
+def test_lora_workspace_at_every_tile_border(rank):
+    """The same where the second tile of tokens takes a call's splits away (more row panels, or long K), and the
+    fewest tokens of a tile are queried right after the most of the one before."""
+    tokens = [1, 2, 31, 32, 33, 34, 63, 64, 65, 66, 96, 97, 128, 129, 1024, 1025]
+    for n in (256, 384, 1024, 2048, 4096, 4224, 8192, 32768):
+        for K in (128, 1024, 2048, 4096, 8192, 32768):
+            m = M.matrix(n, K, "bf16", 16)
+            sizes = [M.ft_lora_project_workspace(m, rank, t) for t in tokens]
+            assert sizes == sorted(sizes) and sizes[0] > 0, (n, K, dict(zip(tokens, sizes)))
+            if K <= 8192 and n <= 8192:
+                s = M.shape(1, 1, 1, n, K, "bf16")
+                sizes = [M.ft_lora_expert_workspace(s, rank, t) for t in tokens]
+                assert sizes == sorted(sizes) and sizes[0] > 0, (n, K, dict(zip(tokens, sizes)))
