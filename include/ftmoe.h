@@ -422,7 +422,9 @@ ft_status ft_cache_read_slot(const ft_cache* cache, int64_t slot, void* dst);
  * on one stream, or order them by events; a captured graph keeps using the
  * workspace it was captured with, so two graphs that may run at the same time
  * need two.  Synchronises.  Errors: FT_ERR_ARG, FT_ERR_NOMEM, FT_ERR_HIP.
- * ft_workspace_destroy synchronises; NULL is accepted.
+ * ft_workspace_destroy synchronises the workspace's device, whichever is
+ * current; NULL is accepted, and a handle that is no live workspace is refused
+ * (FT_ERR_ARG), there and in the calls that take one.
  * ------------------------------------------------------------------------- */
 typedef struct ft_workspace ft_workspace;
 ft_status ft_workspace_create(size_t bytes, ft_workspace** out);

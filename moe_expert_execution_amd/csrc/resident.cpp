@@ -3,6 +3,7 @@
 // exception crosses the boundary.
 #include <stdlib.h>
 
+#include <mutex>
 #include <new>
 
 #include "resident_api.h"
@@ -11,14 +12,35 @@ using namespace ftmoe;
 
 namespace {
 
-constexpr uint64_t kMagic = 0x66746D6F65777331ull;
+// The live workspaces.  A handle is looked up here before it is read, so that a
+// destroyed one is told by its address alone.
+std::mutex g_live_mutex;
+ft_workspace* g_live = nullptr;
+
+bool is_live(const ft_workspace* ws) {
+    std::lock_guard<std::mutex> lock(g_live_mutex);
+    const ft_workspace* p = g_live;
+    while (p && p != ws) p = p->next;
+    return p != nullptr;
+}
+
+// Takes a live workspace out of the list; false if it is none.
+bool unlink_live(ft_workspace* ws) {
+    std::lock_guard<std::mutex> lock(g_live_mutex);
+    for (ft_workspace** p = &g_live; *p; p = &(*p)->next)
+        if (*p == ws) {
+            *p = ws->next;
+            return true;
+        }
+    return false;
+}
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // The device the workspace lives on has to be current and own the stream.
 ft_status check_workspace(const ft_workspace* ws, size_t need, void* stream) {
     FT_REQUIRE(ws, "workspace is null");
-    FT_REQUIRE(ws->magic == kMagic, "not a workspace (or a destroyed one)");
+    FT_REQUIRE(is_live(ws), "not a workspace (or a destroyed one)");
     FT_REQUIRE(need <= ws->bytes, "workspace holds %zu bytes; this call needs %zu", ws->bytes, need);
     int dev = -1;
     FT_HIP(hipGetDevice(&dev));
@@ -126,7 +148,11 @@ ft_status ft_workspace_create(size_t bytes, ft_workspace** out) {
     ws->bytes = bytes;
     ws->low_polls = kMaxPolls;
     if (const char* v = getenv("FTMOE_LAYER_WAIT_POLLS")) ws->low_polls = (uint32_t)strtoul(v, nullptr, 10);
-    ws->magic = kMagic;
+    {
+        std::lock_guard<std::mutex> lock(g_live_mutex);
+        ws->next = g_live;
+        g_live = ws;
+    }
     *out = ws;
     return FT_OK;
 }
@@ -134,12 +160,21 @@ ft_status ft_workspace_create(size_t bytes, ft_workspace** out) {
 ft_status ft_workspace_destroy(ft_workspace* ws) {
     clear_error();
     if (!ws) return FT_OK;
-    FT_REQUIRE(ws->magic == kMagic, "not a workspace (or a destroyed one)");
-    ws->magic = 0;
+    FT_REQUIRE(unlink_live(ws), "not a workspace (or a destroyed one)");
     void* mem = ws->mem;
+    const int device = ws->device;
     delete ws;
-    FT_HIP(hipDeviceSynchronize());
-    FT_HIP(hipFree(mem));
+    // calls that use it run on its own device, whichever is current
+    int dev = device;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess && dev != device) e = hipSetDevice(device);
+    if (e == hipSuccess) e = hipDeviceSynchronize();
+    if (e == hipSuccess) e = hipFree(mem);
+    if (dev != device) {
+        const hipError_t back = hipSetDevice(dev);
+        if (e == hipSuccess) e = back;
+    }
+    FT_HIP(e);
     return FT_OK;
 }
 

@@ -21,7 +21,7 @@ struct ft_workspace {
     uint8_t* mem;
     size_t bytes;        // of the buffers after the counters
     int device;
-    uint64_t magic;      // set while the handle is valid
+    ft_workspace* next;  // in the list of live workspaces (resident.cpp)
     // for tests: the bound in the lower half of the launch's workgroups (FTMOE_LAYER_WAIT_POLLS)
     uint32_t low_polls;
 };
