@@ -422,6 +422,8 @@ ft_status ft_cache_read_slot(const ft_cache* cache, int64_t slot, void* dst);
  * on one stream, or order them by events; a captured graph keeps using the
  * workspace it was captured with, so two graphs that may run at the same time
  * need two.  Synchronises.  Errors: FT_ERR_ARG, FT_ERR_NOMEM, FT_ERR_HIP.
+ * The calls' `stream` is NULL (the default stream) or a created stream of the
+ * workspace's device; hipStreamLegacy and hipStreamPerThread are refused.
  * ft_workspace_destroy synchronises the workspace's device, whichever is
  * current; NULL is accepted, and a handle that is no live workspace is refused
  * (FT_ERR_ARG), there and in the calls that take one.

@@ -42,6 +42,10 @@ ft_status check_workspace(const ft_workspace* ws, size_t need, void* stream) {
     FT_REQUIRE(ws, "workspace is null");
     FT_REQUIRE(is_live(ws), "not a workspace (or a destroyed one)");
     FT_REQUIRE(need <= ws->bytes, "workspace holds %zu bytes; this call needs %zu", ws->bytes, need);
+    // The runtime's two handles that are no stream objects: a call with one of them,
+    // asked about its device or launched on, has ended the process.
+    FT_REQUIRE(stream != hipStreamLegacy && stream != hipStreamPerThread,
+               "stream must be NULL or a created stream, not hipStreamLegacy or hipStreamPerThread");
     int dev = -1;
     FT_HIP(hipGetDevice(&dev));
     if (stream) {

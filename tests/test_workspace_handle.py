@@ -1,6 +1,7 @@
 """The workspace handle (csrc/resident.cpp) over a stand-in for the HIP runtime with two devices: destroying waits for
-and frees on the workspace's own device, leaves the current one as it was, and never reads a destroyed handle.  A small
-harness includes the source, compiled as the library compiles it.  CPU only."""
+and frees on the workspace's own device, leaves the current one as it was, and never reads a destroyed handle; the
+runtime is not asked about handles that are no stream objects.  A small harness includes the source, compiled as the
+library compiles it.  CPU only."""
 import os
 import subprocess
 
@@ -106,6 +107,13 @@ int main(int argc, char** argv) {
         CHECK(layer(b, nullptr) == FT_OK);
         CHECK(ft_workspace_destroy(b) == FT_OK && ft_workspace_destroy(nullptr) == FT_OK);
         CHECK(layer(b, nullptr) == FT_ERR_ARG && ftmoe::calls == 1);
+    } else if (!strcmp(what, "special")) {
+        for (long h = 1; h <= 2; ++h)
+            for (auto call : {layer, project, expert}) {
+                CHECK(call(a, (void*)h) == FT_ERR_ARG && strstr(ftmoe::err, "created stream"));
+                CHECK(call(a, nullptr) == FT_OK);
+            }
+        CHECK(ftmoe::calls == 6);
     }
     printf("ok\n");
     return 0;
@@ -123,7 +131,7 @@ def harness(tmp_path_factory):
     return str(exe)
 
 
-@pytest.mark.parametrize("what", ["device", "destroyed"])
+@pytest.mark.parametrize("what", ["device", "destroyed", "special"])
 def test_workspace(harness, what):
     r = subprocess.run([harness, what], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout == "ok\n", (r.returncode, r.stdout)
