@@ -313,6 +313,7 @@ struct ExpertArgs {
     uint32_t* counters;    // one per workgroup of row panels of WdT
     uint32_t* hand;        // the launch's hand-over counters, zero at its start
     uint32_t polls, low_polls;   // bounds of the hand-over's wait (ft_workspace)
+    int absent;                  // odd workgroups draw no number when they start (ft_workspace)
     int T, E, k, d, f, splits;
 };
 
@@ -803,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 2) layer_experts_kernel(ExpertArgs a
     const int grid = gridDim.x;
     if (tid == 0) {
         const int shard = blockIdx.x % kShards;
-        const uint32_t v = draw(a.hand, shard);
+        const uint32_t v = a.absent && (blockIdx.x & 1) ? ~0u : draw(a.hand, shard);
         number = v < shard_size(shard, grid) ? (int)v * kShards + shard : -1;
     }
     if constexpr (ONE) {
@@ -1019,6 +1020,7 @@ hipError_t launch_layer(const ft_shape& s, const LayerArgs& la, ft_workspace* ws
     a.hand = counters + kHandAt;
     a.polls = kMaxPolls;
     a.low_polls = ws->low_polls;
+    a.absent = ws->absent;
     a.T = la.T;
     a.E = s.experts;
     a.k = s.top_k;

@@ -152,6 +152,7 @@ ft_status ft_workspace_create(size_t bytes, ft_workspace** out) {
     ws->bytes = bytes;
     ws->low_polls = kMaxPolls;
     if (const char* v = getenv("FTMOE_LAYER_WAIT_POLLS")) ws->low_polls = (uint32_t)strtoul(v, nullptr, 10);
+    if (const char* v = getenv("FTMOE_LAYER_ABSENT")) ws->absent = atoi(v) != 0;
     {
         std::lock_guard<std::mutex> lock(g_live_mutex);
         ws->next = g_live;

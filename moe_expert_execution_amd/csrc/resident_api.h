@@ -24,6 +24,8 @@ struct ft_workspace {
     ft_workspace* next;  // in the list of live workspaces (resident.cpp)
     // for tests: the bound in the lower half of the launch's workgroups (FTMOE_LAYER_WAIT_POLLS)
     uint32_t low_polls;
+    // for tests: odd workgroups leave their gate/up numbers to those that wait (FTMOE_LAYER_ABSENT)
+    int absent;
 };
 
 namespace ftmoe {

@@ -23,7 +23,7 @@ def layer_with(monkeypatch, name, value, cfg, max_tokens, recs):
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "mxfp4"])
 @pytest.mark.parametrize("T", [1, 5, 16])
-@pytest.mark.parametrize("d,f,E,k,whole", [(2048, 768, 32, 8, True), (8192, 128, 8, 2, False)])
+@pytest.mark.parametrize("d,f,E,k,whole", [(2048, 768, 16, 8, True), (8192, 128, 8, 2, False)])
 def test_wait_that_runs_out_leaves_nan(monkeypatch, fmt, T, d, f, E, k, whole):
     """The lower half of the workgroups gives up its wait at once (FTMOE_LAYER_WAIT_POLLS=0).  Where row panels have
     several splits (d = 2,048: the lower half holds some of each panel's) y is NaN everywhere, whoever adds the
@@ -47,3 +47,23 @@ def test_wait_that_runs_out_leaves_nan(monkeypatch, fmt, T, d, f, E, k, whole):
             np.testing.assert_array_equal(nan, np.broadcast_to(np.arange(d) < d // 2, (T, d)))
             np.testing.assert_array_equal(y[~nan], oy[~nan])
     check(low, synth.tokens(cfg, 40, 0), what="three launches over the same workspace")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 2, 5, 16])
+@pytest.mark.parametrize("d,f,E,k", [(2048, 768, 16, 8), (256, 640, 8, 2), (8192, 128, 8, 2)])
+def test_waiting_workgroups_do_the_work_of_absent_ones(monkeypatch, fmt, T, d, f, E, k):
+    """Odd workgroups draw no gate/up number when they start (FTMOE_LAYER_ABSENT): half of the numbers, whose counters
+    nobody else draws from at first, are found and done by workgroups that wait, and each of those loads its first down
+    weights again.  The bits are those of the ordinary call; MXFP4 from 32 routes on has two row panels."""
+    cfg = config(fmt, d, f, E, k, seed=42)
+    recs = synth.bank(cfg)
+    ordinary = Layer(cfg, T, recs)
+    absent = layer_with(monkeypatch, "FTMOE_LAYER_ABSENT", "1", cfg, T, recs)
+    for i in range(3):
+        x = synth.tokens(cfg, T, T, i)
+        base = synth.tokens(cfg, T, T, i, 1) if i else None
+        if i == 0:
+            check(ordinary, x, base, f"{fmt} T={T}")
+        for got, want in zip(absent(x, base), ordinary(x, base)):
+            np.testing.assert_array_equal(got, want)
