@@ -15,17 +15,14 @@
 // that path (the layer's down product over MXFP4, 64 tokens on 256 experts,
 // ran at a fifth of the card's bandwidth with 32 columns).
 #pragma once
+#include "lora_rules.h"
 #include "resident_api.h"
 #include "wfmt.h"
 
 namespace ftmoe {
 namespace rs {
 
-constexpr int kWaves = 8;                 // waves of a streaming workgroup, splitting K
 constexpr int kThreads = kWaves * 64;
-constexpr int kUnit = 128;                // elements along K per unit (one fp8 scale block)
-constexpr int kCols = 16;                 // tokens of one operand
-constexpr int kTile = 2 * kCols;          // tokens of one tile: at most two operands
 
 template <int FMT>
 struct Panel {
