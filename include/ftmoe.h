@@ -476,7 +476,8 @@ ft_status ft_moe_layer(const ft_shape* shape, const uint16_t* x, const uint16_t*
  *   where one is taken) means no adapters.
  * adapter [T] int32, device: the adapter of each token; any value outside
  *   0..count-1 means none.  Tokens of one adapter need not be neighbours, but
- *   an adapter is read once per 32 consecutive tokens that name it.
+ *   an adapter's weights are read again for every 32 to 128 consecutive tokens
+ *   among which it is named.
  *   May be NULL when the call has no adapters.
  *
  * ft_lora_project:
@@ -488,10 +489,12 @@ ft_status ft_moe_layer(const ft_shape* shape, const uint16_t* x, const uint16_t*
  *   h[t] = silu(x Wg + lora_gate(x)) * (x Wu + lora_up(x)),
  *   y[t] = base[t] + h Wd + lora_down(h).
  * fp32 sums, one bf16 rounding of y; the x A products keep 16 significant
- * bits in between, and so does h up to 64 tokens (above that it may be
- * rounded to bf16).  An adapter's weights reach only the
- * tokens that name it, and a token's result does not depend on the batch
- * around it beyond the order of fp32 sums.
+ * bits in between, and so does h up to 64 tokens.  Above that h is rounded to
+ * bf16 where the call goes through matrix-core tiles, which the shape, T and
+ * whether y and base are 16-byte aligned decide.  An adapter's weights reach
+ * only the tokens that name it.  The values of other tokens do not reach a
+ * token's result; their number and adapters do, by the order of fp32 sums, and
+ * their number by that rounding of h.
  * Block-FP8 products are summed as code times x, in fp32, and then take their
  * block's scale, so those sums have to fit fp32 (|x| up to 2^112; up to 2^80
  * above 64 tokens).  Above 64 tokens a block whose scale is zero, subnormal or

@@ -2,13 +2,15 @@
 //
 //   y[t] = base[t] + x[t] W^T + s_a (x[t] A_a^T) B_a^T,   a = adapter[t],
 //
-// and a SwiGLU expert whose three projections carry adapters.  W is read
-// once for all requests; an adapter's A [r x K] and B [n x r] are read once
-// per 32 tokens that name it.  The first launch computes v = s_a x A_a^T
-// (r <= 128 values per token), the second streams W and adds v B_a^T to its
-// accumulators.  The expert FFN reads one complete record ("The Expert Cache
-// That Follows the Router", section "One logical expert, two physical levels
-// of memory").
+// and a SwiGLU expert whose three projections carry adapters.  Up to 32 tokens
+// read W once for all requests, longer calls once per tile of 32 tokens (the
+// prompts' GEMM: of 64 or 128); an adapter's A [r x K] and B [n x r] are read
+// once per tile, or span of up to 64 tokens, that names it.  The first launch
+// computes v = s_a x A_a^T (r <= 128 values per token), the second streams W
+// and adds v B_a^T to its accumulators.  With few adapters one launch does
+// both, and each panel of 32 rows of W reads their A again.  The expert FFN
+// reads one complete record ("The Expert Cache That Follows the Router",
+// section "One logical expert, two physical levels of memory").
 #include "lora_rules.h"
 #include "resident.h"
 
@@ -421,7 +423,9 @@ __device__ __forceinline__ void adapt(Acc (&acc)[NX], const LoraView& lo, const 
 // the list are in, 4.5 for the stream's other two, 3.4 for the adapters and 1.4 for
 // the sum over waves, with two units in flight (17.3 us; three fit where one matrix
 // and one plane of x take part).  v and the list loaded before the stream took 1 us
-// more, four steps of B before it changed nothing.
+// more, four steps of B before it changed nothing.  The bf16 pair of matrices over
+// two operands behind a shrink launch (an expert's gate and up for more than 16
+// tokens of many adapters) spills 43 registers.
 template <int FMT, int NM, int PL, int NX, bool FUSED>
 __global__ void __launch_bounds__(kThreads, 2) lora_project_kernel(ProjectArgs a) {
     extern __shared__ __attribute__((aligned(16))) float red[];

@@ -4,9 +4,9 @@
 //   y[t] = base[t] + sum_j w[t, j] FFN_{ids[t, j]}(x[t]),
 //   FFN(x) = (silu(x Wg) * (x Wu)) Wd.
 //
-// The experts' records are read once each from where they lie (E records,
-// `stride` bytes apart); no control step, no planner and no host branch takes
-// part.  The router picks k of the layer's experts per token ("Making Large
+// The experts' records are read from where they lie (E records, `stride` bytes
+// apart), once per tile of 16 or 32 of their routes; no control step, no planner
+// and no host branch takes part.  The router picks k of the layer's experts per token ("Making Large
 // MoE Models Practical on a Single Machine", section 1); the expert FFN reads
 // a complete layer-expert record ("The Expert Cache That Follows the Router",
 // section "One logical expert, two physical levels of memory").
@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 2) layer_down_kernel(ExpertArgs a) {
 }
 
 // Tiles of 16 routes instead of 32 (more than 16 tokens).  The second operand
-// costs registers (28 spilled in MXFP4's down, 21 in bf16) whether a tile fills it
+// costs registers (28 spilled in MXFP4's down, 21 in bf16, 6 in FP8) whether a tile fills it
 // or not: 64 tokens on 256 MXFP4 experts (2 routes each) take 930 us and 1,085
 // with 32, 64 on 128 bf16 experts (4) 199 and 235, 64 on 8 (16) 41 and 43.  An
 // expert with more than 16 routes reads its weights again, from L2 at best: with

@@ -8,9 +8,10 @@
 // bf16 in registers, exact for e4m3 and for e2m1 times a power of two); a load
 // is four runs of 256 bytes.  Up to 16 tokens are the B operand: lane l holds
 // token l % 16 at the same K positions, read from memory (L2).  So a panel
-// streams from HBM once whatever the token count, and lane l ends with token
-// l % 16 and rows 4 (l / 16) .. + 3 of each half.  16 columns and not 32: a
-// token load returns 1 KiB to the lanes whatever its rows hold, at 64 bytes
+// streams from HBM once for the tokens of one tile, of one or two operands (32
+// tokens, or an expert's routes in the layer); the next tile of the same rows
+// streams it again.  Lane l ends with token l % 16 and rows 4 (l / 16) .. + 3 of
+// each half.  16 columns and not 32: a token load returns 1 KiB to the lanes whatever its rows hold, at 64 bytes
 // per cycle and CU, so narrower tiles halve what stands beside the weights on
 // that path (the layer's down product over MXFP4, 64 tokens on 256 experts,
 // ran at a fifth of the card's bandwidth with 32 columns).
@@ -61,8 +62,8 @@ __device__ __forceinline__ int lane_unit(int lane) {
     return (g >> 1) * 64 + (g & 1) * 32 + (lane & 15);
 }
 
-// Weights are read once per call: non-temporal, so that they leave the caches
-// to the tokens and the partial sums.
+// Weights are read once per tile of tokens, mostly once per call: non-temporal, so
+// that they leave the caches to the tokens and the partial sums.
 template <int FMT>
 __device__ __forceinline__ void load_unit(WUnit<FMT>& u, const PanelRef& p, int unit, int lane) {
     constexpr int LPH = Panel<FMT>::LPH;
