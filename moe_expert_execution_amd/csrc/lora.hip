@@ -417,13 +417,13 @@ __device__ __forceinline__ void adapt(Acc (&acc)[NX], const LoraView& lo, const 
 // tile).  NM matrices share x; PL planes of x add up.
 //
 // One token through [2,048 x 2,048] bf16 takes 6.5 us, 2.4 of them the launch (8.4 MB;
-// latency); 64 tokens with 32 FP8 adapters of [4,096 x 4,096] 16.9: each workgroup
+// latency); 64 tokens with 32 FP8 adapters of [4,096 x 4,096] 16 to 17.3: each workgroup
 // brings 0.13 MB of weights, 0.26 of x and some 0.1 of B to its compute unit, at
 // the 40 to 80 GB/s that one draws from L2: 6.4 us until the first two units, v and
 // the list are in, 4.5 for the stream's other two, 3.4 for the adapters and 1.4 for
-// the sum over waves, with two units in flight (17.3 us; three fit where one matrix
-// and one plane of x take part).  v and the list loaded before the stream took 1 us
-// more, four steps of B before it changed nothing.  The bf16 pair of matrices over
+// the sum over waves, measured with two units in flight (three, which fit where one
+// matrix and one plane of x take part, took 0.4 us off the call on one box).  v and
+// the list loaded before the stream took 1 us more, four steps of B before it changed nothing.  The bf16 pair of matrices over
 // two operands behind a shrink launch (an expert's gate and up for more than 16
 // tokens of many adapters) spills 43 registers.
 template <int FMT, int NM, int PL, int NX, bool FUSED>
