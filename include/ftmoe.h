@@ -426,7 +426,9 @@ ft_status ft_cache_read_slot(const ft_cache* cache, int64_t slot, void* dst);
  * workspace's device; hipStreamLegacy and hipStreamPerThread are refused.
  * ft_workspace_destroy synchronises the workspace's device, whichever is
  * current; NULL is accepted, and a handle that is no live workspace is refused
- * (FT_ERR_ARG), there and in the calls that take one.
+ * (FT_ERR_ARG), there and in the calls that take one.  Where the device cannot
+ * be waited for (a stream capture that forbids it) it returns FT_ERR_HIP and the
+ * workspace stays valid.
  * ------------------------------------------------------------------------- */
 typedef struct ft_workspace ft_workspace;
 ft_status ft_workspace_create(size_t bytes, ft_workspace** out);

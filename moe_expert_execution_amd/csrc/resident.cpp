@@ -165,16 +165,17 @@ ft_status ft_workspace_create(size_t bytes, ft_workspace** out) {
 ft_status ft_workspace_destroy(ft_workspace* ws) {
     clear_error();
     if (!ws) return FT_OK;
-    FT_REQUIRE(unlink_live(ws), "not a workspace (or a destroyed one)");
-    void* mem = ws->mem;
-    const int device = ws->device;
-    delete ws;
+    FT_REQUIRE(is_live(ws), "not a workspace (or a destroyed one)");
     // calls that use it run on its own device, whichever is current
+    const int device = ws->device;
     int dev = device;
     hipError_t e = hipGetDevice(&dev);
     if (e == hipSuccess && dev != device) e = hipSetDevice(device);
     if (e == hipSuccess) e = hipDeviceSynchronize();
-    if (e == hipSuccess) e = hipFree(mem);
+    if (e == hipSuccess && unlink_live(ws)) {     // (a wait that was refused, as in a capture, leaves it as it was)
+        e = hipFree(ws->mem);
+        delete ws;
+    }
     if (dev != device) {
         const hipError_t back = hipSetDevice(dev);
         if (e == hipSuccess) e = back;

@@ -30,14 +30,14 @@ void* operator new(size_t n, const std::nothrow_t&) noexcept {
 void operator delete(void* p) noexcept { if (p) mprotect(p, 4096, PROT_NONE); }
 void operator delete(void* p, size_t) noexcept { if (p) mprotect(p, 4096, PROT_NONE); }
 
-static int current = 0, synced = -1, freed_on = -1, stream_device = 0;
+static int current = 0, synced = -1, freed_on = -1, stream_device = 0, busy = 0;
 extern "C" {
 hipError_t hipGetDevice(int* d) { *d = current; return hipSuccess; }
 hipError_t hipSetDevice(int d) { current = d; return d >= 0 && d < 2 ? hipSuccess : hipErrorInvalidDevice; }
 hipError_t hipMalloc(void** p, size_t n) { *p = malloc(64); return hipSuccess; }
 hipError_t hipFree(void* p) { freed_on = current; free(p); return hipSuccess; }
 hipError_t hipMemset(void*, int, size_t) { return hipSuccess; }
-hipError_t hipDeviceSynchronize() { synced = current; return hipSuccess; }
+hipError_t hipDeviceSynchronize() { synced = current; return busy ? hipErrorStreamCaptureUnsupported : hipSuccess; }
 hipError_t hipGetLastError() { return hipSuccess; }
 const char* hipGetErrorString(hipError_t) { return "error"; }
 hipError_t hipStreamGetDevice(hipStream_t s, hipDevice_t* d) {
@@ -107,6 +107,15 @@ int main(int argc, char** argv) {
         CHECK(layer(b, nullptr) == FT_OK);
         CHECK(ft_workspace_destroy(b) == FT_OK && ft_workspace_destroy(nullptr) == FT_OK);
         CHECK(layer(b, nullptr) == FT_ERR_ARG && ftmoe::calls == 1);
+    } else if (!strcmp(what, "capturing")) {      // a wait that the runtime refuses: nothing is freed, and it may be tried again
+        current = 0;
+        busy = 1;
+        CHECK(ft_workspace_destroy(a) == FT_ERR_HIP && freed_on == -1 && current == 0);
+        busy = 0;
+        current = 1;
+        CHECK(layer(a, nullptr) == FT_OK);
+        CHECK(ft_workspace_destroy(a) == FT_OK && freed_on == 1);
+        CHECK(ft_workspace_destroy(a) == FT_ERR_ARG);
     } else if (!strcmp(what, "special")) {
         for (long h = 1; h <= 2; ++h)
             for (auto call : {layer, project, expert}) {
@@ -131,7 +140,7 @@ def harness(tmp_path_factory):
     return str(exe)
 
 
-@pytest.mark.parametrize("what", ["device", "destroyed", "special"])
+@pytest.mark.parametrize("what", ["device", "destroyed", "capturing", "special"])
 def test_workspace(harness, what):
     r = subprocess.run([harness, what], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout == "ok\n", (r.returncode, r.stdout)
