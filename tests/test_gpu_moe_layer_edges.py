@@ -101,3 +101,35 @@ def test_records_further_apart_than_their_size():
         for a, b in zip(layer(synth.tokens(cfg, T, T)), ref):
             np.testing.assert_array_equal(a, b)
     assert np.isfinite(OF.bf16_to_f64(want[20][2])).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "mxfp4"])
+def test_two_and_three_launches_in_one_graph(fmt):
+    """Calls of 17, 64, 16 and 2 tokens captured one after the other over one workspace, in both of its forms."""
+    cfg = config(fmt, 640, 384, 24, 4, seed=35)
+    layer, eager = Layer(cfg, 64), Layer(cfg, 64)
+    Ts = (17, 64, 16, 2)
+    xds, outs = [dev_u16(synth.tokens(cfg, T, T)) for T in Ts], [layer.outputs(T) for T in Ts]
+
+    def all_four():
+        for xd, out in zip(xds, outs):
+            layer.enqueue(xd, out)
+
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        all_four()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        all_four()
+    for i in range(1, 5):
+        xs = [synth.tokens(cfg, T, T, i) for T in Ts]
+        for xd, x in zip(xds, xs):
+            xd.copy_(dev_u16(x))
+        g.replay()
+        torch.cuda.synchronize()
+        for x, out in zip(xs, outs):
+            ids, w, y = eager(x)
+            np.testing.assert_array_equal(out[0].cpu().numpy(), ids)
+            np.testing.assert_array_equal(out[1].cpu().numpy(), w)
+            np.testing.assert_array_equal(bits(out[2]), y)
