@@ -538,6 +538,226 @@ ft_status ft_lora_expert(const ft_shape* shape, const void* record, const ft_lor
                          const ft_lora* down, const uint16_t* x, const int32_t* adapter, int32_t T,
                          const uint16_t* base, uint16_t* y, ft_workspace* ws, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * What stands around the layer in a decoder step: a paged key-value cache in
+ * device memory (where its pages are, writing it, one new token per request
+ * attending over it) and the norms between blocks.
+ *
+ * Conventions of these four calls.  Everything is enqueued on `stream`: NULL
+ * (the default stream) or a created stream of the current device, on which all
+ * pointers have to be; hipStreamLegacy and hipStreamPerThread are refused.
+ * Nothing synchronises, allocates or waits for another workgroup, and every
+ * call may be captured into a graph.  The descriptors are read during the call
+ * only.  Equal inputs give equal bits.  Strides of q, k, v and out are in
+ * elements (a multiple of 8, so that rows stay 16-byte aligned).  No output may
+ * overlap an input or another output except where a call says so.
+ *
+ * ft_kv_cache — one layer's cache: `pages` pages of page_tokens tokens (16, 32,
+ *   64, 128 or 256) for kv_heads heads (1..1024) of head_dim values (64, 128 or
+ *   256), keys in k and values in v, page p of either at byte p * page_stride
+ *   (a multiple of 16, at least a page's bytes; page pools of several layers
+ *   may interleave).  Cache slot s is token s % page_tokens of page
+ *   s / page_tokens; pages * page_tokens is below 2^31.
+ *   fmt FT_KV_BF16, or FT_KV_E4M3: e4m3fn codes, value = code * scale of the
+ *   head (k_scale, v_scale: fp32 [kv_heads], device; NULL with FT_KV_BF16).
+ * Layout of a page: head h's part begins h * page_tokens * head_dim elements
+ *   in; inside it, each block of 16 tokens is contiguous and made of 16-byte
+ *   units.  Keys: unit c of token r of the block (the elements
+ *   c * ck .. + ck - 1, ck = 8 for bf16 and 16 for e4m3) is at unit index
+ *   c * 16 + r.  Values: a unit holds cv dimensions of tu consecutive tokens
+ *   (cv = 4 for head_dim 64, else 8; tu * cv elements fill 16 bytes), token
+ *   after token; the unit of token r and dimension e is at index
+ *   (r / tu) * (head_dim / cv) + e / cv.  So a wave's 64 loads of 16 bytes are
+ *   1 KiB runs of keys in matrix-core operand order, and whole rows of values.
+ * ------------------------------------------------------------------------- */
+enum { FT_KV_BF16 = 0, FT_KV_E4M3 = 1 };
+
+typedef struct {
+    int32_t pages;
+    int32_t page_tokens;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t fmt;             /* FT_KV_*                                          */
+    int32_t reserved;        /* 0                                                */
+    int64_t page_stride;     /* bytes                                            */
+    void* k;
+    void* v;
+    const float* k_scale;
+    const float* v_scale;
+} ft_kv_cache;
+
+/* ---------------------------------------------------------------------------
+ * ft_kv_plan — block tables and slot maps of a batch from its lengths, with the
+ * pages taken from and returned to a free list: the step before a layer's
+ * appends, all on the device.
+ * Request b (of `requests`, 0..4096; 0 enqueues nothing) holds context[b] tokens
+ * (clamped to 0..width * page_tokens) in the pages table[b][0 .. have - 1],
+ * have = ceil(context / page_tokens); table is [requests x width] (width
+ * 1..131072).  add[b] >= 0: it gets that many new tokens, add[b] < 0: it has
+ * ended and its pages go back.
+ * The free list is a stack: free_pages[0 .. *free_count - 1] of the `pages`
+ * entries of free_pages, and on top of them the pages of the ended requests in
+ * the order of their rows.  A request fits if its context + add stays within
+ * width * page_tokens and its tokens within the token rows (below); the pages
+ * that a fitting request lacks are counted in the order of the requests, and
+ * it is served if it lacks none or its count's running sum is within the
+ * stack.  Served requests take their pages from the top of the stack, in order,
+ * into table[b][have ..]; the others are refused and keep what they had.
+ * Token rows: `tokens` of them (0..65535, >= requests * row_tokens).
+ * row_tokens = 0: packed, request b's tokens follow request b - 1's (refused
+ * requests' too; an ended one has none).  row_tokens = n > 0: request b's are
+ * rows b * n .. b * n + add[b] - 1 (n = 1: a decode step of fixed shape).
+ * Out: kv_len [requests] = context + add if served, 0 if ended, else context (it
+ * may be context itself); start [requests + 1] the first token row of each
+ * request (at most `tokens`); slot, pos [tokens] the cache slot and the
+ * position of each token, both -1 in rows that no served token has (slot -1 also
+ * where the page's id in the table is outside 0..pages - 1);
+ * counts [4] = tokens served, pages taken, pages in the free list afterwards
+ * (free_pages holds them; entries past that are unspecified), requests refused.
+ * free_count may be counts + 2 of the call before, or of this call.
+ * The workspace is used for its arrival counters only: any size serves.
+ * Errors: FT_ERR_ARG, FT_ERR_HIP.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t requests;
+    int32_t pages;
+    int32_t page_tokens;
+    int32_t width;
+    int32_t tokens;
+    int32_t row_tokens;
+    const int32_t* context;
+    const int32_t* add;
+    int32_t* table;
+    int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t* kv_len;
+    int32_t* start;
+    int32_t* slot;
+    int32_t* pos;
+    int32_t* counts;
+} ft_kv_batch;
+ft_status ft_kv_plan(const ft_kv_batch* batch, ft_workspace* ws, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ft_kv_append — the new tokens' keys and values into their slots, with the
+ * rotary embedding of keys and queries.
+ * k, v [tokens x kv_heads x head_dim], q [tokens x q_heads x head_dim]: bf16
+ *   rows k_stride, v_stride, q_stride apart (slices of one projection's output,
+ *   for instance).  tokens 0..65535 (0 enqueues nothing); q_heads 0..1024, 0
+ *   with a NULL q and q_out: no queries.
+ * rot: 0 (no rotation; q is then copied), or a multiple of 16 up to head_dim:
+ *   the pair (i, i + rot / 2), i < rot / 2, of every key and query head turns by
+ *   the angle of its position: (a, b) -> (a cos - b sin, b cos + a sin),
+ *   cos = cos_sin[p][i], sin = cos_sin[p][rot / 2 + i], cos_sin fp32
+ *   [positions x rot], p = pos[token].
+ * fp32 arithmetic, one rounding to bf16, or to e4m3 after a division by the
+ * head's scale (values beyond +-448 become +-448; NaN stays NaN).
+ * A token whose slot is outside 0..pages * page_tokens - 1, or (rot > 0) whose
+ * position is outside 0..positions - 1, is padding: nothing of it is written,
+ * q_out included.  Slots of one call are distinct; of tokens that share one the
+ * slot holds a mixture.  pos may be NULL when rot is 0.  q_out may be q.
+ * Errors: FT_ERR_ARG, FT_ERR_HIP.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t tokens;
+    int32_t q_heads;
+    int32_t rot;
+    int32_t positions;
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* slot;
+    const int32_t* pos;
+    const float* cos_sin;
+    uint16_t* q_out;         /* bf16 [tokens x q_heads x head_dim]               */
+    int64_t q_out_stride;
+} ft_append;
+ft_status ft_kv_append(const ft_kv_cache* cache, const ft_append* args, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ft_kv_attend — attention of one new token per request over its pages:
+ *   s_t = scale * q_h . k_t,   out_h = sum_t exp(s_t) v_t /
+ *                                      (sum_t exp(s_t) + exp(sinks[h])),
+ * over the positions t of 0..kv_len[b] - 1 (the new token's own among them,
+ * once appended), or the last `window` of them (window > 0); query head h reads
+ * KV head h / (q_heads / kv_heads).  sinks fp32 [q_heads], or NULL: no such term.
+ * requests 0..4096 (0 enqueues nothing); q_heads: a multiple of kv_heads, at
+ *   most 1024; table [requests x width]; kv_len [requests] (clamped to
+ *   0..width * page_tokens); requests * width * page_tokens below 2^36.  q, out
+ *   [requests x q_heads x head_dim] bf16.  scale is finite.
+ * A position whose page id is outside 0..pages - 1 is left out.  A request that
+ * sees no position gets zeros.  What pages hold beyond the visible positions,
+ * and table entries beyond them, reaches no result.
+ * Sums and softmax statistics are fp32; probabilities keep 16 significant bits
+ * for the product with the values.  The work of all requests is divided evenly
+ * over workgroups, so the order of a request's sums depends on the lengths of the
+ * others.
+ * Errors: FT_ERR_ARG (shape, strides, null or misaligned pointers, a workspace
+ * that is too small or of another device than the current one or the
+ * stream's), FT_ERR_HIP.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t requests;
+    int32_t q_heads;
+    int32_t width;
+    int32_t window;
+    float scale;
+    int32_t reserved;        /* 0 */
+    const uint16_t* q;
+    int64_t q_stride;
+    const int32_t* table;
+    const int32_t* kv_len;
+    const float* sinks;
+    uint16_t* out;
+    int64_t out_stride;
+} ft_attend;
+int64_t ft_kv_attend_workspace(const ft_kv_cache* cache, int32_t q_heads, int32_t max_requests);  /* 0 if invalid */
+ft_status ft_kv_attend(const ft_kv_cache* cache, const ft_attend* args, ft_workspace* ws, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ft_block_norm — what lies between one block's output and the next block's
+ * input: the norm after the block, its gate, the residual and the norm before
+ * the next one, in one pass.
+ *   u = block                                              (post_w NULL)
+ *     = block / sqrt(mean(block^2) + eps) * (weight_offset + post_w)
+ *   sum = residual_scale * residual + gate * u
+ *   normed = sum / sqrt(mean(sum^2) + eps) * (weight_offset + pre_w)
+ * per token, in fp32, the second norm from the sum before its rounding.
+ * block, residual, sum, normed [T x d] bf16; post_w, pre_w [d] bf16.
+ * T 0..2^24 (0 enqueues nothing), d a multiple of 8, 8..32768; strides in
+ *   elements, a multiple of 8 and at least d; everything 16-byte aligned (a gate
+ *   per token: 2-byte).
+ * block NULL: no such term (then post_w and gate are NULL); residual NULL: no
+ *   such term; one of them is there.  sum or normed may be NULL: not written;
+ *   normed needs pre_w, and pre_w normed.
+ * gate_kind: FT_GATE_NONE; FT_GATE_CHANNEL gate [d]; FT_GATE_TOKEN gate [T];
+ *   FT_GATE_FULL gate [T x d], rows gate_stride apart; | FT_GATE_SIGMOID: the
+ *   sigmoid of the given values is the gate.
+ * sum may be residual or block, and normed block or residual, with equal
+ * strides.  Squares are summed in fp32 (values up to 2^56).
+ * Errors: FT_ERR_ARG, FT_ERR_HIP.
+ * ------------------------------------------------------------------------- */
+enum { FT_GATE_NONE = 0, FT_GATE_CHANNEL = 1, FT_GATE_TOKEN = 2, FT_GATE_FULL = 3, FT_GATE_SIGMOID = 0x10 };
+
+typedef struct {
+    int32_t T;
+    int32_t d;
+    int32_t gate_kind;       /* FT_GATE_*                                        */
+    float eps;               /* >= 0                                             */
+    float residual_scale;
+    float weight_offset;
+    const uint16_t* block;
+    const uint16_t* residual;
+    const uint16_t* post_w;
+    const uint16_t* pre_w;
+    const uint16_t* gate;
+    uint16_t* sum;
+    uint16_t* normed;
+    int64_t block_stride, residual_stride, gate_stride, sum_stride, normed_stride;
+} ft_norm;
+ft_status ft_block_norm(const ft_norm* args, void* stream);
+
 /* Pinned, device-mapped host memory for host banks (hipHostMalloc).  Banks
  * larger than torch's power-of-two pinned allocator can serve come from here. */
 ft_status ft_host_alloc(size_t bytes, void** ptr);

@@ -64,6 +64,43 @@ class FtMatrix(ctypes.Structure):
     _fields_ = [("n", i32), ("K", i32), ("fmt", i32), ("reserved", i32), ("codes", vp), ("scales", vp)]
 
 
+FT_KV_BF16, FT_KV_E4M3 = 0, 1
+KV_FMT = {"bf16": FT_KV_BF16, "e4m3": FT_KV_E4M3}
+FT_GATE_NONE, FT_GATE_CHANNEL, FT_GATE_TOKEN, FT_GATE_FULL, FT_GATE_SIGMOID = 0, 1, 2, 3, 0x10
+GATE = {"none": FT_GATE_NONE, "channel": FT_GATE_CHANNEL, "token": FT_GATE_TOKEN, "full": FT_GATE_FULL}
+
+
+class FtKvCache(ctypes.Structure):
+    _fields_ = [("pages", i32), ("page_tokens", i32), ("kv_heads", i32), ("head_dim", i32), ("fmt", i32),
+                ("reserved", i32), ("page_stride", i64), ("k", vp), ("v", vp), ("k_scale", vp), ("v_scale", vp)]
+
+
+class FtKvBatch(ctypes.Structure):
+    _fields_ = [("requests", i32), ("pages", i32), ("page_tokens", i32), ("width", i32), ("tokens", i32),
+                ("row_tokens", i32), ("context", vp), ("add", vp), ("table", vp), ("free_pages", vp),
+                ("free_count", vp), ("kv_len", vp), ("start", vp), ("slot", vp), ("pos", vp), ("counts", vp)]
+
+
+class FtAppend(ctypes.Structure):
+    _fields_ = [("tokens", i32), ("q_heads", i32), ("rot", i32), ("positions", i32), ("q", vp), ("k", vp), ("v", vp),
+                ("q_stride", i64), ("k_stride", i64), ("v_stride", i64), ("slot", vp), ("pos", vp), ("cos_sin", vp),
+                ("q_out", vp), ("q_out_stride", i64)]
+
+
+class FtAttend(ctypes.Structure):
+    _fields_ = [("requests", i32), ("q_heads", i32), ("width", i32), ("window", i32), ("scale", ctypes.c_float),
+                ("reserved", i32), ("q", vp), ("q_stride", i64), ("table", vp), ("kv_len", vp), ("sinks", vp),
+                ("out", vp), ("out_stride", i64)]
+
+
+class FtNorm(ctypes.Structure):
+    _fields_ = [("T", i32), ("d", i32), ("gate_kind", i32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("weight_offset", ctypes.c_float), ("block", vp),
+                ("residual", vp), ("post_w", vp), ("pre_w", vp), ("gate", vp), ("sum", vp), ("normed", vp),
+                ("block_stride", i64), ("residual_stride", i64), ("gate_stride", i64), ("sum_stride", i64),
+                ("normed_stride", i64)]
+
+
 class FtError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__(f"ftmoe status {status}: {msg}")
@@ -100,6 +137,11 @@ _SIGS = {
     "ft_lora_expert_workspace": (i64, [ctypes.POINTER(FtShape), i32, i32]),
     "ft_lora_expert": (i32, [ctypes.POINTER(FtShape), vp, ctypes.POINTER(FtLora), ctypes.POINTER(FtLora),
                              ctypes.POINTER(FtLora), vp, vp, i32, vp, vp, vp, vp]),
+    "ft_kv_plan": (i32, [ctypes.POINTER(FtKvBatch), vp, vp]),
+    "ft_kv_append": (i32, [ctypes.POINTER(FtKvCache), ctypes.POINTER(FtAppend), vp]),
+    "ft_kv_attend_workspace": (i64, [ctypes.POINTER(FtKvCache), i32, i32]),
+    "ft_kv_attend": (i32, [ctypes.POINTER(FtKvCache), ctypes.POINTER(FtAttend), vp, vp]),
+    "ft_block_norm": (i32, [ctypes.POINTER(FtNorm), vp]),
     "ft_host_alloc": (i32, [ctypes.c_size_t, ctypes.POINTER(vp)]),
     "ft_host_free": (i32, [vp]),
     "ft_last_error": (ctypes.c_char_p, []),
@@ -287,3 +329,58 @@ def ft_lora_expert(shp: FtShape, record: int, gate, up, down, x: int, adapter: i
     """`gate`, `up`, `down`: FtLora or None; `base` and (without adapters) `adapter` may be 0."""
     _check(lib().ft_lora_expert(ctypes.byref(shp), record, _opt(gate), _opt(up), _opt(down), x, adapter, T, base, y,
                                 ws, stream))
+
+
+def kv_cache(pages, page_tokens, kv_heads, head_dim, fmt, k: int, v: int, k_scale: int = 0, v_scale: int = 0,
+             page_stride: int = 0) -> FtKvCache:
+    """A paged key-value cache; page_stride 0: pages back to back."""
+    f = KV_FMT[fmt] if isinstance(fmt, str) else fmt
+    stride = page_stride or kv_heads * page_tokens * head_dim * (2 if f == FT_KV_BF16 else 1)
+    return FtKvCache(pages, page_tokens, kv_heads, head_dim, f, 0, stride, k, v, k_scale, v_scale)
+
+
+def kv_batch(requests, pages, page_tokens, width, tokens, row_tokens, context: int, add: int, table: int,
+             free_pages: int, free_count: int, kv_len: int, start: int, slot: int, pos: int, counts: int) -> FtKvBatch:
+    return FtKvBatch(requests, pages, page_tokens, width, tokens, row_tokens, context, add, table, free_pages,
+                     free_count, kv_len, start, slot, pos, counts)
+
+
+def kv_append(tokens, k: int, k_stride, v: int, v_stride, slot: int, pos: int = 0, rot=0, positions=0,
+              cos_sin: int = 0, q_heads=0, q: int = 0, q_stride=0, q_out: int = 0, q_out_stride=0) -> FtAppend:
+    return FtAppend(tokens, q_heads, rot, positions, q, k, v, q_stride, k_stride, v_stride, slot, pos, cos_sin, q_out,
+                    q_out_stride)
+
+
+def kv_attend(requests, q_heads, width, scale, q: int, q_stride, table: int, kv_len: int, out: int, out_stride,
+              window=0, sinks: int = 0) -> FtAttend:
+    return FtAttend(requests, q_heads, width, window, scale, 0, q, q_stride, table, kv_len, sinks, out, out_stride)
+
+
+def block_norm(T, d, eps, block: int = 0, residual: int = 0, post_w: int = 0, pre_w: int = 0, gate: int = 0,
+               gate_kind="none", sigmoid=False, sum: int = 0, normed: int = 0, residual_scale=1.0, weight_offset=0.0,
+               block_stride=0, residual_stride=0, gate_stride=0, sum_stride=0, normed_stride=0) -> FtNorm:
+    """Strides of 0 mean d."""
+    kind = GATE[gate_kind] if isinstance(gate_kind, str) else gate_kind
+    kind |= FT_GATE_SIGMOID if sigmoid and kind else 0
+    return FtNorm(T, d, kind, eps, residual_scale, weight_offset, block, residual, post_w, pre_w, gate, sum, normed,
+                  block_stride or d, residual_stride or d, gate_stride or d, sum_stride or d, normed_stride or d)
+
+
+def ft_kv_plan(batch: FtKvBatch, ws: int, stream: int = 0) -> None:
+    _check(lib().ft_kv_plan(ctypes.byref(batch), ws, stream))
+
+
+def ft_kv_append(cache: FtKvCache, args: FtAppend, stream: int = 0) -> None:
+    _check(lib().ft_kv_append(ctypes.byref(cache), ctypes.byref(args), stream))
+
+
+def ft_kv_attend_workspace(cache: FtKvCache, q_heads: int, max_requests: int) -> int:
+    return lib().ft_kv_attend_workspace(ctypes.byref(cache), q_heads, max_requests)
+
+
+def ft_kv_attend(cache: FtKvCache, args: FtAttend, ws: int, stream: int = 0) -> None:
+    _check(lib().ft_kv_attend(ctypes.byref(cache), ctypes.byref(args), ws, stream))
+
+
+def ft_block_norm(args: FtNorm, stream: int = 0) -> None:
+    _check(lib().ft_block_norm(ctypes.byref(args), stream))

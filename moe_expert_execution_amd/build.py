@@ -20,8 +20,8 @@ BUILD = os.path.join(HERE, "_build")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 HIP_SOURCES = ["control.hip", "route.hip", "plan.hip", "gemv.hip", "gemm.hip", "combine.hip", "scratch.hip", "decode.hip",
-               "moe_layer.hip", "lora.hip"]
-HOST_SOURCES = ["api.cpp", "host_exec.cpp", "resident.cpp"]
+               "moe_layer.hip", "lora.hip", "kv_plan.hip", "kv_append.hip", "kv_attend.hip", "block_norm.hip"]
+HOST_SOURCES = ["api.cpp", "host_exec.cpp", "resident.cpp", "kv.cpp"]
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-I", INCLUDE, "-I", CSRC, "-Wall", "-Wno-unused-function",
           "-Wno-unused-variable"]
 HIP_FLAGS = ["--offload-arch=gfx950", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -1,0 +1,141 @@
+// The norms after one block and before the next, with the block's gate and the
+// residual between them (ft_block_norm):
+//   u = b / sqrt(mean b^2 + eps) * w1,  s = a r + g u,  n = s / sqrt(mean s^2 + eps) * w2.
+//
+// Every input is read once and every output written once: a row stays in
+// registers, 8 elements per 16-byte unit, between its two sums of squares, which
+// are the only points where its threads meet.  The second norm uses the fp32
+// sum; rounding it first would feed the next block the residual's bf16 error
+// twice.  Memory bounds it, or the launch where there are few rows.
+#include "kv.h"
+#include "wfmt.h"
+
+namespace ftmoe {
+namespace {
+
+// Sum over the threads of a row: R lanes of a wave, or the whole workgroup (R > 64).
+template <int R>
+__device__ __forceinline__ float row_sum(float v, float* lds) {
+#pragma unroll
+    for (int m = 1; m < (R < 64 ? R : 64); m *= 2) v += __shfl_xor(v, m);
+    if constexpr (R > 64) {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) lds[wave] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < R / 64; ++w) v += lds[w];
+    }
+    return v;
+}
+
+__device__ __forceinline__ u32x4_t load_unit(const uint16_t* p) { return *reinterpret_cast<const u32x4_t*>(p); }
+
+__device__ __forceinline__ float element(const u32x4_t u, int i) {
+    return i & 1 ? bf16hi(u[i >> 1]) : bf16lo(u[i >> 1]);
+}
+
+__device__ __forceinline__ float sigmoid_of(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return (uint32_t)f32_to_bf16_rne(lo) | (uint32_t)f32_to_bf16_rne(hi) << 16;
+}
+
+// R threads per row, U units of 8 elements per thread; workgroups of max(R, 256) threads.
+template <int R, int U>
+__global__ void __launch_bounds__(R > 256 ? R : 256) norm_kernel(ft_norm a) {
+    constexpr int kThreads = R > 256 ? R : 256;
+    __shared__ float lds[2][R > 64 ? R / 64 : 1];
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / R) + threadIdx.x / R;
+    const int lane = threadIdx.x % R, units = a.d >> 3;
+    if (t >= a.T) return;                   // (rows of a workgroup-wide reduction have one row a workgroup)
+    const int kind = a.gate_kind & ~FT_GATE_SIGMOID;
+    const bool sigmoid = a.gate_kind & FT_GATE_SIGMOID;
+    const float inv_d = 1.0f / (float)a.d;
+    const u32x4_t zero = {0, 0, 0, 0};
+    u32x4_t b[U], r[U], g[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int u = lane + i * R;
+        const bool on = u < units;
+        b[i] = on && a.block ? load_unit(a.block + t * a.block_stride + u * 8) : zero;
+        r[i] = on && a.residual ? load_unit(a.residual + t * a.residual_stride + u * 8) : zero;
+        g[i] = on && kind == FT_GATE_FULL    ? load_unit(a.gate + t * a.gate_stride + u * 8)
+               : on && kind == FT_GATE_CHANNEL ? load_unit(a.gate + u * 8)
+                                               : zero;
+    }
+    float token_gate = 1.0f;
+    if (kind == FT_GATE_TOKEN) {
+        token_gate = __uint_as_float((uint32_t)a.gate[t] << 16);
+        if (sigmoid) token_gate = sigmoid_of(token_gate);
+    }
+    float s1 = token_gate;
+    if (a.post_w) {
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q = fmaf(element(b[i], e), element(b[i], e), q);
+        s1 = token_gate * (1.0f / sqrtf(row_sum<R>(q, lds[0]) * inv_d + a.eps));
+    }
+    float s[U][8];
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int u = lane + i * R;
+        const bool on = u < units;
+        const u32x4_t w = on && a.post_w ? load_unit(a.post_w + u * 8) : zero;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float v = element(b[i], e) * s1;
+            if (a.post_w) v *= a.weight_offset + element(w, e);
+            if (kind == FT_GATE_FULL || kind == FT_GATE_CHANNEL) {
+                const float x = element(g[i], e);
+                v *= sigmoid ? sigmoid_of(x) : x;
+            }
+            if (a.residual) v = fmaf(a.residual_scale, element(r[i], e), v);
+            s[i][e] = v;
+            q = fmaf(v, v, q);
+        }
+        if (on && a.sum) {
+            u32x4_t o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = pack_bf16(s[i][2 * e], s[i][2 * e + 1]);
+            *reinterpret_cast<u32x4_t*>(a.sum + t * a.sum_stride + u * 8) = o;
+        }
+    }
+    if (!a.normed) return;
+    const float s2 = 1.0f / sqrtf(row_sum<R>(q, lds[1]) * inv_d + a.eps);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int u = lane + i * R;
+        if (u >= units) continue;
+        const u32x4_t w = load_unit(a.pre_w + u * 8);
+        u32x4_t o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[e] = pack_bf16(s[i][2 * e] * s2 * (a.weight_offset + element(w, 2 * e)),
+                             s[i][2 * e + 1] * s2 * (a.weight_offset + element(w, 2 * e + 1)));
+        *reinterpret_cast<u32x4_t*>(a.normed + t * a.normed_stride + u * 8) = o;
+    }
+}
+
+template <int R, int U>
+hipError_t go(const ft_norm& a, hipStream_t st) {
+    constexpr int kThreads = R > 256 ? R : 256;
+    const int64_t rows = kThreads / R;
+    return launch(norm_kernel<R, U>, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(kThreads), 0, st, a);
+}
+
+}  // namespace
+
+hipError_t launch_block_norm(const ft_norm& a, hipStream_t st) {
+    const int units = a.d >> 3;
+    if (units <= 16) return go<16, 1>(a, st);
+    if (units <= 64) return go<64, 1>(a, st);
+    if (units <= 256) return go<256, 1>(a, st);
+    if (units <= 1024) return go<256, 4>(a, st);
+    return go<1024, 4>(a, st);
+}
+
+}  // namespace ftmoe

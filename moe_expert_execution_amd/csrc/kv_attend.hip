@@ -1,0 +1,521 @@
+// Attention of one new token per request over a paged key-value cache
+// (ft_kv_attend):  out = sum_t exp(s_t) v_t / sum_t exp(s_t), s_t = scale q . k_t.
+//
+// The query heads that share a KV head are the columns of one matrix-core operand,
+// so a page is read once for all of them.  S^T = K Q^T takes 16 tokens of keys as the
+// A operand straight from memory (the cache's unit order is that operand's order) and
+// leaves lane l with column l % 16 and tokens 4 (l / 16) .. + 3 of each of two blocks.
+// The order of a product's contraction is free, so these very registers are the B
+// operand of O^T += V^T P^T if V's lanes take the tokens in the same order: lane l
+// loads tokens 4 (l / 16) .. + 3 of both blocks at its own dimensions (whole rows over
+// the lanes) and transposes them in registers, one byte permute per pair.  So neither
+// keys, values nor probabilities pass through LDS.
+//
+// Up to 8 query heads the operand's other 8 columns hold the same heads: columns 0 .. 7
+// take each probability's nearest bf16, 8 .. 15 the rest's, and the two sums add up to
+// 16 significant bits at no cost; wider groups take two products.  e4m3 codes become bf16
+// exactly; the heads' scales multiply the logits and the result.
+//
+// Statistics are fp32, one running maximum and sum per column and wave, in base 2.  The
+// work is divided as kv_rules.h says; memory bounds long contexts, latency short ones.
+#include "kv.h"
+#include "resident.h"
+
+namespace ftmoe {
+namespace {
+
+using rs::last_arrival;
+constexpr int kWaves = kv::kWaves, kThreads = kWaves * 64;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct AttendArgs {
+    CacheView c;
+    ft_attend a;
+    int g, blocks;            // query heads per KV head, items per KV head
+    float* part;              // partial results: two per team
+    uint32_t part_bytes;
+    uint32_t* counters;       // one per team
+};
+
+// Agent-scope 16-byte access (sc1): a partial result crosses XCDs, whose L2s do not
+// see each other.
+constexpr int kAgent = 16;
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+template <int D, int FMT>
+struct Kv {
+    static constexpr int E = FMT == FT_KV_BF16 ? 2 : 1;
+    static constexpr int ck = kv::key_unit(E), cv = kv::value_dims(D), tu = kv::value_tokens(D, E);
+    static constexpr int BB = 16 * D * E;              // bytes of a block
+    static constexpr int L = BB / 1024;                // 16-byte loads of a lane per block
+    static constexpr int R = D / (16 * cv);            // rounds of 16 value units
+    static constexpr int S = D / 32;                   // matrix-core steps of a block's keys
+};
+
+// One step's keys and values in registers, as stored.
+template <int D, int FMT>
+struct Step {
+    u32x4_t k[2][Kv<D, FMT>::L];
+    u32x4_t v[2][Kv<D, FMT>::L];
+};
+
+template <int D, int FMT>
+__device__ __forceinline__ void load_step(Step<D, FMT>& s, const uint8_t* k0, const uint8_t* v0, const uint8_t* k1,
+                                          const uint8_t* v1, int lane) {
+    using T = Kv<D, FMT>;
+    const int q = lane >> 4, m = lane & 15;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const uint8_t* k = b ? k1 : k0;
+#pragma unroll
+        for (int i = 0; i < T::L; ++i)
+            s.k[b][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(k + i * 1024 + lane * 16));
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const uint8_t* v = b ? v1 : v0;
+#pragma unroll
+        for (int r = 0; r < T::R; ++r)
+#pragma unroll
+            for (int i = 0; i < 4 / T::tu; ++i) {
+                const int unit = ((4 / T::tu) * q + i) * (D / T::cv) + r * 16 + m;
+                s.v[b][r * (4 / T::tu) + i] =
+                    __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(v + unit * 16));
+            }
+    }
+}
+
+__device__ __forceinline__ uint32_t cvt_pair(uint32_t w, bool high) {
+    const bf16x2_t p = high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
+                            : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
+    return __builtin_bit_cast(uint32_t, p);
+}
+
+// The A operand of step j of a block's keys.
+template <int D, int FMT>
+__device__ __forceinline__ bf16x8_t key_frag(const u32x4_t (&k)[Kv<D, FMT>::L], int j) {
+    if constexpr (FMT == FT_KV_BF16) {
+        return __builtin_bit_cast(bf16x8_t, k[j]);
+    } else {
+        return rs::a_frag<FT_FMT_FP8_B128>(k[j >> 1], j & 1, 1.0f);
+    }
+}
+
+// Two tokens' value at dimension i (of cv) of round r, tokens 2 p and 2 p + 1 of the lane's
+// four, as one register of the A operand.
+template <int D, int FMT>
+__device__ __forceinline__ uint32_t value_pair(const u32x4_t (&v)[Kv<D, FMT>::L], int r, int i, int p) {
+    using T = Kv<D, FMT>;
+    constexpr int N = 4 / T::tu;
+    if constexpr (T::E == 2) {
+        // bf16: dimension i is half i % 2 of dword i / 2 of the token's cv / 2
+        const u32x4_t u0 = T::tu == 1 ? v[r * N + 2 * p] : v[r * N + p];
+        const u32x4_t u1 = T::tu == 1 ? v[r * N + 2 * p + 1] : u0;
+        const uint32_t w0 = u0[i >> 1], w1 = T::tu == 1 ? u1[i >> 1] : u1[2 + (i >> 1)];
+        return __builtin_amdgcn_perm(w1, w0, i & 1 ? 0x07060302u : 0x05040100u);
+    } else {
+        // e4m3: byte i % 4 of dword i / 4 of the token's cv / 4; bytes of two tokens side by side, then
+        // both converted
+        const u32x4_t u = T::tu == 2 ? v[r * N + p] : v[r * N];
+        const uint32_t w0 = T::tu == 2 ? u[i >> 2] : u[2 * p], w1 = T::tu == 2 ? u[2 + (i >> 2)] : u[2 * p + 1];
+        const uint32_t b = __builtin_amdgcn_perm(w1, w0, i & 2 ? 0x07030602u : 0x05010400u);
+        return cvt_pair(b, i & 1);
+    }
+}
+
+// The running state of a wave: column l % 16, of which the lane has the sums at dimensions
+// r 16 cv + (4 (l / 16) + v) cv + i in o[r cv + i][v].
+template <int D, int FMT, bool WIDE>
+struct State {
+    f32x4_t o[D / 16];
+    float m, l;          // maximum in base 2; this lane's share of the sum
+};
+
+template <int D, int FMT, bool WIDE>
+__device__ __forceinline__ void work_step(State<D, FMT, WIDE>& st, const Step<D, FMT>& x,
+                                          const bf16x8_t (&q)[Kv<D, FMT>::S], float scale, bool masked, int t0, int lo,
+                                          int hi, int lane) {
+    using T = Kv<D, FMT>;
+    float s[2][4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < T::S; ++j)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key_frag<D, FMT>(x.k[b], j), q[j], acc, 0, 0, 0);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) s[b][v] = acc[v] * scale;
+    }
+    uint32_t keep[2][2] = {{~0u, ~0u}, {~0u, ~0u}};    // halves of value pairs that are visible
+    if (masked) {
+        const int t = t0 + 4 * (lane >> 4);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int at = t + 16 * b + v;
+                if (at < lo || at >= hi) {
+                    s[b][v] = -INFINITY;
+                    keep[b][v >> 1] &= v & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                }
+            }
+    }
+    float mt = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                     fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+    mt = fmaxf(mt, __shfl_xor(mt, 16));
+    mt = fmaxf(mt, __shfl_xor(mt, 32));
+    const float m = fmaxf(st.m, mt);
+    const float base = m == -INFINITY ? 0.0f : m;      // (nothing visible so far: all terms are 0)
+    const float alpha = exp2_of(st.m - base);
+    st.m = m;
+    float sum = 0.0f;
+    uint32_t hi_p[4], lo_p[4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const float p0 = exp2_of(s[b][2 * p] - base), p1 = exp2_of(s[b][2 * p + 1] - base);
+            sum += p0 + p1;
+            const bf16x2_t h = {(__bf16)p0, (__bf16)p1};
+            const bf16x2_t r = {(__bf16)(p0 - (float)h[0]), (__bf16)(p1 - (float)h[1])};
+            hi_p[b * 2 + p] = __builtin_bit_cast(uint32_t, h);
+            lo_p[b * 2 + p] = __builtin_bit_cast(uint32_t, r);
+        }
+    st.l = st.l * alpha + sum;
+    u32x4_t ph, pl;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        ph[i] = WIDE || !(lane & 8) ? hi_p[i] : lo_p[i];
+        pl[i] = lo_p[i];
+    }
+#pragma unroll
+    for (int r = 0; r < T::R; ++r)
+#pragma unroll
+        for (int i = 0; i < T::cv; ++i) {
+            u32x4_t a;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) a[b * 2 + p] = value_pair<D, FMT>(x.v[b], r, i, p) & keep[b][p];
+            f32x4_t& o = st.o[r * T::cv + i];
+            o *= alpha;
+            const bf16x8_t av = __builtin_bit_cast(bf16x8_t, a);
+            o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8_t, ph), o, 0, 0, 0);
+            if constexpr (WIDE)
+                o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8_t, pl), o, 0, 0, 0);
+        }
+}
+
+// A row of 16 lanes turned by 8: column n and column n + 8 change places.
+__device__ __forceinline__ float other_half(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x128, 0xF, 0xF, true));
+}
+
+// Weight of a part whose maximum is m, beside the whole's maximum.
+__device__ __forceinline__ float part_weight(float m, float whole) {
+    return whole == -INFINITY ? 0.0f : exp2_of(m - whole);
+}
+
+// out[0..3] of one head: o / l, zeros where nothing was visible.
+__device__ __forceinline__ void store_out(uint16_t* to, const f32x4_t o, float l, float v_scale) {
+    const float f = l == 0.0f ? 0.0f : v_scale / l;
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = l == 0.0f ? 0.0f : o[i] * f;
+    *reinterpret_cast<u32x2_t*>(to) = u32x2_t{(uint32_t)f32_to_bf16_rne(x[0]) | (uint32_t)f32_to_bf16_rne(x[1]) << 16,
+                                              (uint32_t)f32_to_bf16_rne(x[2]) | (uint32_t)f32_to_bf16_rne(x[3]) << 16};
+}
+
+template <int D, int FMT, bool WIDE, int DEPTH>
+__global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
+    using T = Kv<D, FMT>;
+    constexpr int kChunk = D / T::R, kRow = kChunk + 4;          // dimensions of a round; padded in LDS
+    extern __shared__ int lds[];
+    const int B = a.a.requests, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int* pre = lds;                                              // [B + 1] steps of the requests before
+    float* wm = reinterpret_cast<float*>(lds + ((B + 1 + 3) & ~3));   // [kWaves][16]
+    float* wl = wm + kWaves * kv::kCols;
+    float* wo = wl + kWaves * kv::kCols;                         // [kWaves][heads][kRow]
+    __shared__ uint32_t flag;
+    __shared__ int scan[kWaves];
+    const int shift = a.c.page_shift, room = a.a.width << shift;
+
+    auto range = [&](int b, int& lo, int& hi) {
+        const int n = a.a.kv_len[b];
+        hi = n < 0 ? 0 : n > room ? room : n;
+        lo = a.a.window && hi > a.a.window ? hi - a.a.window : 0;
+    };
+    auto steps_of = [&](int b) {
+        int lo, hi;
+        range(b, lo, hi);
+        return hi ? (hi + kv::kStep - 1) / kv::kStep - lo / kv::kStep : 0;
+    };
+    // the requests' steps, summed in slices of the workgroup's width
+    int carry = 0;
+    for (int b0 = 0; b0 < B; b0 += kThreads) {
+        const int b = b0 + tid;
+        int x = b < B ? steps_of(b) : 0;
+        const int own = x;
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+            const int y = __shfl_up(x, m);
+            if (lane >= m) x += y;
+        }
+        __syncthreads();
+        if (lane == 63) scan[wave] = x;
+        __syncthreads();
+        int before = carry;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) before += scan[w];
+            carry += scan[w];
+        }
+        if (b < B) pre[b] = before + x - own;
+    }
+    if (tid == 0) pre[B] = carry;
+    __syncthreads();
+
+    const int g = a.g, heads_all = a.c.heads * a.blocks;
+    // requests that see nothing
+    for (int b = blockIdx.x; b < B; b += gridDim.x)
+        if (pre[b] == pre[b + 1])
+            for (int i = tid * 8; i < a.a.q_heads * D; i += kThreads * 8)
+                *reinterpret_cast<u32x4_t*>(a.a.out + b * a.a.out_stride + i) = u32x4_t{0, 0, 0, 0};
+
+    const int64_t total = (int64_t)carry * heads_all;
+    if (total == 0) return;
+    const int teams = kv::teams_of(total, gridDim.x), self = blockIdx.x;
+    if (self >= teams) return;
+    const int64_t begin = kv::team_begin(total, teams, self), end = kv::team_begin(total, teams, self + 1);
+    const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(a.part, 0, a.part_bytes, 0x00020000);
+    const uint32_t part_stride = (uint32_t)kv::part_floats(g, D) * 4;
+
+    for (int64_t at = begin; at < end;) {
+        // the item that holds step `at`
+        int b = 0, top = B;
+        while (top - b > 1) {
+            const int mid = (b + top) >> 1;
+            if ((int64_t)pre[mid] * heads_all <= at) b = mid;
+            else top = mid;
+        }
+        const int nb = pre[b + 1] - pre[b];
+        const int64_t rem = at - (int64_t)pre[b] * heads_all;
+        const int item = (int)(rem / nb), first = (int)(rem % nb);
+        const int64_t item_begin = at - first;
+        const int n = (int)(end - at < nb - first ? end - at : nb - first);       // steps of this segment
+        at += n;
+        const int h = item / a.blocks, q0 = h * g + (item % a.blocks) * kv::kCols;
+        const int heads = min(kv::kCols, g - (item % a.blocks) * kv::kCols);
+        int lo, hi;
+        range(b, lo, hi);
+        const int step0 = lo / kv::kStep + first;                // in the request's own steps
+        const float scale = a.a.scale * kLog2e * (FMT == FT_KV_E4M3 ? a.c.k_scale[h] : 1.0f);
+        const float v_scale = FMT == FT_KV_E4M3 ? a.c.v_scale[h] : 1.0f;
+
+        bf16x8_t q[T::S];
+        {
+            const int col = WIDE ? lane & 15 : lane & 7, quarter = lane >> 4;
+            const uint16_t* row = a.a.q + b * a.a.q_stride + (int64_t)(q0 + (col < heads ? col : 0)) * D;
+#pragma unroll
+            for (int j = 0; j < T::S; ++j) {
+                // the dimensions that key_frag's step j has at this quarter
+                const int e = T::E == 2 ? (j * 4 + quarter) * 8 : ((j >> 1) * 4 + quarter) * 16 + (j & 1) * 8;
+                u32x4_t v = *reinterpret_cast<const u32x4_t*>(row + e);
+                if (col >= heads) v = u32x4_t{0, 0, 0, 0};
+                q[j] = __builtin_bit_cast(bf16x8_t, v);
+            }
+        }
+        State<D, FMT, WIDE> st;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) st.o[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        st.m = -INFINITY;
+        st.l = 0.0f;
+
+        const int64_t head_off = (int64_t)h * ((int64_t)(D * T::E) << shift);
+        const int32_t* table = a.a.table + (int64_t)b * a.a.width;
+        const int mine = (n - wave + kWaves - 1) / kWaves;       // this wave's steps: wave, wave + kWaves, ...
+        Step<D, FMT> buf[DEPTH];
+        bool masked[DEPTH];
+        int ids[DEPTH][2];
+        auto load = [&](int d, int i) {
+            const int t0 = (step0 + wave + i * kWaves) * kv::kStep;
+            const uint8_t *kp[2], *vp[2];
+            masked[d] = t0 < lo || t0 + kv::kStep > hi;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int t = t0 + 16 * x;
+                // (a block past the request's end is not looked up: its page may not exist)
+                const int id = t < hi ? __builtin_amdgcn_readfirstlane(table[t >> shift]) : -1;
+                const bool on = id >= 0 && id < a.c.pages;
+                ids[d][x] = on;
+                masked[d] |= !on;
+                const int64_t off = (on ? (int64_t)id * a.c.page_stride : 0) + head_off +
+                                    (int64_t)((t & ((1 << shift) - 1)) >> 4) * T::BB;
+                kp[x] = a.c.k + off;
+                vp[x] = a.c.v + off;
+            }
+            load_step<D, FMT>(buf[d], kp[0], vp[0], kp[1], vp[1], lane);
+        };
+        auto work = [&](int d, int i) {
+            const int t0 = (step0 + wave + i * kWaves) * kv::kStep;
+            // blocks without a page are left out: the visible range shrinks to the other one, or to nothing
+            int from = lo, to = hi;
+            if (!ids[d][0]) from = max(from, t0 + 16);
+            if (!ids[d][1]) to = min(to, t0 + 16);
+            work_step<D, FMT, WIDE>(st, buf[d], q, scale, masked[d], t0, from, to, lane);
+        };
+        if (mine > 0) rs::pipelined<DEPTH>(mine, load, work);
+
+        // ---- the waves' parts together ----
+        float l = st.l;
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        const int col = lane & 15;
+        if (lane < 16) {
+            wm[wave * kv::kCols + col] = st.m;
+            wl[wave * kv::kCols + col] = l;
+        }
+        __syncthreads();
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) M = fmaxf(M, wm[w * kv::kCols + col]);
+        const float f = part_weight(st.m, M);
+        const int waves = min(n, kWaves);                        // those that had steps
+
+        const int tf = kv::team_of(total, teams, item_begin), tl = kv::team_of(total, teams, item_begin + nb - 1);
+        const bool whole = tf == tl;
+        const uint32_t slot = (uint32_t)(2 * self + (item_begin < begin ? 0 : 1)) * part_stride;
+        uint16_t* out = a.a.out + b * a.a.out_stride + (int64_t)q0 * D;
+
+#pragma unroll
+        for (int r = 0; r < T::R; ++r) {
+            if (r) __syncthreads();
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int i = 0; i < T::cv; i += 4) {
+                    f32x4_t o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[e] = st.o[r * T::cv + i + e][v] * f;
+                        if constexpr (!WIDE) o[e] += other_half(o[e]);
+                    }
+                    if (col < heads && wave < waves)
+                        *reinterpret_cast<f32x4_t*>(wo + (wave * heads + col) * kRow + (4 * (lane >> 4) + v) * T::cv + i) = o;
+                }
+            __syncthreads();
+            for (int x = tid; x < heads * (kChunk / 4); x += kThreads) {
+                const int c = x / (kChunk / 4), e = x % (kChunk / 4) * 4;
+                f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int w = 0; w < waves; ++w) o += *reinterpret_cast<const f32x4_t*>(wo + (w * heads + c) * kRow + e);
+                if (whole) {
+                    float m = -INFINITY, lt = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, wm[w * kv::kCols + c]);
+                    const float sink = a.a.sinks ? a.a.sinks[q0 + c] * kLog2e : -INFINITY;
+                    const float mm = fmaxf(m, sink);
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w)
+                        lt += wl[w * kv::kCols + c] * part_weight(wm[w * kv::kCols + c], mm);
+                    lt += part_weight(sink, mm);
+                    o *= part_weight(m, mm);
+                    store_out(out + (int64_t)c * D + r * kChunk + e, o, lt, v_scale);
+                } else {
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), parts,
+                                                           slot + (uint32_t)(c * D + r * kChunk + e) * 4, 0, kAgent);
+                }
+            }
+        }
+        if (!whole) {
+            // statistics behind the sums: maxima, then totals
+            if (tid < kv::kCols) {
+                float m = -INFINITY, lt = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) m = fmaxf(m, wm[w * kv::kCols + tid]);
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w)
+                    lt += wl[w * kv::kCols + tid] * part_weight(wm[w * kv::kCols + tid], m);
+                const uint32_t p = slot + (uint32_t)(kv::item_heads(g) * D + tid) * 4;
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), parts, p, 0, kAgent);
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lt), parts, p + kv::kCols * 4, 0, kAgent);
+            }
+            if (last_arrival(a.counters + tf, (uint32_t)(tl - tf + 1), &flag)) {
+                // every part of the item is there: their sum, in the teams' order
+                for (int x = tid; x < heads * (D / 4); x += kThreads) {
+                    const int c = x / (D / 4), e = x % (D / 4) * 4;
+                    const float sink = a.a.sinks ? a.a.sinks[q0 + c] * kLog2e : -INFINITY;
+                    float m = sink, lt = sink == -INFINITY ? 0.0f : 1.0f;
+                    f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+                    constexpr int N = 8;                         // parts in flight
+                    for (int t = tf; t <= tl; t += N) {
+                        float pm[N], pl[N];
+                        f32x4_t po[N];
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            const int u = min(t + i, tl);
+                            const uint32_t s = (uint32_t)(2 * u + (u == tf ? 1 : 0)) * part_stride;
+                            const uint32_t p = s + (uint32_t)(kv::item_heads(g) * D + c) * 4;
+                            pm[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(parts, p, 0, kAgent));
+                            pl[i] = __uint_as_float(
+                                __builtin_amdgcn_raw_buffer_load_b32(parts, p + kv::kCols * 4, 0, kAgent));
+                            po[i] = __builtin_bit_cast(
+                                f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(parts, s + (uint32_t)(c * D + e) * 4, 0,
+                                                                               kAgent));
+                        }
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            if (t + i > tl) continue;
+                            const float mn = fmaxf(m, pm[i]);
+                            const float f0 = part_weight(m, mn), f1 = part_weight(pm[i], mn);
+                            lt = lt * f0 + pl[i] * f1;
+                            o = o * f0 + po[i] * f1;
+                            m = mn;
+                        }
+                    }
+                    store_out(out + (int64_t)c * D + e, o, lt, v_scale);
+                }
+            }
+        }
+        __syncthreads();                                         // the next segment writes wm, wl and wo
+    }
+}
+
+template <int D, int FMT, bool WIDE>
+hipError_t go(const AttendArgs& a, int grid, hipStream_t st) {
+    const size_t lds = (((size_t)a.a.requests + 1 + 3) & ~(size_t)3) * 4 + 2 * kWaves * kv::kCols * 4 +
+                       (size_t)kWaves * kv::item_heads(a.g) * (D / Kv<D, FMT>::R + 4) * 4;
+    return launch(attend_kernel<D, FMT, WIDE, 1>, dim3(grid), dim3(kThreads), lds, st, a);
+}
+
+template <int D>
+hipError_t pick(const AttendArgs& a, int grid, hipStream_t st) {
+    const bool wide = a.g > kv::kCols / 2;
+    if (a.c.fmt == FT_KV_BF16)
+        return wide ? go<D, FT_KV_BF16, true>(a, grid, st) : go<D, FT_KV_BF16, false>(a, grid, st);
+    return wide ? go<D, FT_KV_E4M3, true>(a, grid, st) : go<D, FT_KV_E4M3, false>(a, grid, st);
+}
+
+}  // namespace
+
+size_t kv_attend_workspace(int g, int D) { return (size_t)2 * kv::kMaxTeams * kv::part_floats(g, D) * 4; }
+
+hipError_t launch_kv_attend(const CacheView& c, const ft_attend& q, ft_workspace* ws, hipStream_t st) {
+    AttendArgs a;
+    a.c = c;
+    a.a = q;
+    a.g = q.q_heads / c.heads;
+    a.blocks = kv::head_blocks(a.g);
+    a.part = reinterpret_cast<float*>(ws->mem + kCounterBytes);
+    a.part_bytes = (uint32_t)kv_attend_workspace(a.g, c.D);
+    a.counters = reinterpret_cast<uint32_t*>(ws->mem);
+    const int64_t most = (((int64_t)q.width << c.page_shift) + kv::kStep - 1) / kv::kStep + (q.window ? 1 : 0);
+    const int64_t seen = q.window ? q.window / kv::kStep + 2 : most;
+    const int grid = kv::grid_of((int64_t)q.requests * c.heads * a.blocks * (seen < most ? seen : most));
+    if (c.D == 64) return pick<64>(a, grid, st);
+    if (c.D == 128) return pick<128>(a, grid, st);
+    return pick<256>(a, grid, st);
+}
+
+}  // namespace ftmoe

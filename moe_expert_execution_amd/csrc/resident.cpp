@@ -37,27 +37,6 @@ bool unlink_live(ft_workspace* ws) {
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// The device the workspace lives on has to be current and own the stream.
-ft_status check_workspace(const ft_workspace* ws, size_t need, void* stream) {
-    FT_REQUIRE(ws, "workspace is null");
-    FT_REQUIRE(is_live(ws), "not a workspace (or a destroyed one)");
-    FT_REQUIRE(need <= ws->bytes, "workspace holds %zu bytes; this call needs %zu", ws->bytes, need);
-    // The runtime's two handles that are no stream objects: a call with one of them,
-    // asked about its device or launched on, has ended the process.
-    FT_REQUIRE(stream != hipStreamLegacy && stream != hipStreamPerThread,
-               "stream must be NULL or a created stream, not hipStreamLegacy or hipStreamPerThread");
-    int dev = -1;
-    FT_HIP(hipGetDevice(&dev));
-    if (stream) {
-        hipDevice_t sd = -1;
-        FT_HIP(hipStreamGetDevice((hipStream_t)stream, &sd));
-        FT_REQUIRE(sd == ws->device, "the stream belongs to device %d; the workspace was created on device %d", sd,
-                   ws->device);
-    }
-    FT_REQUIRE(dev == ws->device, "device %d is current; the workspace was created on device %d", dev, ws->device);
-    return FT_OK;
-}
-
 ft_status check_layer_shape(const ft_shape* s) {
     FT_REQUIRE(s, "shape is null");
     FT_REQUIRE(s->experts >= 1 && s->experts <= kMaxRouteExperts, "a layer call supports 1..%d experts",
@@ -118,6 +97,36 @@ ft_status check_lora_tokens(int32_t T) {
 }
 
 }  // namespace
+
+namespace ftmoe {
+
+ft_status check_stream(void* stream, int device, const char* owner) {
+    // The runtime's two handles that are no stream objects: a call with one of them,
+    // asked about its device or launched on, has ended the process.
+    FT_REQUIRE(stream != hipStreamLegacy && stream != hipStreamPerThread,
+               "stream must be NULL or a created stream, not hipStreamLegacy or hipStreamPerThread");
+    if (stream) {
+        hipDevice_t sd = -1;
+        FT_HIP(hipStreamGetDevice((hipStream_t)stream, &sd));
+        FT_REQUIRE(sd == device, "the stream belongs to device %d; %s device %d", sd, owner, device);
+    }
+    return FT_OK;
+}
+
+// The device the workspace lives on has to be current and own the stream.
+ft_status check_workspace(const ft_workspace* ws, size_t need, void* stream) {
+    FT_REQUIRE(ws, "workspace is null");
+    FT_REQUIRE(is_live(ws), "not a workspace (or a destroyed one)");
+    FT_REQUIRE(need <= ws->bytes, "workspace holds %zu bytes; this call needs %zu", ws->bytes, need);
+    const ft_status s = check_stream(stream, ws->device, "the workspace was created on");
+    if (s != FT_OK) return s;
+    int dev = -1;
+    FT_HIP(hipGetDevice(&dev));
+    FT_REQUIRE(dev == ws->device, "device %d is current; the workspace was created on device %d", dev, ws->device);
+    return FT_OK;
+}
+
+}  // namespace ftmoe
 
 extern "C" {
 
