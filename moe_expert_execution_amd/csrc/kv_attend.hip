@@ -26,15 +26,17 @@ namespace {
 
 using rs::last_arrival;
 constexpr int kWaves = kv::kWaves, kThreads = kWaves * 64;
+constexpr int kDepth = 1;                 // steps in flight per wave
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct AttendArgs {
     CacheView c;
     ft_attend a;
     int g, blocks;            // query heads per KV head, items per KV head
+    bool direct;              // a workgroup is an item
     float* part;              // partial results: two per team
     uint32_t part_bytes;
-    uint32_t* counters;       // one per team
+    uint32_t* counters;       // one per team for its run, one for its item
 };
 
 // Agent-scope 16-byte access (sc1): a partial result crosses XCDs, whose L2s do not
@@ -229,87 +231,117 @@ __device__ __forceinline__ void store_out(uint16_t* to, const f32x4_t o, float l
 }
 
 template <int D, int FMT, bool WIDE, int DEPTH>
-__global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) attend_kernel(AttendArgs a) {
     using T = Kv<D, FMT>;
-    constexpr int kChunk = D / T::R, kRow = kChunk + 4;          // dimensions of a round; padded in LDS
+    constexpr int kUnit = WIDE ? 4 : T::cv, kHalves = T::cv / kUnit;  // dimensions of a value unit that a round takes
+    constexpr int kChunk = 16 * kUnit, kRow = kChunk + 4;        // dimensions of a round; padded in LDS
     extern __shared__ int lds[];
     const int B = a.a.requests, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int* pre = lds;                                              // [B + 1] steps of the requests before
-    float* wm = reinterpret_cast<float*>(lds + ((B + 1 + 3) & ~3));   // [kWaves][16]
+    int* lens = pre + B + 1;                                     // [B] visible lengths' ends
+    float* wm = reinterpret_cast<float*>(lds + (a.direct ? 0 : (2 * B + 1 + 3) & ~3));   // [kWaves][16]
     float* wl = wm + kWaves * kv::kCols;
     float* wo = wl + kWaves * kv::kCols;                         // [kWaves][heads][kRow]
     __shared__ uint32_t flag;
-    __shared__ int scan[kWaves];
+    __shared__ int scan[2][kWaves];
     const int shift = a.c.page_shift, room = a.a.width << shift;
 
-    auto range = [&](int b, int& lo, int& hi) {
+    auto first_of = [&](int hi) { return a.a.window && hi > a.a.window ? hi - a.a.window : 0; };
+    auto end_of = [&](int b) {
         const int n = a.a.kv_len[b];
-        hi = n < 0 ? 0 : n > room ? room : n;
-        lo = a.a.window && hi > a.a.window ? hi - a.a.window : 0;
+        return n < 0 ? 0 : n > room ? room : n;
     };
-    auto steps_of = [&](int b) {
-        int lo, hi;
-        range(b, lo, hi);
-        return hi ? (hi + kv::kStep - 1) / kv::kStep - lo / kv::kStep : 0;
+    auto steps_of = [&](int hi) {
+        return hi ? (hi + kv::kStep - 1) / kv::kStep - first_of(hi) / kv::kStep : 0;
     };
-    // the requests' steps, summed in slices of the workgroup's width
-    int carry = 0;
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
+    const int g = a.g, heads_all = a.c.heads * a.blocks;
+    // the requests' steps, summed in slices of the workgroup's width, and how many have any
+    int carry = 0, busy = 0;
+    for (int b0 = 0; b0 < B && !a.direct; b0 += kThreads) {
         const int b = b0 + tid;
-        int x = b < B ? steps_of(b) : 0;
-        const int own = x;
+        const int hi = b < B ? end_of(b) : 0, own = steps_of(hi);
+        int x = own;
+        const int some = __popcll(__ballot(own > 0));
 #pragma unroll
         for (int m = 1; m < 64; m *= 2) {
             const int y = __shfl_up(x, m);
             if (lane >= m) x += y;
         }
         __syncthreads();
-        if (lane == 63) scan[wave] = x;
+        if (lane == 63) {
+            scan[0][wave] = x;
+            scan[1][wave] = some;
+        }
         __syncthreads();
         int before = carry;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            if (w < wave) before += scan[w];
-            carry += scan[w];
+            if (w < wave) before += scan[0][w];
+            carry += scan[0][w];
+            busy += scan[1][w];
         }
-        if (b < B) pre[b] = before + x - own;
+        if (b < B) {
+            pre[b] = before + x - own;
+            lens[b] = hi;
+        }
     }
-    if (tid == 0) pre[B] = carry;
-    __syncthreads();
-
-    const int g = a.g, heads_all = a.c.heads * a.blocks;
-    // requests that see nothing
-    for (int b = blockIdx.x; b < B; b += gridDim.x)
-        if (pre[b] == pre[b + 1])
-            for (int i = tid * 8; i < a.a.q_heads * D; i += kThreads * 8)
-                *reinterpret_cast<u32x4_t*>(a.a.out + b * a.a.out_stride + i) = u32x4_t{0, 0, 0, 0};
-
-    const int64_t total = (int64_t)carry * heads_all;
-    if (total == 0) return;
-    const int teams = kv::teams_of(total, gridDim.x), self = blockIdx.x;
-    if (self >= teams) return;
-    const int64_t begin = kv::team_begin(total, teams, self), end = kv::team_begin(total, teams, self + 1);
+    kv::Division div = {};
+    const int self = a.direct ? 0 : blockIdx.x;
+    int b = 0, item;
+    if (a.direct) {
+        b = blockIdx.x / heads_all;
+        item = blockIdx.x % heads_all;
+    } else {
+        if (tid == 0) pre[B] = carry;
+        __syncthreads();
+        // requests that see nothing
+        for (int r = blockIdx.x; r < B; r += gridDim.x)
+            if (pre[r] == pre[r + 1])
+                for (int i = tid * 8; i < a.a.q_heads * D; i += kThreads * 8)
+                    *reinterpret_cast<u32x4_t*>(a.a.out + r * a.a.out_stride + i) = u32x4_t{0, 0, 0, 0};
+        if (carry == 0) return;
+        div = kv::divide((int64_t)busy * heads_all, (int64_t)carry * heads_all, gridDim.x);
+        if (self >= div.teams) return;
+        // the item that this team's cut falls into, before it moves (64 requests a look); then on from item to
+        // item
+        const int64_t at = kv::cut(div, self);
+        const int q = (int)((double)at / (double)heads_all);     // (exact: both are whole numbers below 2^42 and 2^11)
+        for (int left = B; left > 1;) {
+            const int width = (left + 63) >> 6, i = lane * width;
+            b += (__popcll(__ballot(i < left && pre[b + (i < left ? i : 0)] <= q)) - 1) * width;
+            left = min(width, B - b);
+        }
+        item = (int)((double)(at - (int64_t)pre[b] * heads_all) / (double)(pre[b + 1] - pre[b]));
+    }
     const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(a.part, 0, a.part_bytes, 0x00020000);
     const uint32_t part_stride = (uint32_t)kv::part_floats(g, D) * 4;
 
-    for (int64_t at = begin; at < end;) {
-        // the item that holds step `at`
-        int b = 0, top = B;
-        while (top - b > 1) {
-            const int mid = (b + top) >> 1;
-            if ((int64_t)pre[mid] * heads_all <= at) b = mid;
-            else top = mid;
+    for (;; ++item) {
+        int hi, nb, first = 0, n;                                // the request's length, the item's steps, this segment's
+        kv::Teams who = {0, 0};
+        if (a.direct) {
+            hi = end_of(b);
+            n = nb = steps_of(hi);
+        } else {
+            if (item == heads_all) {
+                item = 0;
+                do ++b;
+                while (b < B && pre[b] == pre[b + 1]);
+                if (b == B) return;
+            }
+            hi = lens[b];
+            nb = pre[b + 1] - pre[b];
+            const int64_t item_begin = (int64_t)pre[b] * heads_all + (int64_t)item * nb;
+            who = kv::teams_of(div, item_begin, nb);
+            if (self > who.last) continue;                       // (the cut has moved to the item's end)
+            if (self < who.first) return;
+            const kv::Segment seg = kv::segment(div, who, item_begin, nb, self);
+            first = seg.from;
+            n = seg.to - seg.from;
         }
-        const int nb = pre[b + 1] - pre[b];
-        const int64_t rem = at - (int64_t)pre[b] * heads_all;
-        const int item = (int)(rem / nb), first = (int)(rem % nb);
-        const int64_t item_begin = at - first;
-        const int n = (int)(end - at < nb - first ? end - at : nb - first);       // steps of this segment
-        at += n;
+        const int lo = first_of(hi);
         const int h = item / a.blocks, q0 = h * g + (item % a.blocks) * kv::kCols;
         const int heads = min(kv::kCols, g - (item % a.blocks) * kv::kCols);
-        int lo, hi;
-        range(b, lo, hi);
         const int step0 = lo / kv::kStep + first;                // in the request's own steps
         const float scale = a.a.scale * kLog2e * (FMT == FT_KV_E4M3 ? a.c.k_scale[h] : 1.0f);
         const float v_scale = FMT == FT_KV_E4M3 ? a.c.v_scale[h] : 1.0f;
@@ -337,21 +369,25 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
         const int32_t* table = a.a.table + (int64_t)b * a.a.width;
         const int mine = (n - wave + kWaves - 1) / kWaves;       // this wave's steps: wave, wave + kWaves, ...
         Step<D, FMT> buf[DEPTH];
-        bool masked[DEPTH];
-        int ids[DEPTH][2];
+        bool on[DEPTH][2];
+        int pages[2] = {-1, -1};
         auto load = [&](int d, int i) {
+            if ((i & 63) == 0) {
+                // the page ids of this wave's next 64 steps, one step a lane (a block past the request's end is not
+                // looked up: it may have no entry)
+                const int t = (step0 + wave + (i + lane) * kWaves) * kv::kStep;
+                const bool mine_too = i + lane < mine;
+                pages[0] = mine_too && t < hi ? table[t >> shift] : -1;
+                pages[1] = mine_too && t + 16 < hi ? table[(t + 16) >> shift] : -1;
+            }
             const int t0 = (step0 + wave + i * kWaves) * kv::kStep;
             const uint8_t *kp[2], *vp[2];
-            masked[d] = t0 < lo || t0 + kv::kStep > hi;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int t = t0 + 16 * x;
-                // (a block past the request's end is not looked up: its page may not exist)
-                const int id = t < hi ? __builtin_amdgcn_readfirstlane(table[t >> shift]) : -1;
-                const bool on = id >= 0 && id < a.c.pages;
-                ids[d][x] = on;
-                masked[d] |= !on;
-                const int64_t off = (on ? (int64_t)id * a.c.page_stride : 0) + head_off +
+                const int id = __builtin_amdgcn_readlane(pages[x], i & 63);
+                on[d][x] = id >= 0 && id < a.c.pages;
+                const int64_t off = (on[d][x] ? (int64_t)id * a.c.page_stride : 0) + head_off +
                                     (int64_t)((t & ((1 << shift) - 1)) >> 4) * T::BB;
                 kp[x] = a.c.k + off;
                 vp[x] = a.c.v + off;
@@ -361,10 +397,8 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
         auto work = [&](int d, int i) {
             const int t0 = (step0 + wave + i * kWaves) * kv::kStep;
             // blocks without a page are left out: the visible range shrinks to the other one, or to nothing
-            int from = lo, to = hi;
-            if (!ids[d][0]) from = max(from, t0 + 16);
-            if (!ids[d][1]) to = min(to, t0 + 16);
-            work_step<D, FMT, WIDE>(st, buf[d], q, scale, masked[d], t0, from, to, lane);
+            const int from = on[d][0] ? lo : max(lo, t0 + 16), to = on[d][1] ? hi : min(hi, t0 + 16);
+            work_step<D, FMT, WIDE>(st, buf[d], q, scale, from > t0 || to < t0 + kv::kStep, t0, from, to, lane);
         };
         if (mine > 0) rs::pipelined<DEPTH>(mine, load, work);
 
@@ -384,30 +418,114 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
         const float f = part_weight(st.m, M);
         const int waves = min(n, kWaves);                        // those that had steps
 
-        const int tf = kv::team_of(total, teams, item_begin), tl = kv::team_of(total, teams, item_begin + nb - 1);
+        const int tf = who.first, tl = who.last;
         const bool whole = tf == tl;
-        const uint32_t slot = (uint32_t)(2 * self + (item_begin < begin ? 0 : 1)) * part_stride;
+        const uint32_t slot = (uint32_t)(2 * self + (self == tf ? 1 : 0)) * part_stride;
         uint16_t* out = a.a.out + b * a.a.out_stride + (int64_t)q0 * D;
 
+        // The sum of `count` parts, of teams t0, t0 + by, ...: to the output, or in the place of the first, whose
+        // threads alone read them (its statistics, which all read, stay beside the run's).  Threads that have no four
+        // dimensions of their own take a share of the parts, and the shares add up in LDS.
+        auto join = [&](int t0, int count, int by, bool final) {
+            auto place = [&](int t) { return (uint32_t)(2 * t + (t == tf ? 1 : 0)) * part_stride; };
+            const uint32_t stats_at = (uint32_t)(kv::item_heads(g) * D) * 4, run_stats = 2 * kv::kCols * 4;
+            const int tasks = heads * (D / 4), groups = max(1, min(kThreads / tasks, count));
+            for (int x0 = 0; x0 < tasks; x0 += kThreads) {
+                const int group = groups > 1 ? tid / tasks : 0, x = groups > 1 ? tid - group * tasks : x0 + tid;
+                const int c = x / (D / 4), e = x % (D / 4) * 4;
+                const bool works = x < tasks && group < groups;
+                float m = -INFINITY, lt = 0.0f;
+                f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+                constexpr int N = kv::kJoin;                     // parts in flight
+                const int p0 = count * group / groups, p1 = works ? count * (group + 1) / groups : p0;
+                for (int p = p0; p < p1; p += N) {
+                    float pm[N], pl[N];
+                    f32x4_t po[N];
 #pragma unroll
-        for (int r = 0; r < T::R; ++r) {
-            if (r) __syncthreads();
+                    for (int i = 0; i < N; ++i) {
+                        if (p + i >= p1) continue;
+                        const int t = t0 + (p + i) * by;
+                        const uint32_t s = place(t), stats = stats_at + (by > 1 && t < tl ? run_stats : 0);
+                        pm[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(parts, s + stats + c * 4, 0, kAgent));
+                        pl[i] = __uint_as_float(
+                            __builtin_amdgcn_raw_buffer_load_b32(parts, s + stats + (kv::kCols + c) * 4, 0, kAgent));
+                        po[i] = __builtin_bit_cast(
+                            f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(parts, s + (uint32_t)(c * D + e) * 4, 0, kAgent));
+                    }
+                    float mn = m;
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        if (p + i < p1) mn = fmaxf(mn, pm[i]);
+                    const float f0 = part_weight(m, mn);
+                    lt *= f0;
+                    o *= f0;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        if (p + i >= p1) continue;
+                        const float f1 = part_weight(pm[i], mn);
+                        lt += pl[i] * f1;
+                        o += po[i] * f1;
+                    }
+                    m = mn;
+                }
+                if (groups > 1) {
+                    float* js = wo + kThreads * 4;               // (no wave reads wo any more)
+                    if (works) {
+                        *reinterpret_cast<f32x4_t*>(wo + tid * 4) = o;
+                        js[tid] = m;
+                        js[kThreads + tid] = lt;
+                    }
+                    __syncthreads();
+                    if (works && group == 0) {
+                        for (int i = 1; i < groups; ++i) m = fmaxf(m, js[i * tasks + x]);
+                        lt = 0.0f;
+                        o = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                        for (int i = 0; i < groups; ++i) {
+                            const float f1 = part_weight(js[i * tasks + x], m);
+                            lt += js[kThreads + i * tasks + x] * f1;
+                            o += *reinterpret_cast<const f32x4_t*>(wo + (i * tasks + x) * 4) * f1;
+                        }
+                    }
+                }
+                if (works && group == 0) {
+                    if (final) {
+                        const float sink = a.a.sinks ? a.a.sinks[q0 + c] * kLog2e : -INFINITY, mn = fmaxf(m, sink);
+                        const float f1 = part_weight(m, mn);
+                        store_out(out + (int64_t)c * D + e, o * f1, lt * f1 + part_weight(sink, mn), v_scale);
+                    } else {
+                        const uint32_t s = place(t0), stats = stats_at + run_stats;
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), parts,
+                                                               s + (uint32_t)(c * D + e) * 4, 0, kAgent);
+                        if (e == 0) {
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), parts, s + stats + c * 4, 0, kAgent);
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lt), parts,
+                                                                  s + stats + (kv::kCols + c) * 4, 0, kAgent);
+                        }
+                    }
+                }
+            }
+        };
+#pragma unroll
+        for (int round = 0; round < T::R * kHalves; ++round) {
+            const int r = round / kHalves, half = round % kHalves * kUnit;
+            if (round) __syncthreads();
 #pragma unroll
             for (int v = 0; v < 4; ++v)
 #pragma unroll
-                for (int i = 0; i < T::cv; i += 4) {
+                for (int i = 0; i < kUnit; i += 4) {
                     f32x4_t o;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        o[e] = st.o[r * T::cv + i + e][v] * f;
+                        o[e] = st.o[r * T::cv + half + i + e][v] * f;
                         if constexpr (!WIDE) o[e] += other_half(o[e]);
                     }
                     if (col < heads && wave < waves)
-                        *reinterpret_cast<f32x4_t*>(wo + (wave * heads + col) * kRow + (4 * (lane >> 4) + v) * T::cv + i) = o;
+                        *reinterpret_cast<f32x4_t*>(wo + (wave * heads + col) * kRow + (4 * (lane >> 4) + v) * kUnit + i) = o;
                 }
             __syncthreads();
             for (int x = tid; x < heads * (kChunk / 4); x += kThreads) {
                 const int c = x / (kChunk / 4), e = x % (kChunk / 4) * 4;
+                const int dim = r * 16 * T::cv + e / kUnit * T::cv + half + e % kUnit;
                 f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
                 for (int w = 0; w < waves; ++w) o += *reinterpret_cast<const f32x4_t*>(wo + (w * heads + c) * kRow + e);
                 if (whole) {
@@ -421,10 +539,10 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
                         lt += wl[w * kv::kCols + c] * part_weight(wm[w * kv::kCols + c], mm);
                     lt += part_weight(sink, mm);
                     o *= part_weight(m, mm);
-                    store_out(out + (int64_t)c * D + r * kChunk + e, o, lt, v_scale);
+                    store_out(out + (int64_t)c * D + dim, o, lt, v_scale);
                 } else {
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), parts,
-                                                           slot + (uint32_t)(c * D + r * kChunk + e) * 4, 0, kAgent);
+                                                           slot + (uint32_t)(c * D + dim) * 4, 0, kAgent);
                 }
             }
         }
@@ -441,52 +559,32 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
                 __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), parts, p, 0, kAgent);
                 __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lt), parts, p + kv::kCols * 4, 0, kAgent);
             }
-            if (last_arrival(a.counters + tf, (uint32_t)(tl - tf + 1), &flag)) {
-                // every part of the item is there: their sum, in the teams' order
-                for (int x = tid; x < heads * (D / 4); x += kThreads) {
-                    const int c = x / (D / 4), e = x % (D / 4) * 4;
-                    const float sink = a.a.sinks ? a.a.sinks[q0 + c] * kLog2e : -INFINITY;
-                    float m = sink, lt = sink == -INFINITY ? 0.0f : 1.0f;
-                    f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-                    constexpr int N = 8;                         // parts in flight
-                    for (int t = tf; t <= tl; t += N) {
-                        float pm[N], pl[N];
-                        f32x4_t po[N];
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const int u = min(t + i, tl);
-                            const uint32_t s = (uint32_t)(2 * u + (u == tf ? 1 : 0)) * part_stride;
-                            const uint32_t p = s + (uint32_t)(kv::item_heads(g) * D + c) * 4;
-                            pm[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(parts, p, 0, kAgent));
-                            pl[i] = __uint_as_float(
-                                __builtin_amdgcn_raw_buffer_load_b32(parts, p + kv::kCols * 4, 0, kAgent));
-                            po[i] = __builtin_bit_cast(
-                                f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(parts, s + (uint32_t)(c * D + e) * 4, 0,
-                                                                               kAgent));
-                        }
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            if (t + i > tl) continue;
-                            const float mn = fmaxf(m, pm[i]);
-                            const float f0 = part_weight(m, mn), f1 = part_weight(pm[i], mn);
-                            lt = lt * f0 + pl[i] * f1;
-                            o = o * f0 + po[i] * f1;
-                            m = mn;
-                        }
-                    }
-                    store_out(out + (int64_t)c * D + e, o, lt, v_scale);
-                }
+            // the run's last team adds its parts up, and the last run's team the runs' sums (a run of one is its
+            // part)
+            const int run = kv::join_run(who), r0 = tf + (self - tf) / run * run, rn = min(run, tl - r0 + 1);
+            const int runs = (tl - tf) / run + 1;
+            bool go_on = true;
+            if (runs > 1 && rn > 1) {
+                go_on = last_arrival(a.counters + r0, (uint32_t)rn, &flag);
+                if (go_on) join(r0, rn, 1, false);
             }
+            if (go_on && last_arrival(a.counters + kv::kMaxTeams + tf, (uint32_t)(runs > 1 ? runs : rn), &flag))
+                join(tf, runs > 1 ? runs : rn, runs > 1 ? run : 1, true);
         }
+        if (a.direct) return;
         __syncthreads();                                         // the next segment writes wm, wl and wo
     }
 }
 
 template <int D, int FMT, bool WIDE>
 hipError_t go(const AttendArgs& a, int grid, hipStream_t st) {
-    const size_t lds = (((size_t)a.a.requests + 1 + 3) & ~(size_t)3) * 4 + 2 * kWaves * kv::kCols * 4 +
-                       (size_t)kWaves * kv::item_heads(a.g) * (D / Kv<D, FMT>::R + 4) * 4;
-    return launch(attend_kernel<D, FMT, WIDE, 1>, dim3(grid), dim3(kThreads), lds, st, a);
+    // (the join's shares take 6 floats a thread)
+    const size_t row = 16 * (WIDE ? 4 : Kv<D, FMT>::cv) + 4;
+    const size_t waves = (size_t)kWaves * kv::item_heads(a.g) * row * 4, join = kThreads * 6 * 4;
+    const size_t list = a.direct ? 0 : ((size_t)2 * a.a.requests + 1 + 3) & ~(size_t)3;
+    const size_t lds = list * 4 + 2 * kWaves * kv::kCols * 4 +
+                       (waves > join ? waves : join);
+    return launch(attend_kernel<D, FMT, WIDE, kDepth>, dim3(grid), dim3(kThreads), lds, st, a);
 }
 
 template <int D>
@@ -512,7 +610,10 @@ hipError_t launch_kv_attend(const CacheView& c, const ft_attend& q, ft_workspace
     a.counters = reinterpret_cast<uint32_t*>(ws->mem);
     const int64_t most = (((int64_t)q.width << c.page_shift) + kv::kStep - 1) / kv::kStep + (q.window ? 1 : 0);
     const int64_t seen = q.window ? q.window / kv::kStep + 2 : most;
-    const int grid = kv::grid_of((int64_t)q.requests * c.heads * a.blocks * (seen < most ? seen : most));
+    const int64_t items = (int64_t)q.requests * c.heads * a.blocks, steps = seen < most ? seen : most;
+    a.direct = steps <= kv::kDirectSteps;
+    const int teams = kv::kComputeUnits * kv::teams_per_cu(c.D, c.fmt == FT_KV_BF16 ? 2 : 1);
+    const int grid = a.direct ? (int)items : kv::grid_of(items, items * steps, teams);
     if (c.D == 64) return pick<64>(a, grid, st);
     if (c.D == 128) return pick<128>(a, grid, st);
     return pick<256>(a, grid, st);

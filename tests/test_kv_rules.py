@@ -1,5 +1,4 @@
-"""How attention's work is divided (csrc/kv_rules.h): the teams' ranges cover every step once, team_of finds the team of
-a step, parts of one item have slots of their own, and the join counts each of them.  Compiled as plain C++; CPU only."""
+"""How attention's work is divided (csrc/kv_rules.h): every step of every item belongs to one team, parts of one item have slots of their own, and the join counts each of them.  Compiled as plain C++; CPU only."""
 import os
 import subprocess
 
@@ -21,39 +20,62 @@ using namespace ftmoe::kv;
 
 int division(const std::vector<int>& items, int grid) {
     std::vector<long long> first{0};
-    for (int n : items) first.push_back(first.back() + n);
+    long long busy = 0;
+    for (int n : items) {
+        first.push_back(first.back() + n);
+        busy += n > 0;
+    }
     const long long total = first.back();
-    const int teams = teams_of(total, grid);
-    CHECK(teams >= 1 && teams <= grid && teams <= total && teams <= kMaxTeams);
-    CHECK(team_begin(total, teams, 0) == 0 && team_begin(total, teams, teams) == total);
+    const Division d = divide(busy, total, grid);
+    CHECK(d.teams >= 1 && d.teams <= grid && d.teams <= total && d.teams <= kMaxTeams);
+    CHECK(cut(d, 0) == 0 && cut(d, d.teams) == total && d.slack >= 0 && 2 * d.slack < total / d.teams + 1);
+    std::vector<int> load(d.teams, 0);
     std::map<int, int> arrived;                       // by counter
     std::map<int, int> expected;
     std::set<int> slots;
-    for (int t = 0; t < teams; ++t) {
-        const long long b = team_begin(total, teams, t), e = team_begin(total, teams, t + 1);
-        CHECK(b < e);
-        for (long long s = b; s < e; ++s) CHECK(team_of(total, teams, s) == t);
-        int open = 0;                                 // items that go on in the next team
-        for (size_t i = 0; i < items.size(); ++i) {
-            if (items[i] == 0 || first[i] >= e || first[i + 1] <= b) continue;
-            const int tf = team_of(total, teams, first[i]), tl = team_of(total, teams, first[i + 1] - 1);
-            if (tf == tl) continue;
-            const int slot = 2 * t + (first[i] < b ? 0 : 1);
-            CHECK(slots.insert(slot).second);         // no two parts in one place
-            CHECK(slot == 2 * t + (t == tf ? 1 : 0)); // where the join looks for it
-            if (t == tf) ++open;
-            ++arrived[tf];
-            expected[tf] = tl - tf + 1;
+    for (size_t i = 0; i < items.size(); ++i) {
+        const int n = items[i];
+        if (n == 0) continue;
+        const Teams who = teams_of(d, first[i], n);
+        CHECK(0 <= who.first && who.first <= who.last && who.last < d.teams);
+        int next = 0;
+        for (int t = who.first; t <= who.last; ++t) {
+            const Segment s = segment(d, who, first[i], n, t);
+            CHECK(s.from == next && s.to > s.from);   // every step once, in order
+            next = s.to;
+            load[t] += s.to - s.from;
+            if (who.first == who.last) continue;
+            CHECK(slots.insert(2 * t + (t == who.first ? 1 : 0)).second);     // no two parts in one place
+            ++arrived[who.first];
         }
-        CHECK(open <= 1);                             // so a team's counter serves one item
+        CHECK(next == n);
+        if (who.first != who.last) {
+            CHECK(!expected.count(who.first));        // a team's counter serves one item
+            expected[who.first] = who.last - who.first + 1;
+        }
     }
     CHECK(arrived == expected);
+    for (int t = 0; t < d.teams; ++t) CHECK(load[t] <= total / d.teams + 1 + 2 * d.slack);
+    // how a team finds its items: from the one that its cut falls into, on while they are its own
+    for (int t = 0; t < d.teams; ++t) {
+        size_t i = 0;
+        while (!(first[i] <= cut(d, t) && cut(d, t) < first[i + 1])) ++i;
+        for (int mine = 0;; ++i) {
+            while (i < items.size() && items[i] == 0) ++i;
+            if (i == items.size()) { CHECK(mine == load[t]); break; }
+            const Teams who = teams_of(d, first[i], items[i]);
+            if (t > who.last) { CHECK(mine == 0); continue; }
+            if (t < who.first) { CHECK(mine == load[t]); break; }
+            const Segment s = segment(d, who, first[i], items[i], t);
+            mine += s.to - s.from;
+        }
+    }
     return 0;
 }
 
 int main() {
     srand(5);
-    const int grids[] = {1, 2, 3, 7, 64, 511, kMaxTeams};
+    const int grids[] = {1, 2, 3, 7, 64, 511, 512, kMaxTeams};
     for (int g : grids)
         for (int r = 0; r < 60; ++r) {
             std::vector<int> items;
@@ -62,18 +84,32 @@ int main() {
             items.push_back(1);
             if (division(items, g)) return 1;
         }
-    // totals beyond 32 bits
-    for (long long total : {1ll << 31, (1ll << 38) + 12345, (1ll << 41) - 1})
-        for (int t = 0; t < kMaxTeams; ++t) {
-            const long long b = team_begin(total, kMaxTeams, t), e = team_begin(total, kMaxTeams, t + 1);
-            CHECK(b < e && team_of(total, kMaxTeams, b) == t && team_of(total, kMaxTeams, e - 1) == t);
+    // equal short items are not cut
+    for (int n = 1; n <= 40; ++n)
+        for (int items : {1, 3, 64, 100, 500}) {
+            const Division d = divide(items, (long long)items * n, kMaxTeams);
+            for (int i = 0; i < items && n <= kWaves; ++i) {
+                const Teams who = teams_of(d, (long long)i * n, n);
+                CHECK(who.first == who.last);
+            }
         }
+    // totals beyond 32 bits
+    for (long long total : {1ll << 31, (1ll << 38) + 12345, (1ll << 41) - 1}) {
+        const Division d = divide(total >> 20, total, kMaxTeams);
+        CHECK(cut(d, 0) == 0 && cut(d, d.teams) == total);
+        for (int t = 0; t < d.teams; ++t) {
+            const long long b = cut(d, t), e = cut(d, t + 1);
+            CHECK(b < e && team_at(d, b) == t && team_at(d, e - 1) == t);
+        }
+    }
     for (int g : {1, 8, 9, 16, 17, 32, 33, 128}) {
         int n = 0;
         for (int i = 0; i < head_blocks(g); ++i) n += g - i * kCols < kCols ? g - i * kCols : kCols;
         CHECK(n == g && item_heads(g) <= kCols);
     }
-    CHECK(grid_of(0) == 1 && grid_of(1ll << 40) == kMaxTeams);
+    CHECK(grid_of(1, 1, kMaxTeams) == 1 && grid_of(4096, 1ll << 40, 700) == 700);
+    for (int D : {64, 128, 256})
+        for (int e : {1, 2}) CHECK(kComputeUnits * teams_per_cu(D, e) <= kMaxTeams);
     printf("ok\n");
     return 0;
 }
