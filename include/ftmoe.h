@@ -684,8 +684,9 @@ ft_status ft_kv_append(const ft_kv_cache* cache, const ft_append* args, void* st
  * KV head h / (q_heads / kv_heads).  sinks fp32 [q_heads], or NULL: no such term.
  * requests 0..4096 (0 enqueues nothing); q_heads: a multiple of kv_heads, at
  *   most 1024; table [requests x width]; kv_len [requests] (clamped to
- *   0..width * page_tokens); requests * width * page_tokens below 2^36.  q, out
- *   [requests x q_heads x head_dim] bf16.  scale is finite.
+ *   0..width * page_tokens); requests * kv_heads * ceil(q_heads / kv_heads / 16) *
+ *   width * page_tokens at most 2^35.  q, out [requests x q_heads x head_dim]
+ *   bf16.  scale is finite.
  * A position whose page id is outside 0..pages - 1 is left out.  A request that
  * sees no position gets zeros.  What pages hold beyond the visible positions,
  * and table entries beyond them, reaches no result.

@@ -153,9 +153,10 @@ ft_status ft_kv_attend(const ft_kv_cache* cache, const ft_attend* a, ft_workspac
     FT_REQUIRE(a->requests >= 0 && a->requests <= kv::kMaxRequests, "requests must be in 0..%d", kv::kMaxRequests);
     s = check_q_heads(a->q_heads, c.heads);
     if (s != FT_OK) return s;
-    FT_REQUIRE(a->width >= 1 && a->width <= kv::kMaxWidth &&
-                   ((int64_t)a->requests * a->width << c.page_shift) < ((int64_t)1 << 36),
-               "width must be in 1..%d, and requests * width * page_tokens below 2^36", kv::kMaxWidth);
+    FT_REQUIRE(a->width >= 1 && a->width <= kv::kMaxWidth, "width must be in 1..%d", kv::kMaxWidth);
+    const int64_t items = (int64_t)a->requests * c.heads * kv::head_blocks(a->q_heads / c.heads);
+    FT_REQUIRE(items * (((int64_t)a->width << c.page_shift) / kv::kBlock) <= 2 * kv::kMaxSteps,
+               "requests * kv_heads * ceil(group / 16) * width * page_tokens must be at most 2^35");
     FT_REQUIRE(a->window >= 0, "window must be >= 0");
     FT_REQUIRE(isfinite(a->scale), "scale must be finite");
     FT_REQUIRE(a->reserved == 0, "reserved must be 0");

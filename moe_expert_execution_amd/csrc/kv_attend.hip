@@ -26,7 +26,6 @@ namespace {
 
 using rs::last_arrival;
 constexpr int kWaves = kv::kWaves, kThreads = kWaves * 64;
-constexpr int kDepth = 1;                 // steps in flight per wave
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct AttendArgs {
@@ -43,6 +42,11 @@ struct AttendArgs {
 // see each other.
 constexpr int kAgent = 16;
 
+constexpr uint32_t kRunStats = 2 * kv::kCols * 4;        // a run's statistics, behind its first part's
+
+// A value that all lanes of the wave have, as a scalar.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
 template <int D, int FMT>
@@ -53,39 +57,33 @@ struct Kv {
     static constexpr int L = BB / 1024;                // 16-byte loads of a lane per block
     static constexpr int R = D / (16 * cv);            // rounds of 16 value units
     static constexpr int S = D / 32;                   // matrix-core steps of a block's keys
+    typedef u32x4_t Block[L];                          // a block's keys or values in registers, as stored
 };
 
-// One step's keys and values in registers, as stored.
+// One step: two blocks.
 template <int D, int FMT>
 struct Step {
-    u32x4_t k[2][Kv<D, FMT>::L];
-    u32x4_t v[2][Kv<D, FMT>::L];
+    typename Kv<D, FMT>::Block k[2], v[2];
 };
 
 template <int D, int FMT>
-__device__ __forceinline__ void load_step(Step<D, FMT>& s, const uint8_t* k0, const uint8_t* v0, const uint8_t* k1,
-                                          const uint8_t* v1, int lane) {
+__device__ __forceinline__ void load_keys(typename Kv<D, FMT>::Block& k, const uint8_t* p, int lane) {
+#pragma unroll
+    for (int i = 0; i < Kv<D, FMT>::L; ++i)
+        k[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p + i * 1024 + lane * 16));
+}
+
+template <int D, int FMT>
+__device__ __forceinline__ void load_values(typename Kv<D, FMT>::Block& v, const uint8_t* p, int lane) {
     using T = Kv<D, FMT>;
-    const int q = lane >> 4, m = lane & 15;
+    constexpr int N = 4 / T::tu;                       // units of a lane's four tokens
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        const uint8_t* k = b ? k1 : k0;
+    for (int r = 0; r < T::R; ++r)
 #pragma unroll
-        for (int i = 0; i < T::L; ++i)
-            s.k[b][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(k + i * 1024 + lane * 16));
-    }
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        const uint8_t* v = b ? v1 : v0;
-#pragma unroll
-        for (int r = 0; r < T::R; ++r)
-#pragma unroll
-            for (int i = 0; i < 4 / T::tu; ++i) {
-                const int unit = ((4 / T::tu) * q + i) * (D / T::cv) + r * 16 + m;
-                s.v[b][r * (4 / T::tu) + i] =
-                    __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(v + unit * 16));
-            }
-    }
+        for (int i = 0; i < N; ++i) {
+            const int unit = (N * (lane >> 4) + i) * (D / T::cv) + r * 16 + (lane & 15);
+            v[r * N + i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p + unit * 16));
+        }
 }
 
 __device__ __forceinline__ uint32_t cvt_pair(uint32_t w, bool high) {
@@ -96,7 +94,7 @@ __device__ __forceinline__ uint32_t cvt_pair(uint32_t w, bool high) {
 
 // The A operand of step j of a block's keys.
 template <int D, int FMT>
-__device__ __forceinline__ bf16x8_t key_frag(const u32x4_t (&k)[Kv<D, FMT>::L], int j) {
+__device__ __forceinline__ bf16x8_t key_frag(const typename Kv<D, FMT>::Block& k, int j) {
     if constexpr (FMT == FT_KV_BF16) {
         return __builtin_bit_cast(bf16x8_t, k[j]);
     } else {
@@ -107,7 +105,7 @@ __device__ __forceinline__ bf16x8_t key_frag(const u32x4_t (&k)[Kv<D, FMT>::L], 
 // Two tokens' value at dimension i (of cv) of round r, tokens 2 p and 2 p + 1 of the lane's
 // four, as one register of the A operand.
 template <int D, int FMT>
-__device__ __forceinline__ uint32_t value_pair(const u32x4_t (&v)[Kv<D, FMT>::L], int r, int i, int p) {
+__device__ __forceinline__ uint32_t value_pair(const typename Kv<D, FMT>::Block& v, int r, int i, int p) {
     using T = Kv<D, FMT>;
     constexpr int N = 4 / T::tu;
     if constexpr (T::E == 2) {
@@ -134,22 +132,64 @@ struct State {
     float m, l;          // maximum in base 2; this lane's share of the sum
 };
 
-template <int D, int FMT, bool WIDE>
-__device__ __forceinline__ void work_step(State<D, FMT, WIDE>& st, const Step<D, FMT>& x,
-                                          const bf16x8_t (&q)[Kv<D, FMT>::S], float scale, bool masked, int t0, int lo,
-                                          int hi, int lane) {
-    using T = Kv<D, FMT>;
-    float s[2][4];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < T::S; ++j)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key_frag<D, FMT>(x.k[b], j), q[j], acc, 0, 0, 0);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) s[b][v] = acc[v] * scale;
+// The query operands of a wave: in registers, or (256 dimensions: with the sums and a step's keys and values they
+// pass the 256 registers of two waves) in LDS, one copy for the workgroup.
+template <int D, int FMT>
+struct Queries {
+    static constexpr bool kShared = D == 256;
+    bf16x8_t r[kShared ? 1 : Kv<D, FMT>::S];
+    const u32x4_t* lds;      // [S][64 lanes]
+    __device__ __forceinline__ bf16x8_t operator()(int j, int lane) const {
+        if constexpr (kShared) return __builtin_bit_cast(bf16x8_t, lds[j * 64 + lane]);
+        else return r[j];
     }
-    uint32_t keep[2][2] = {{~0u, ~0u}, {~0u, ~0u}};    // halves of value pairs that are visible
+};
+
+// The step's logits in base 2: tokens 16 b + 4 (l / 16) + v of column l % 16.
+template <int D, int FMT>
+__device__ __forceinline__ void logits(float (&s)[2][4], const Step<D, FMT>& x, const Queries<D, FMT>& q, float scale,
+                                       int lane) {
+    using T = Kv<D, FMT>;
+    f32x4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+    for (int j = 0; j < T::S; ++j) {
+        const bf16x8_t y = q(j, lane);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key_frag<D, FMT>(x.k[b], j), y, acc[b], 0, 0, 0);
+        if constexpr (D == 256) __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) s[b][v] = acc[b][v] * scale;
+}
+
+// f over the four lanes of a column, l % 16.
+template <typename F>
+__device__ __forceinline__ float quarters(float v, F&& f) {
+    const uint32_t a = __float_as_uint(v);
+    const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    const uint32_t b = __float_as_uint(f(__uint_as_float(p[0]), __uint_as_float(p[1])));
+    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// A step's probabilities as operands (WIDE: high and low halves; else both in `high`), and which halves of
+// value pairs are visible.
+struct Probs {
+    u32x4_t high, low;
+    uint32_t keep[2][2];
+    float alpha;             // what the sums so far are multiplied with
+};
+
+// Positions t0 + 16 b + 4 (l / 16) + v outside lo .. hi - 1 count for nothing.
+template <int D, int FMT, bool WIDE>
+__device__ __forceinline__ Probs softmax_step(State<D, FMT, WIDE>& st, float (&s)[2][4], bool masked, int t0, int lo,
+                                              int hi, int lane) {
+    Probs out;
+    uint32_t (&keep)[2][2] = out.keep;
+    keep[0][0] = keep[0][1] = keep[1][0] = keep[1][1] = ~0u;
     if (masked) {
         const int t = t0 + 4 * (lane >> 4);
 #pragma unroll
@@ -165,11 +205,10 @@ __device__ __forceinline__ void work_step(State<D, FMT, WIDE>& st, const Step<D,
     }
     float mt = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-    mt = fmaxf(mt, __shfl_xor(mt, 16));
-    mt = fmaxf(mt, __shfl_xor(mt, 32));
+    mt = quarters(mt, [](float x, float y) { return fmaxf(x, y); });
     const float m = fmaxf(st.m, mt);
     const float base = m == -INFINITY ? 0.0f : m;      // (nothing visible so far: all terms are 0)
-    const float alpha = exp2_of(st.m - base);
+    out.alpha = exp2_of(st.m - base);
     st.m = m;
     float sum = 0.0f;
     uint32_t hi_p[4], lo_p[4];
@@ -184,13 +223,18 @@ __device__ __forceinline__ void work_step(State<D, FMT, WIDE>& st, const Step<D,
             hi_p[b * 2 + p] = __builtin_bit_cast(uint32_t, h);
             lo_p[b * 2 + p] = __builtin_bit_cast(uint32_t, r);
         }
-    st.l = st.l * alpha + sum;
-    u32x4_t ph, pl;
+    st.l = st.l * out.alpha + sum;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        ph[i] = WIDE || !(lane & 8) ? hi_p[i] : lo_p[i];
-        pl[i] = lo_p[i];
+        out.high[i] = WIDE || !(lane & 8) ? hi_p[i] : lo_p[i];
+        out.low[i] = lo_p[i];
     }
+    return out;
+}
+
+template <int D, int FMT, bool WIDE>
+__device__ __forceinline__ void add_values(State<D, FMT, WIDE>& st, const Step<D, FMT>& x, const Probs& p) {
+    using T = Kv<D, FMT>;
 #pragma unroll
     for (int r = 0; r < T::R; ++r)
 #pragma unroll
@@ -199,13 +243,15 @@ __device__ __forceinline__ void work_step(State<D, FMT, WIDE>& st, const Step<D,
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int p = 0; p < 2; ++p) a[b * 2 + p] = value_pair<D, FMT>(x.v[b], r, i, p) & keep[b][p];
+                for (int h = 0; h < 2; ++h) a[b * 2 + h] = value_pair<D, FMT>(x.v[b], r, i, h) & p.keep[b][h];
             f32x4_t& o = st.o[r * T::cv + i];
-            o *= alpha;
+            o *= p.alpha;
             const bf16x8_t av = __builtin_bit_cast(bf16x8_t, a);
-            o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8_t, ph), o, 0, 0, 0);
+            o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8_t, p.high), o, 0, 0, 0);
             if constexpr (WIDE)
-                o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8_t, pl), o, 0, 0, 0);
+                o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8_t, p.low), o, 0, 0, 0);
+            // (256 dimensions: operands are made one at a time, not all ahead, which would take their registers)
+            if constexpr (D == 256) __builtin_amdgcn_sched_barrier(0);
         }
 }
 
@@ -230,20 +276,21 @@ __device__ __forceinline__ void store_out(uint16_t* to, const f32x4_t o, float l
                                               (uint32_t)f32_to_bf16_rne(x[2]) | (uint32_t)f32_to_bf16_rne(x[3]) << 16};
 }
 
-template <int D, int FMT, bool WIDE, int DEPTH>
-__global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) attend_kernel(AttendArgs a) {
+template <int D, int FMT, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 2) attend_kernel(AttendArgs a) {
     using T = Kv<D, FMT>;
     constexpr int kUnit = WIDE ? 4 : T::cv, kHalves = T::cv / kUnit;  // dimensions of a value unit that a round takes
     constexpr int kChunk = 16 * kUnit, kRow = kChunk + 4;        // dimensions of a round; padded in LDS
     extern __shared__ int lds[];
-    const int B = a.a.requests, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int* pre = lds;                                              // [B + 1] steps of the requests before
+    const int B = a.a.requests, tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    int* pre = lds;                                              // [B + 1] length of an item of each request before
     int* lens = pre + B + 1;                                     // [B] visible lengths' ends
     float* wm = reinterpret_cast<float*>(lds + (a.direct ? 0 : (2 * B + 1 + 3) & ~3));   // [kWaves][16]
     float* wl = wm + kWaves * kv::kCols;
     float* wo = wl + kWaves * kv::kCols;                         // [kWaves][heads][kRow]
     __shared__ uint32_t flag;
     __shared__ int scan[2][kWaves];
+    __shared__ u32x4_t wq[Queries<D, FMT>::kShared ? T::S * 64 : 1];
     const int shift = a.c.page_shift, room = a.a.width << shift;
 
     auto first_of = [&](int hi) { return a.a.window && hi > a.a.window ? hi - a.a.window : 0; };
@@ -255,11 +302,11 @@ __global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) 
         return hi ? (hi + kv::kStep - 1) / kv::kStep - first_of(hi) / kv::kStep : 0;
     };
     const int g = a.g, heads_all = a.c.heads * a.blocks;
-    // the requests' steps, summed in slices of the workgroup's width, and how many have any
+    // the lengths of the requests' items, summed in slices of the workgroup's width, and how many have any
     int carry = 0, busy = 0;
     for (int b0 = 0; b0 < B && !a.direct; b0 += kThreads) {
         const int b = b0 + tid;
-        const int hi = b < B ? end_of(b) : 0, own = steps_of(hi);
+        const int hi = b < B ? end_of(b) : 0, own = kv::item_length(steps_of(hi));
         int x = own;
         const int some = __popcll(__ballot(own > 0));
 #pragma unroll
@@ -276,9 +323,10 @@ __global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) 
         int before = carry;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            if (w < wave) before += scan[0][w];
-            carry += scan[0][w];
-            busy += scan[1][w];
+            const int sum = uniform(scan[0][w]);
+            if (w < wave) before += sum;
+            carry += sum;
+            busy += uniform(scan[1][w]);
         }
         if (b < B) {
             pre[b] = before + x - own;
@@ -300,18 +348,19 @@ __global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) 
                 for (int i = tid * 8; i < a.a.q_heads * D; i += kThreads * 8)
                     *reinterpret_cast<u32x4_t*>(a.a.out + r * a.a.out_stride + i) = u32x4_t{0, 0, 0, 0};
         if (carry == 0) return;
-        div = kv::divide((int64_t)busy * heads_all, (int64_t)carry * heads_all, gridDim.x);
+        div = kv::divide((uint32_t)busy * heads_all, (uint32_t)carry * heads_all, gridDim.x);
         if (self >= div.teams) return;
         // the item that this team's cut falls into, before it moves (64 requests a look); then on from item to
         // item
-        const int64_t at = kv::cut(div, self);
-        const int q = (int)((double)at / (double)heads_all);     // (exact: both are whole numbers below 2^42 and 2^11)
+        const uint32_t at = kv::cut(div, self);
+        const int q = at / (uint32_t)heads_all;
         for (int left = B; left > 1;) {
             const int width = (left + 63) >> 6, i = lane * width;
             b += (__popcll(__ballot(i < left && pre[b + (i < left ? i : 0)] <= q)) - 1) * width;
             left = min(width, B - b);
         }
-        item = (int)((double)(at - (int64_t)pre[b] * heads_all) / (double)(pre[b + 1] - pre[b]));
+        const uint32_t before = uniform(pre[b]), length = uniform(pre[b + 1]) - before;
+        item = (at - before * heads_all) / length;
     }
     const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(a.part, 0, a.part_bytes, 0x00020000);
     const uint32_t part_stride = (uint32_t)kv::part_floats(g, D) * 4;
@@ -320,19 +369,22 @@ __global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) 
         int hi, nb, first = 0, n;                                // the request's length, the item's steps, this segment's
         kv::Teams who = {0, 0};
         if (a.direct) {
-            hi = end_of(b);
+            hi = uniform(end_of(b));
             n = nb = steps_of(hi);
         } else {
             if (item == heads_all) {
                 item = 0;
                 do ++b;
-                while (b < B && pre[b] == pre[b + 1]);
+                while (b < B && uniform(pre[b]) == uniform(pre[b + 1]));
                 if (b == B) return;
             }
-            hi = lens[b];
-            nb = pre[b + 1] - pre[b];
-            const int64_t item_begin = (int64_t)pre[b] * heads_all + (int64_t)item * nb;
+            hi = uniform(lens[b]);
+            const int before = uniform(pre[b]), length = uniform(pre[b + 1]) - before;
+            nb = length - kv::kItemCost;
+            const uint32_t item_begin = (uint32_t)before * heads_all + (uint32_t)item * length;
             who = kv::teams_of(div, item_begin, nb);
+            who.first = uniform(who.first);
+            who.last = uniform(who.last);
             if (self > who.last) continue;                       // (the cut has moved to the item's end)
             if (self < who.first) return;
             const kv::Segment seg = kv::segment(div, who, item_begin, nb, self);
@@ -346,18 +398,22 @@ __global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) 
         const float scale = a.a.scale * kLog2e * (FMT == FT_KV_E4M3 ? a.c.k_scale[h] : 1.0f);
         const float v_scale = FMT == FT_KV_E4M3 ? a.c.v_scale[h] : 1.0f;
 
-        bf16x8_t q[T::S];
+        Queries<D, FMT> q;
+        q.lds = wq;
         {
             const int col = WIDE ? lane & 15 : lane & 7, quarter = lane >> 4;
             const uint16_t* row = a.a.q + b * a.a.q_stride + (int64_t)(q0 + (col < heads ? col : 0)) * D;
 #pragma unroll
             for (int j = 0; j < T::S; ++j) {
+                if (Queries<D, FMT>::kShared && j % kWaves != wave) continue;
                 // the dimensions that key_frag's step j has at this quarter
                 const int e = T::E == 2 ? (j * 4 + quarter) * 8 : ((j >> 1) * 4 + quarter) * 16 + (j & 1) * 8;
                 u32x4_t v = *reinterpret_cast<const u32x4_t*>(row + e);
                 if (col >= heads) v = u32x4_t{0, 0, 0, 0};
-                q[j] = __builtin_bit_cast(bf16x8_t, v);
+                if constexpr (Queries<D, FMT>::kShared) wq[j * 64 + lane] = v;
+                else q.r[j] = __builtin_bit_cast(bf16x8_t, v);
             }
+            if constexpr (Queries<D, FMT>::kShared) __syncthreads();
         }
         State<D, FMT, WIDE> st;
 #pragma unroll
@@ -368,44 +424,66 @@ __global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) 
         const int64_t head_off = (int64_t)h * ((int64_t)(D * T::E) << shift);
         const int32_t* table = a.a.table + (int64_t)b * a.a.width;
         const int mine = (n - wave + kWaves - 1) / kWaves;       // this wave's steps: wave, wave + kWaves, ...
-        Step<D, FMT> buf[DEPTH];
-        bool on[DEPTH][2];
+        // The next step's keys are loaded once this one's have been used, its values likewise, into the same
+        // registers: one or the other is always under way.
+        Step<D, FMT> x;
         int pages[2] = {-1, -1};
-        auto load = [&](int d, int i) {
+        bool on[2], on_next[2];
+        int64_t off[2];
+        auto find = [&](int i) {
             if ((i & 63) == 0) {
                 // the page ids of this wave's next 64 steps, one step a lane (a block past the request's end is not
                 // looked up: it may have no entry)
                 const int t = (step0 + wave + (i + lane) * kWaves) * kv::kStep;
-                const bool mine_too = i + lane < mine;
-                pages[0] = mine_too && t < hi ? table[t >> shift] : -1;
-                pages[1] = mine_too && t + 16 < hi ? table[(t + 16) >> shift] : -1;
+                const bool some = i + lane < mine;
+                pages[0] = some && t < hi ? table[t >> shift] : -1;
+                pages[1] = some && t + 16 < hi ? table[(t + 16) >> shift] : -1;
+                // (waited for here: where the branches meet, every step would wait for all its loads)
+                asm volatile("" : "+v"(pages[0]), "+v"(pages[1]));
             }
             const int t0 = (step0 + wave + i * kWaves) * kv::kStep;
-            const uint8_t *kp[2], *vp[2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int t = t0 + 16 * x;
-                const int id = __builtin_amdgcn_readlane(pages[x], i & 63);
-                on[d][x] = id >= 0 && id < a.c.pages;
-                const int64_t off = (on[d][x] ? (int64_t)id * a.c.page_stride : 0) + head_off +
-                                    (int64_t)((t & ((1 << shift) - 1)) >> 4) * T::BB;
-                kp[x] = a.c.k + off;
-                vp[x] = a.c.v + off;
+            for (int b = 0; b < 2; ++b) {
+                const int id = __builtin_amdgcn_readlane(pages[b], i & 63);
+                on_next[b] = id >= 0 && id < a.c.pages;
+                off[b] = (on_next[b] ? (int64_t)id * a.c.page_stride : 0) + head_off +
+                         (int64_t)(((t0 + 16 * b) & ((1 << shift) - 1)) >> 4) * T::BB;
             }
-            load_step<D, FMT>(buf[d], kp[0], vp[0], kp[1], vp[1], lane);
         };
-        auto work = [&](int d, int i) {
+        auto keys = [&] {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) load_keys<D, FMT>(x.k[b], a.c.k + off[b], lane);
+        };
+        auto values = [&] {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) load_values<D, FMT>(x.v[b], a.c.v + off[b], lane);
+        };
+        if (mine > 0) {
+            find(0);
+            keys();
+            values();
+        }
+        for (int i = 0; i < mine; ++i) {
             const int t0 = (step0 + wave + i * kWaves) * kv::kStep;
+            on[0] = on_next[0];
+            on[1] = on_next[1];
+            float s[2][4];
+            logits<D, FMT>(s, x, q, scale, lane);
+            __builtin_amdgcn_sched_barrier(0);
+            // (behind the last step it is the pool's first page, which nothing waits for: were these loads
+            // conditional, every step would wait for all loads under way)
+            find(i + 1);
+            keys();
             // blocks without a page are left out: the visible range shrinks to the other one, or to nothing
-            const int from = on[d][0] ? lo : max(lo, t0 + 16), to = on[d][1] ? hi : min(hi, t0 + 16);
-            work_step<D, FMT, WIDE>(st, buf[d], q, scale, from > t0 || to < t0 + kv::kStep, t0, from, to, lane);
-        };
-        if (mine > 0) rs::pipelined<DEPTH>(mine, load, work);
+            const int from = on[0] ? lo : max(lo, t0 + 16), to = on[1] ? hi : min(hi, t0 + 16);
+            const Probs p = softmax_step<D, FMT, WIDE>(st, s, from > t0 || to < t0 + kv::kStep, t0, from, to, lane);
+            add_values<D, FMT, WIDE>(st, x, p);
+            __builtin_amdgcn_sched_barrier(0);
+            values();
+        }
 
         // ---- the waves' parts together ----
-        float l = st.l;
-        l += __shfl_xor(l, 16);
-        l += __shfl_xor(l, 32);
+        const float l = quarters(st.l, [](float x, float y) { return x + y; });
         const int col = lane & 15;
         if (lane < 16) {
             wm[wave * kv::kCols + col] = st.m;
@@ -420,15 +498,15 @@ __global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) 
 
         const int tf = who.first, tl = who.last;
         const bool whole = tf == tl;
-        const uint32_t slot = (uint32_t)(2 * self + (self == tf ? 1 : 0)) * part_stride;
+        const uint32_t slot = kv::part_slot(who, self) * part_stride, stats_at = (uint32_t)(kv::item_heads(g) * D) * 4;
         uint16_t* out = a.a.out + b * a.a.out_stride + (int64_t)q0 * D;
 
         // The sum of `count` parts, of teams t0, t0 + by, ...: to the output, or in the place of the first, whose
-        // threads alone read them (its statistics, which all read, stay beside the run's).  Threads that have no four
+        // threads alone read it (all read its statistics, so the run's have a place of their own).  Threads that have no four
         // dimensions of their own take a share of the parts, and the shares add up in LDS.
         auto join = [&](int t0, int count, int by, bool final) {
-            auto place = [&](int t) { return (uint32_t)(2 * t + (t == tf ? 1 : 0)) * part_stride; };
-            const uint32_t stats_at = (uint32_t)(kv::item_heads(g) * D) * 4, run_stats = 2 * kv::kCols * 4;
+            const uint32_t step = (uint32_t)by * part_stride, first_at = kv::part_slot(who, t0) * part_stride;
+            const uint32_t stats = stats_at + (by > 1 ? kRunStats : 0);
             const int tasks = heads * (D / 4), groups = max(1, min(kThreads / tasks, count));
             for (int x0 = 0; x0 < tasks; x0 += kThreads) {
                 const int group = groups > 1 ? tid / tasks : 0, x = groups > 1 ? tid - group * tasks : x0 + tid;
@@ -436,21 +514,21 @@ __global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) 
                 const bool works = x < tasks && group < groups;
                 float m = -INFINITY, lt = 0.0f;
                 f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-                constexpr int N = kv::kJoin;                     // parts in flight
+                constexpr int N = 8;                             // parts in flight
                 const int p0 = count * group / groups, p1 = works ? count * (group + 1) / groups : p0;
-                for (int p = p0; p < p1; p += N) {
+                uint32_t at = first_at + (uint32_t)p0 * step;
+                for (int p = p0; p < p1; p += N, at += N * step) {
                     float pm[N], pl[N];
                     f32x4_t po[N];
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
                         if (p + i >= p1) continue;
-                        const int t = t0 + (p + i) * by;
-                        const uint32_t s = place(t), stats = stats_at + (by > 1 && t < tl ? run_stats : 0);
-                        pm[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(parts, s + stats + c * 4, 0, kAgent));
+                        const uint32_t v = at + stats + c * 4, w = i * step;
+                        pm[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(parts, v, w, kAgent));
                         pl[i] = __uint_as_float(
-                            __builtin_amdgcn_raw_buffer_load_b32(parts, s + stats + (kv::kCols + c) * 4, 0, kAgent));
-                        po[i] = __builtin_bit_cast(
-                            f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(parts, s + (uint32_t)(c * D + e) * 4, 0, kAgent));
+                            __builtin_amdgcn_raw_buffer_load_b32(parts, v + kv::kCols * 4, w, kAgent));
+                        po[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                                parts, at + (uint32_t)(c * D + e) * 4, w, kAgent));
                     }
                     float mn = m;
 #pragma unroll
@@ -493,13 +571,12 @@ __global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) 
                         const float f1 = part_weight(m, mn);
                         store_out(out + (int64_t)c * D + e, o * f1, lt * f1 + part_weight(sink, mn), v_scale);
                     } else {
-                        const uint32_t s = place(t0), stats = stats_at + run_stats;
                         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), parts,
-                                                               s + (uint32_t)(c * D + e) * 4, 0, kAgent);
+                                                               first_at + (uint32_t)(c * D + e) * 4, 0, kAgent);
                         if (e == 0) {
-                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), parts, s + stats + c * 4, 0, kAgent);
-                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lt), parts,
-                                                                  s + stats + (kv::kCols + c) * 4, 0, kAgent);
+                            const uint32_t v = first_at + stats_at + kRunStats + c * 4;
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), parts, v, 0, kAgent);
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lt), parts, v + kv::kCols * 4, 0, kAgent);
                         }
                     }
                 }
@@ -555,9 +632,12 @@ __global__ void __launch_bounds__(kThreads, kv::teams_per_cu(D, Kv<D, FMT>::E)) 
 #pragma unroll
                 for (int w = 0; w < kWaves; ++w)
                     lt += wl[w * kv::kCols + tid] * part_weight(wm[w * kv::kCols + tid], m);
-                const uint32_t p = slot + (uint32_t)(kv::item_heads(g) * D + tid) * 4;
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), parts, p, 0, kAgent);
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lt), parts, p + kv::kCols * 4, 0, kAgent);
+                const uint32_t v = slot + stats_at + tid * 4;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {                    // (of the part, and of a run that is this part)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), parts, v, i * kRunStats, kAgent);
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lt), parts, v + kv::kCols * 4, i * kRunStats, kAgent);
+                }
             }
             // the run's last team adds its parts up, and the last run's team the runs' sums (a run of one is its
             // part)
@@ -584,7 +664,7 @@ hipError_t go(const AttendArgs& a, int grid, hipStream_t st) {
     const size_t list = a.direct ? 0 : ((size_t)2 * a.a.requests + 1 + 3) & ~(size_t)3;
     const size_t lds = list * 4 + 2 * kWaves * kv::kCols * 4 +
                        (waves > join ? waves : join);
-    return launch(attend_kernel<D, FMT, WIDE, kDepth>, dim3(grid), dim3(kThreads), lds, st, a);
+    return launch(attend_kernel<D, FMT, WIDE>, dim3(grid), dim3(kThreads), lds, st, a);
 }
 
 template <int D>
@@ -612,8 +692,7 @@ hipError_t launch_kv_attend(const CacheView& c, const ft_attend& q, ft_workspace
     const int64_t seen = q.window ? q.window / kv::kStep + 2 : most;
     const int64_t items = (int64_t)q.requests * c.heads * a.blocks, steps = seen < most ? seen : most;
     a.direct = steps <= kv::kDirectSteps;
-    const int teams = kv::kComputeUnits * kv::teams_per_cu(c.D, c.fmt == FT_KV_BF16 ? 2 : 1);
-    const int grid = a.direct ? (int)items : kv::grid_of(items, items * steps, teams);
+    const int grid = a.direct ? (int)items : kv::grid_of(items, items * steps);
     if (c.D == 64) return pick<64>(a, grid, st);
     if (c.D == 128) return pick<128>(a, grid, st);
     return pick<256>(a, grid, st);

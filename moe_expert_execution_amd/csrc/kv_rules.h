@@ -28,66 +28,73 @@ FT_HD constexpr int value_tokens(int D, int esize) { return 16 / (esize * value_
 
 // ---- the division of attention ----------------------------------------------------
 // A work item is one KV head of one request for up to 16 query heads; its visible
-// tokens are steps of 32.  The steps of all items in order (request, then head) are cut
-// into `teams` ranges of equal length, one workgroup each, so ragged lengths balance by
-// themselves.  An item that is cut is joined by the last of its teams to arrive, so a
-// cut that falls within `slack` steps of an item's end moves there.
+// tokens are steps of 32.  All items in order (request, then head), each as long as its
+// steps and kItemCost, are cut into `teams` ranges of equal length, one workgroup each, so
+// ragged lengths balance by themselves.  An item that is cut is joined by the last of its teams to
+// arrive, so a cut within `slack` steps of an item's end moves there.
 constexpr int kWaves = 4;                  // of a team; they share a segment's steps
-constexpr int kMaxTeams = 1024;
-constexpr int kSlack = 4;
-constexpr int kJoin = 8;                   // parts that one join takes
+constexpr int kMaxTeams = 512;             // two for each of 256 compute units: all are resident, as one that starts late ends late
+constexpr int kSlack = 8;
+constexpr int kItemCost = 6;               // what an item takes beside its steps, in steps
+constexpr int kJoin = 16;                  // parts of a run
+
+constexpr int64_t kMaxSteps = 1ll << 30;   // of a call: all lengths below are 32-bit
 
 struct Division {
-    int64_t total;                         // steps, > 0
-    int64_t per;                           // steps of a team, times 2^16
-    float rate;                            // teams per step
+    uint32_t total;                        // of the items' lengths, > 0
+    uint32_t base, part;                   // a range's length: base + part / 2^16
+    float rate;                            // ranges per length
     int teams, slack;
 };
 
-// `items` that have steps, `total` steps, at most `grid` teams: one for as many steps as it has
+FT_HD inline int item_length(int steps) { return steps ? steps + kItemCost : 0; }
+
+// `items` that have steps, `total` length, at most `grid` teams: one for as many steps as it has
 // waves, or for an item where items are shorter.
-FT_HD inline Division divide(int64_t items, int64_t total, int grid) {
-    int64_t t = (total + kWaves - 1) / kWaves;
+FT_HD inline Division divide(uint32_t items, uint32_t total, int grid) {
+    uint32_t t = (total - items * kItemCost + kWaves - 1) / kWaves;
     if (t < items) t = items;
-    if (t > grid) t = grid;
-    // (divisions in doubles: exact enough, and a fraction of a 64-bit integer division's latency)
-    const double per = (double)(total << 16) / (double)t;
-    const double half = (per * (1.0 / 65536) - 1) / 2;           // less than half a range: cuts keep their order
-    return Division{total, (int64_t)per, (float)t / (float)total, (int)t, half < kSlack ? (int)half : kSlack};
+    if (t > (uint32_t)grid) t = grid;
+    const uint32_t base = total / t, half = (base - 1) / 2;      // less than half a range: few teams stay idle
+    return Division{total, base, ((total - base * t) << 16) / t, (float)t / (float)total, (int)t,
+                    (int)(half < kSlack ? half : kSlack)};
 }
-// The cut before team i, and the last team whose cut is at or before a step, before cuts move.
-FT_HD inline int64_t cut(const Division& d, int i) { return i == d.teams ? d.total : d.per * i >> 16; }
-FT_HD inline int team_at(const Division& d, int64_t step) {
-    int i = (int)((float)step * d.rate);               // within one of it
+// The cut before team i, and the last team whose cut is at or before a place, before cuts move.
+FT_HD inline uint32_t cut(const Division& d, int i) { return i == d.teams ? d.total : d.base * i + (d.part * i >> 16); }
+FT_HD inline int team_at(const Division& d, uint32_t place) {
+    int i = (int)((float)place * d.rate);              // within one of it
     i = i < d.teams - 1 ? i : d.teams - 1;
-    while (cut(d, i) > step) --i;
-    while (i < d.teams - 1 && cut(d, i + 1) <= step) ++i;
-    return i;
+    i -= cut(d, i) > place;
+    return i + (i < d.teams - 1 && cut(d, i + 1) <= place);
 }
 
-// The teams of the item of steps [begin, begin + n): cuts in its first and last steps have moved to its
-// ends (the nearer one, the first of two as near).
+// The teams of the item of n steps at `begin`: cuts near its ends, or in its cost, have moved to them.  (A team
+// between two cuts that have moved to one place has no work.)
 struct Teams {
     int first, last;
 };
-FT_HD inline Teams teams_of(const Division& d, int64_t begin, int n) {
+FT_HD inline Teams teams_of(const Division& d, uint32_t begin, int n) {
     const int after = d.slack < n / 2 ? d.slack : n / 2, before = d.slack < (n - 1) / 2 ? d.slack : (n - 1) / 2;
-    return Teams{team_at(d, begin + after), team_at(d, begin + n - 1 - before)};
+    return Teams{team_at(d, begin + kItemCost + after), team_at(d, begin + kItemCost + n - 1 - before)};
 }
-// Steps [from, to) of the item that team i, one of them, works on, counted from the item's begin.
+// Steps [from, to) of the item that team i, one of them, works on.
 struct Segment {
     int from, to;
 };
-FT_HD inline Segment segment(const Division& d, const Teams& t, int64_t begin, int n, int i) {
-    return Segment{i == t.first ? 0 : (int)(cut(d, i) - begin), i == t.last ? n : (int)(cut(d, i + 1) - begin)};
+FT_HD inline Segment segment(const Division& d, const Teams& t, uint32_t begin, int n, int i) {
+    return Segment{i == t.first ? 0 : (int)(cut(d, i) - begin) - kItemCost,
+                   i == t.last ? n : (int)(cut(d, i + 1) - begin) - kItemCost};
 }
 
-// Parts of an item are joined in runs of kJoin teams, counted from its first, and the runs' sums then:
-// runs of more for items of more than kJoin^2 parts.
+// Where a team's part of an item lies: parts of one item side by side, and no two items' overlap, since the
+// next item that is cut begins in this one's last team or later.
+FT_HD inline int part_slot(const Teams& t, int i) { return t.first + i; }
+
+// An item of up to 2 kJoin parts is joined at once; one of more in runs of kJoin teams, counted from its first,
+// and then the runs' sums (at most kMaxTeams / kJoin).
 FT_HD inline int join_run(const Teams& t) {
-    int run = kJoin;
-    while (run * kJoin < t.last - t.first + 1) run *= 2;
-    return run;
+    const int n = t.last - t.first + 1;
+    return n <= 2 * kJoin ? n : kJoin;
 }
 
 // Query heads of an item and items of a KV head, for a group of g query heads.
@@ -98,14 +105,10 @@ FT_HD inline int head_blocks(int g) { return (g + kCols - 1) / kCols; }
 // whose sum takes its place.
 FT_HD inline int64_t part_floats(int g, int D) { return (int64_t)item_heads(g) * D + 4 * kCols; }
 
-// Workgroups of a launch whose items and steps are at most these.
-inline int grid_of(int64_t items, int64_t steps, int most) { return divide(items, steps, most).teams; }
-
-// Teams of a compute unit, as registers allow: all of a call's teams are resident, since one that starts late
-// ends late (64 requests of up to 8,192 tokens, e4m3, 128 dimensions: 73 us with three, 85 with two; bf16, 192
-// registers: 122 with the two that fit, 130 with three).
-constexpr int teams_per_cu(int D, int esize) { return D == 256 ? 2 : D == 128 ? (esize == 2 ? 2 : 3) : esize == 2 ? 3 : 4; }
-constexpr int kComputeUnits = 256;
+// Workgroups of a launch of at most so many items and steps (up to kMaxSteps).
+inline int grid_of(int64_t items, int64_t steps) {
+    return divide((uint32_t)items, (uint32_t)(steps + items * kItemCost), kMaxTeams).teams;
+}
 
 // Items of at most this many steps are not cut, so they need no division: a workgroup each.
 constexpr int kDirectSteps = 4 * kWaves;

@@ -93,9 +93,13 @@ def test_attends_refused(kw, msg):
 
 
 def test_attends_of_too_many_tokens_refused():
-    c = cache(page_tokens=256, page_stride=2 ** 20)
-    check(M.ft_kv_attend, c, attend(requests=4096, width=65536), 0, msg="2^36")
-    check(M.ft_kv_attend, c, attend(requests=4096, width=65535), 0, msg="workspace is null")
+    c = cache(page_tokens=256, kv_heads=2, page_stride=2 ** 20)
+    for requests, q_heads, width in ((4096, 32, 16385), (2048, 34, 16385), (256, 2, 65537 * 4)):
+        a = attend(requests=requests, q_heads=q_heads, width=min(width, 131072), q_stride=8192, out_stride=8192)
+        if width <= 131072:
+            check(M.ft_kv_attend, c, a, 0, msg="2^35")
+    a = attend(requests=4096, q_heads=32, width=16384, q_stride=8192, out_stride=8192)
+    check(M.ft_kv_attend, c, a, 0, msg="workspace is null")
 
 
 def test_reserved_fields_refused():

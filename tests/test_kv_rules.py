@@ -11,6 +11,7 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 SOURCE = r"""
 #include <stdio.h>
 #include <stdlib.h>
+#include <algorithm>
 #include <map>
 #include <set>
 #include <vector>
@@ -19,19 +20,18 @@ using namespace ftmoe::kv;
 #define CHECK(c) do { if (!(c)) { printf("line %d: %s\n", __LINE__, #c); return 1; } } while (0)
 
 int division(const std::vector<int>& items, int grid) {
-    std::vector<long long> first{0};
+    std::vector<uint32_t> first{0};
     long long busy = 0;
     for (int n : items) {
-        first.push_back(first.back() + n);
+        first.push_back(first.back() + item_length(n));
         busy += n > 0;
     }
-    const long long total = first.back();
+    const uint32_t total = first.back();
     const Division d = divide(busy, total, grid);
-    CHECK(d.teams >= 1 && d.teams <= grid && d.teams <= total && d.teams <= kMaxTeams);
-    CHECK(cut(d, 0) == 0 && cut(d, d.teams) == total && d.slack >= 0 && 2 * d.slack < total / d.teams + 1);
-    std::vector<int> load(d.teams, 0);
-    std::map<int, int> arrived;                       // by counter
-    std::map<int, int> expected;
+    CHECK(d.teams >= 1 && d.teams <= grid && (uint32_t)d.teams <= total && d.teams <= kMaxTeams);
+    CHECK(cut(d, 0) == 0 && cut(d, d.teams) == total && d.slack >= 0 && 2 * d.slack < (int)(total / d.teams + 1));
+    std::vector<int> load(d.teams, 0), length(d.teams, 0);
+    std::map<int, int> expected;                      // arrivals by counter
     std::set<int> slots;
     for (size_t i = 0; i < items.size(); ++i) {
         const int n = items[i];
@@ -44,18 +44,25 @@ int division(const std::vector<int>& items, int grid) {
             CHECK(s.from == next && s.to > s.from);   // every step once, in order
             next = s.to;
             load[t] += s.to - s.from;
+            length[t] += s.to - s.from + (t == who.first ? kItemCost : 0);
             if (who.first == who.last) continue;
-            CHECK(slots.insert(2 * t + (t == who.first ? 1 : 0)).second);     // no two parts in one place
-            ++arrived[who.first];
+            CHECK(part_slot(who, t) < 2 * kMaxTeams && slots.insert(part_slot(who, t)).second);
         }
         CHECK(next == n);
-        if (who.first != who.last) {
-            CHECK(!expected.count(who.first));        // a team's counter serves one item
-            expected[who.first] = who.last - who.first + 1;
+        // the join: every team arrives once at its run's counter or is its run; every run at the item's
+        const int run = join_run(who), parts = who.last - who.first + 1, runs = (parts - 1) / run + 1;
+        if (parts == 1) continue;
+        CHECK(run <= 2 * kJoin && (runs == 1 || run == kJoin) && runs <= kMaxTeams / kJoin);
+        int joined = 0;
+        for (int r0 = who.first; r0 <= who.last; r0 += run) {
+            const int n = std::min(run, who.last - r0 + 1);
+            joined += n;
+            if (runs > 1 && n > 1) CHECK(expected.emplace(r0, n).second);     // (a counter serves one run)
         }
+        CHECK(joined == parts);
+        CHECK(expected.emplace(kMaxTeams + who.first, runs > 1 ? runs : parts).second);
     }
-    CHECK(arrived == expected);
-    for (int t = 0; t < d.teams; ++t) CHECK(load[t] <= total / d.teams + 1 + 2 * d.slack);
+    for (int t = 0; t < d.teams; ++t) CHECK(length[t] <= (int)(total / d.teams) + 1 + 2 * d.slack + kItemCost);
     // how a team finds its items: from the one that its cut falls into, on while they are its own
     for (int t = 0; t < d.teams; ++t) {
         size_t i = 0;
@@ -75,7 +82,7 @@ int division(const std::vector<int>& items, int grid) {
 
 int main() {
     srand(5);
-    const int grids[] = {1, 2, 3, 7, 64, 511, 512, kMaxTeams};
+    const int grids[] = {1, 2, 3, 7, 64, 511, kMaxTeams};
     for (int g : grids)
         for (int r = 0; r < 60; ++r) {
             std::vector<int> items;
@@ -87,18 +94,18 @@ int main() {
     // equal short items are not cut
     for (int n = 1; n <= 40; ++n)
         for (int items : {1, 3, 64, 100, 500}) {
-            const Division d = divide(items, (long long)items * n, kMaxTeams);
+            const Division d = divide(items, items * item_length(n), kMaxTeams);
             for (int i = 0; i < items && n <= kWaves; ++i) {
-                const Teams who = teams_of(d, (long long)i * n, n);
+                const Teams who = teams_of(d, i * item_length(n), n);
                 CHECK(who.first == who.last);
             }
         }
-    // totals beyond 32 bits
-    for (long long total : {1ll << 31, (1ll << 38) + 12345, (1ll << 41) - 1}) {
-        const Division d = divide(total >> 20, total, kMaxTeams);
+    // the largest calls
+    for (long long total : {(1ll << 24) + 1, (1ll << 30) + 12345, (1ll << 30) + (4096ll * 1024 * kItemCost)}) {
+        const Division d = divide(1 << 20, (uint32_t)total, kMaxTeams);
         CHECK(cut(d, 0) == 0 && cut(d, d.teams) == total);
         for (int t = 0; t < d.teams; ++t) {
-            const long long b = cut(d, t), e = cut(d, t + 1);
+            const uint32_t b = cut(d, t), e = cut(d, t + 1);
             CHECK(b < e && team_at(d, b) == t && team_at(d, e - 1) == t);
         }
     }
@@ -107,9 +114,7 @@ int main() {
         for (int i = 0; i < head_blocks(g); ++i) n += g - i * kCols < kCols ? g - i * kCols : kCols;
         CHECK(n == g && item_heads(g) <= kCols);
     }
-    CHECK(grid_of(1, 1, kMaxTeams) == 1 && grid_of(4096, 1ll << 40, 700) == 700);
-    for (int D : {64, 128, 256})
-        for (int e : {1, 2}) CHECK(kComputeUnits * teams_per_cu(D, e) <= kMaxTeams);
+    CHECK(grid_of(1, 1) == 1 && grid_of(4096 * 1024, kMaxSteps) == kMaxTeams);
     printf("ok\n");
     return 0;
 }
