@@ -7,8 +7,7 @@
 // are the only points where its threads meet.  The second norm uses the fp32
 // sum; rounding it first would feed the next block the residual's bf16 error
 // twice.  Memory bounds it, or the launch where there are few rows.
-#include "kv.h"
-#include "wfmt.h"
+#include "kv_device.h"
 
 namespace ftmoe {
 namespace {
@@ -29,20 +28,14 @@ __device__ __forceinline__ float row_sum(float v, float* lds) {
     return v;
 }
 
-__device__ __forceinline__ u32x4_t load_unit(const uint16_t* p) { return *reinterpret_cast<const u32x4_t*>(p); }
-
 __device__ __forceinline__ float element(const u32x4_t u, int i) {
     return i & 1 ? bf16hi(u[i >> 1]) : bf16lo(u[i >> 1]);
 }
 
 __device__ __forceinline__ float sigmoid_of(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    return (uint32_t)f32_to_bf16_rne(lo) | (uint32_t)f32_to_bf16_rne(hi) << 16;
-}
-
 // R threads per row, U units of 8 elements per thread; workgroups of max(R, 256) threads.
-template <int R, int U>
+template <int R, int U, bool STREAM>
 __global__ void __launch_bounds__(R > 256 ? R : 256) norm_kernel(ft_norm a) {
     constexpr int kThreads = R > 256 ? R : 256;
     __shared__ float lds[2][R > 64 ? R / 64 : 1];
@@ -58,10 +51,10 @@ __global__ void __launch_bounds__(R > 256 ? R : 256) norm_kernel(ft_norm a) {
     for (int i = 0; i < U; ++i) {
         const int u = lane + i * R;
         const bool on = u < units;
-        b[i] = on && a.block ? load_unit(a.block + t * a.block_stride + u * 8) : zero;
-        r[i] = on && a.residual ? load_unit(a.residual + t * a.residual_stride + u * 8) : zero;
-        g[i] = on && kind == FT_GATE_FULL    ? load_unit(a.gate + t * a.gate_stride + u * 8)
-               : on && kind == FT_GATE_CHANNEL ? load_unit(a.gate + u * 8)
+        b[i] = on && a.block ? kv::load16<STREAM>(a.block + t * a.block_stride + u * 8) : zero;
+        r[i] = on && a.residual ? kv::load16<STREAM>(a.residual + t * a.residual_stride + u * 8) : zero;
+        g[i] = on && kind == FT_GATE_FULL    ? kv::load16<STREAM>(a.gate + t * a.gate_stride + u * 8)
+               : on && kind == FT_GATE_CHANNEL ? kv::load16<false>(a.gate + u * 8)
                                                : zero;
     }
     float token_gate = 1.0f;
@@ -84,7 +77,7 @@ __global__ void __launch_bounds__(R > 256 ? R : 256) norm_kernel(ft_norm a) {
     for (int i = 0; i < U; ++i) {
         const int u = lane + i * R;
         const bool on = u < units;
-        const u32x4_t w = on && a.post_w ? load_unit(a.post_w + u * 8) : zero;
+        const u32x4_t w = on && a.post_w ? kv::load16<false>(a.post_w + u * 8) : zero;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float v = element(b[i], e) * s1;
@@ -100,8 +93,8 @@ __global__ void __launch_bounds__(R > 256 ? R : 256) norm_kernel(ft_norm a) {
         if (on && a.sum) {
             u32x4_t o;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = pack_bf16(s[i][2 * e], s[i][2 * e + 1]);
-            *reinterpret_cast<u32x4_t*>(a.sum + t * a.sum_stride + u * 8) = o;
+            for (int e = 0; e < 4; ++e) o[e] = kv::pack_bf16(s[i][2 * e], s[i][2 * e + 1]);
+            kv::store16<STREAM>(a.sum + t * a.sum_stride + u * 8, o);
         }
     }
     if (!a.normed) return;
@@ -110,13 +103,13 @@ __global__ void __launch_bounds__(R > 256 ? R : 256) norm_kernel(ft_norm a) {
     for (int i = 0; i < U; ++i) {
         const int u = lane + i * R;
         if (u >= units) continue;
-        const u32x4_t w = load_unit(a.pre_w + u * 8);
+        const u32x4_t w = kv::load16<false>(a.pre_w + u * 8);
         u32x4_t o;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            o[e] = pack_bf16(s[i][2 * e] * s2 * (a.weight_offset + element(w, 2 * e)),
+            o[e] = kv::pack_bf16(s[i][2 * e] * s2 * (a.weight_offset + element(w, 2 * e)),
                              s[i][2 * e + 1] * s2 * (a.weight_offset + element(w, 2 * e + 1)));
-        *reinterpret_cast<u32x4_t*>(a.normed + t * a.normed_stride + u * 8) = o;
+        kv::store16<STREAM>(a.normed + t * a.normed_stride + u * 8, o);
     }
 }
 
@@ -124,7 +117,13 @@ template <int R, int U>
 hipError_t go(const ft_norm& a, hipStream_t st) {
     constexpr int kThreads = R > 256 ? R : 256;
     const int64_t rows = kThreads / R;
-    return launch(norm_kernel<R, U>, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(kThreads), 0, st, a);
+    const dim3 grid((unsigned)((a.T + rows - 1) / rows));
+    // Calls that move more than the L2s hold stream past them (4,096 rows of 7,168, a gate of every element:
+    // 56 us, 64 through them).
+    const int full = (a.block != nullptr) + (a.residual != nullptr) + ((a.gate_kind & ~FT_GATE_SIGMOID) == FT_GATE_FULL) +
+                     (a.sum != nullptr) + (a.normed != nullptr);
+    if ((int64_t)a.T * a.d * 2 * full > kv::kStreamBytes) return launch(norm_kernel<R, U, true>, grid, dim3(kThreads), 0, st, a);
+    return launch(norm_kernel<R, U, false>, grid, dim3(kThreads), 0, st, a);
 }
 
 }  // namespace
@@ -134,7 +133,8 @@ hipError_t launch_block_norm(const ft_norm& a, hipStream_t st) {
     if (units <= 16) return go<16, 1>(a, st);
     if (units <= 64) return go<64, 1>(a, st);
     if (units <= 256) return go<256, 1>(a, st);
-    if (units <= 1024) return go<256, 4>(a, st);
+    if (units <= 512) return go<256, 2>(a, st);
+    if (units <= 1024) return go<512, 2>(a, st);
     return go<1024, 4>(a, st);
 }
 

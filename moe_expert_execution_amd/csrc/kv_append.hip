@@ -1,14 +1,13 @@
 // New tokens' keys and values into their cache slots, rotated, with the rotated
 // queries (ft_kv_append).
 //
-// A wave takes 16 tokens, lane l token l % 16, and of each head the two 8-element
-// chunks that rotate together (i and i + rot / 2) of its quarter l / 16, so a
-// pair is read once and the angles' cos and sin stay in registers over the heads.  16
-// consecutive tokens of a prompt fill a block of the cache: the lanes' key units
-// are then runs of 256 bytes, value rows and source rows of 64.  Memory bounds a prompt,
+// A wave takes 8 tokens (16 where heads have 64 dimensions), lane l token l % 8, and
+// of each head the two 8-element chunks that rotate together (i and i + rot / 2) of
+// its eighth l / 8, so a pair is read once and the angles' cos and sin stay in registers
+// over the heads.  8 consecutive tokens of a prompt fill half a block of the cache:
+// the lanes' key units are then runs of 128 bytes, and so are value and source rows.  Memory bounds a prompt,
 // latency a decode step.
-#include "kv.h"
-#include "wfmt.h"
+#include "kv_device.h"
 
 namespace ftmoe {
 namespace {
@@ -23,8 +22,7 @@ struct Chunk {
     float v[8];
 };
 
-__device__ __forceinline__ Chunk load_chunk(const uint16_t* p) {
-    const u32x4_t u = *reinterpret_cast<const u32x4_t*>(p);
+__device__ __forceinline__ Chunk chunk_of(const u32x4_t u) {
     Chunk c;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -38,7 +36,7 @@ __device__ __forceinline__ u32x4_t to_bf16(const Chunk& c) {
     u32x4_t u;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        u[i] = (uint32_t)f32_to_bf16_rne(c.v[2 * i]) | (uint32_t)f32_to_bf16_rne(c.v[2 * i + 1]) << 16;
+        u[i] = kv::pack_bf16(c.v[2 * i], c.v[2 * i + 1]);
     return u;
 }
 
@@ -96,77 +94,111 @@ __device__ __forceinline__ void put(uint8_t* p, int r, int e, const Chunk& c, fl
 }
 
 constexpr int kThreads = 256;
+// Lanes of a token: its chunk pairs of a head that a wave takes, whole 128-byte lines on either side.
+constexpr int lanes_of(int D) { return D == 64 ? 4 : 8; }
+constexpr int kAhead = 2;                 // heads whose loads are under way
 
-template <int D, int FMT>
+template <int D, int FMT, bool STREAM>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     constexpr int E = FMT == FT_KV_BF16 ? 2 : 1;
-    constexpr int kGroups = D / 64;                    // groups of four chunk pairs of a head
+    constexpr int kLanes = lanes_of(D), kTokens = 64 / kLanes, kGroups = D / 16 / kLanes;
     const int lane = threadIdx.x & 63;
     const int64_t wave = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
     const int heads = a.a.q_heads + 2 * a.c.heads, parts = (heads + a.per - 1) / a.per;
     const int group = (int)(wave % kGroups), part = (int)(wave / kGroups % parts);
-    const int64_t t = wave / kGroups / parts * 16 + (lane & 15);
+    const int64_t t = wave / kGroups / parts * kTokens + lane % kTokens;
     if (t >= a.a.tokens) return;
-    const int slot = a.a.slot[t];
-    if (slot < 0 || slot >= a.c.pages << a.c.page_shift) return;
-    const int half = a.a.rot >> 1, pair = group * 4 + (lane >> 4);
+    const int half = a.a.rot >> 1, pair = group * kLanes + lane / kTokens;
     // the pair's first dimensions: rotating ones come first, the rest are neighbours
     const bool turns = pair < half >> 3;
     const int e0 = turns ? pair * 8 : pair * 16, e1 = turns ? e0 + half : e0 + 8;
-    float cs[8], sn[8];
-    if (a.a.rot) {
-        const int p = a.a.pos[t];
-        if (p < 0 || p >= a.a.positions) return;
-        if (turns) {
-            const float* row = a.a.cos_sin + (int64_t)p * a.a.rot + pair * 8;
+    const int h0 = part * a.per, h1 = min(heads, h0 + a.per);
+    u32x4_t raw[kAhead][2];
+    auto load = [&](int from) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                cs[i] = row[i];
-                sn[i] = row[half + i];
+        for (int i = 0; i < kAhead; ++i) {
+            const int h = from + i, kh = h - a.a.q_heads, vh = kh - a.c.heads;
+            if (h >= h1) continue;
+            const uint16_t* src = kh < 0   ? a.a.q + t * a.a.q_stride + h * D
+                                  : vh < 0 ? a.a.k + t * a.a.k_stride + kh * D
+                                           : a.a.v + t * a.a.v_stride + vh * D;
+            raw[i][0] = kv::load16<STREAM>(src + e0);
+            raw[i][1] = kv::load16<STREAM>(src + e1);
+        }
+    };
+    load(h0);                                          // (under way while slot and position come)
+    const int slot = a.a.slot[t], p = a.a.rot ? a.a.pos[t] : 0;
+    if (slot < 0 || slot >= a.c.pages << a.c.page_shift) return;
+    if (a.a.rot && (p < 0 || p >= a.a.positions)) return;
+    float cs[8], sn[8];
+    if (turns) {
+        const float* row = a.a.cos_sin + (int64_t)p * a.a.rot + pair * 8;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const f32x4_t c = *reinterpret_cast<const f32x4_t*>(row + i), s = *reinterpret_cast<const f32x4_t*>(row + half + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                cs[i + e] = c[e];
+                sn[i + e] = s[e];
             }
         }
     }
     const int page = slot >> a.c.page_shift, in = slot & ((1 << a.c.page_shift) - 1), r = in & 15;
     const int64_t head_bytes = (int64_t)(D * E) << a.c.page_shift;
     const int64_t place = (int64_t)page * a.c.page_stride + (in >> 4) * (16 * D * E);
-    const int h1 = min(heads, (part + 1) * a.per);
-    for (int h = part * a.per; h < h1; ++h) {
-        const int kh = h - a.a.q_heads, vh = kh - a.c.heads;
-        const uint16_t* src = kh < 0   ? a.a.q + t * a.a.q_stride + h * D
-                              : vh < 0 ? a.a.k + t * a.a.k_stride + kh * D
-                                       : a.a.v + t * a.a.v_stride + vh * D;
-        Chunk x = load_chunk(src + e0), y = load_chunk(src + e1);
-        if (turns && vh < 0) {
+    for (int from = h0; from < h1; from += kAhead) {
+        Chunk x[kAhead], y[kAhead];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = x.v[i], w = y.v[i];
-                x.v[i] = u * cs[i] - w * sn[i];
-                y.v[i] = w * cs[i] + u * sn[i];
-            }
+        for (int i = 0; i < kAhead; ++i) {
+            x[i] = chunk_of(raw[i][0]);
+            y[i] = chunk_of(raw[i][1]);
         }
-        if (kh < 0) {
-            uint16_t* to = a.a.q_out + t * a.a.q_out_stride + h * D;
-            *reinterpret_cast<u32x4_t*>(to + e0) = to_bf16(x);
-            *reinterpret_cast<u32x4_t*>(to + e1) = to_bf16(y);
-        } else if (vh < 0) {
-            const float scale = FMT == FT_KV_E4M3 ? a.c.k_scale[kh] : 1.0f;
-            uint8_t* to = a.c.k + place + kh * head_bytes;
-            put<D, FMT, true>(to, r, e0, x, scale);
-            put<D, FMT, true>(to, r, e1, y, scale);
-        } else {
-            const float scale = FMT == FT_KV_E4M3 ? a.c.v_scale[vh] : 1.0f;
-            uint8_t* to = a.c.v + place + vh * head_bytes;
-            put<D, FMT, false>(to, r, e0, x, scale);
-            put<D, FMT, false>(to, r, e1, y, scale);
+        if (from + kAhead < h1) load(from + kAhead);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int h = from + i, kh = h - a.a.q_heads, vh = kh - a.c.heads;
+            if (h >= h1) continue;
+            if (turns && vh < 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float u = x[i].v[j], w = y[i].v[j];
+                    x[i].v[j] = u * cs[j] - w * sn[j];
+                    y[i].v[j] = w * cs[j] + u * sn[j];
+                }
+            }
+            if (kh < 0) {
+                uint16_t* to = a.a.q_out + t * a.a.q_out_stride + h * D;
+                kv::store16<STREAM>(to + e0, to_bf16(x[i]));
+                kv::store16<STREAM>(to + e1, to_bf16(y[i]));
+            } else if (vh < 0) {
+                const float scale = FMT == FT_KV_E4M3 ? a.c.k_scale[kh] : 1.0f;
+                uint8_t* to = a.c.k + place + kh * head_bytes;
+                put<D, FMT, true>(to, r, e0, x[i], scale);
+                put<D, FMT, true>(to, r, e1, y[i], scale);
+            } else {
+                const float scale = FMT == FT_KV_E4M3 ? a.c.v_scale[vh] : 1.0f;
+                uint8_t* to = a.c.v + place + vh * head_bytes;
+                put<D, FMT, false>(to, r, e0, x[i], scale);
+                put<D, FMT, false>(to, r, e1, y[i], scale);
+            }
         }
     }
 }
 
-template <int D>
+template <int D, bool STREAM>
 hipError_t go(const AppendArgs& a, int64_t waves, hipStream_t st) {
     const dim3 grid((unsigned)((waves + kThreads / 64 - 1) / (kThreads / 64))), block(kThreads);
-    if (a.c.fmt == FT_KV_BF16) return launch(append_kernel<D, FT_KV_BF16>, grid, block, 0, st, a);
-    return launch(append_kernel<D, FT_KV_E4M3>, grid, block, 0, st, a);
+    if (a.c.fmt == FT_KV_BF16) return launch(append_kernel<D, FT_KV_BF16, STREAM>, grid, block, 0, st, a);
+    return launch(append_kernel<D, FT_KV_E4M3, STREAM>, grid, block, 0, st, a);
+}
+
+// Rows of more than the L2s hold stream past them (8,192 tokens, 40 heads and 8 of values: 42 us, 50 through
+// them; 777 tokens of 20 heads of 256: 6.7, 6.3 through them), the cache's stay: the attention that follows
+// reads them.
+template <int D>
+hipError_t pick(const AppendArgs& a, int64_t waves, hipStream_t st) {
+    const int64_t moved = (int64_t)a.a.tokens * (2 * a.a.q_heads + 2 * a.c.heads) * D * 2;
+    return moved > kv::kStreamBytes ? go<D, true>(a, waves, st) : go<D, false>(a, waves, st);
 }
 
 }  // namespace
@@ -175,14 +207,14 @@ hipError_t launch_kv_append(const CacheView& c, const ft_append& a, hipStream_t 
     AppendArgs k;
     k.c = c;
     k.a = a;
-    const int heads = a.q_heads + 2 * c.heads, groups = c.D / 64;
-    const int64_t blocks = (a.tokens + 15) / 16;
+    const int heads = a.q_heads + 2 * c.heads, lanes = lanes_of(c.D), groups = c.D / 16 / lanes;
+    const int64_t blocks = (a.tokens + 64 / lanes - 1) / (64 / lanes);
     k.per = 1;
-    while (k.per < 8 && blocks * groups * ((heads + 2 * k.per - 1) / (2 * k.per)) >= 4096) k.per *= 2;
+    while (k.per < 4 && blocks * groups * ((heads + 2 * k.per - 1) / (2 * k.per)) >= 4096) k.per *= 2;
     const int64_t waves = blocks * groups * ((heads + k.per - 1) / k.per);
-    if (c.D == 64) return go<64>(k, waves, st);
-    if (c.D == 128) return go<128>(k, waves, st);
-    return go<256>(k, waves, st);
+    if (c.D == 64) return pick<64>(k, waves, st);
+    if (c.D == 128) return pick<128>(k, waves, st);
+    return pick<256>(k, waves, st);
 }
 
 }  // namespace ftmoe

@@ -18,7 +18,7 @@
 //
 // Statistics are fp32, one running maximum and sum per column and wave, in base 2.  The
 // work is divided as kv_rules.h says; memory bounds long contexts, latency short ones.
-#include "kv.h"
+#include "kv_device.h"
 #include "resident.h"
 
 namespace ftmoe {
@@ -272,8 +272,7 @@ __device__ __forceinline__ void store_out(uint16_t* to, const f32x4_t o, float l
     float x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = l == 0.0f ? 0.0f : o[i] * f;
-    *reinterpret_cast<u32x2_t*>(to) = u32x2_t{(uint32_t)f32_to_bf16_rne(x[0]) | (uint32_t)f32_to_bf16_rne(x[1]) << 16,
-                                              (uint32_t)f32_to_bf16_rne(x[2]) | (uint32_t)f32_to_bf16_rne(x[3]) << 16};
+    *reinterpret_cast<u32x2_t*>(to) = u32x2_t{kv::pack_bf16(x[0], x[1]), kv::pack_bf16(x[2], x[3])};
 }
 
 template <int D, int FMT, bool WIDE>
@@ -307,13 +306,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(AttendArgs a) {
     for (int b0 = 0; b0 < B && !a.direct; b0 += kThreads) {
         const int b = b0 + tid;
         const int hi = b < B ? end_of(b) : 0, own = kv::item_length(steps_of(hi));
-        int x = own;
+        const int x = kv::wave_scan(own);
         const int some = __popcll(__ballot(own > 0));
-#pragma unroll
-        for (int m = 1; m < 64; m *= 2) {
-            const int y = __shfl_up(x, m);
-            if (lane >= m) x += y;
-        }
         __syncthreads();
         if (lane == 63) {
             scan[0][wave] = x;

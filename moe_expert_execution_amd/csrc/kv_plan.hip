@@ -7,37 +7,48 @@
 // workgroup computes the sums for itself (some 4096 lengths, L2-resident) and
 // takes a share of the rows; the one that arrives last writes what may alias an
 // input (kv_len, counts), when nobody reads those any more.  Latency bounds it.
-#include "kv.h"
+#include "kv_device.h"
 #include "resident.h"
 
 namespace ftmoe {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kPer = kv::kMaxRequests / kThreads;      // requests of a thread
-constexpr int kRowsPerGroup = 4096;                    // token rows or page moves of a workgroup
+constexpr int kPer = 4;                                // requests of a thread
+constexpr int kThreads = kv::kMaxRequests / kPer;
+constexpr int kFew = 64;                               // threads of a call of few requests and rows: one wave
 
-// Exclusive prefix sums over the workgroup of each thread's own sum.
-__device__ __forceinline__ int block_scan(int v, int* lds, int* total) {
+// N exclusive prefix sums over the workgroup, of each thread's own sums v; total: the workgroup's.
+template <int THREADS, int N>
+__device__ __forceinline__ void block_scan(int (&v)[N], int (&total)[N], int (*lds)[THREADS / 64]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int x = v;
+    int x[N];
 #pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-        const int y = __shfl_up(x, m);
-        if (lane >= m) x += y;
+    for (int i = 0; i < N; ++i) {
+        x[i] = kv::wave_scan(v[i]);
+        if constexpr (THREADS == 64) {
+            total[i] = __builtin_amdgcn_readlane(x[i], 63);
+            v[i] = x[i] - v[i];
+        }
     }
-    __syncthreads();                                   // (lds may still be read from the scan before)
-    if (lane == 63) lds[wave] = x;
-    __syncthreads();
-    int before = 0, all = 0;
+    if constexpr (THREADS > 64) {
+        __syncthreads();                               // (lds may still be read from the scan before)
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) {
-        const int s = lds[w];
-        if (w < wave) before += s;
-        all += s;
+        for (int i = 0; i < N; ++i)
+            if (lane == 63) lds[i][wave] = x[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            int before = 0, all = 0;
+#pragma unroll
+            for (int w = 0; w < THREADS / 64; ++w) {
+                const int s = lds[i][w];
+                if (w < wave) before += s;
+                all += s;
+            }
+            total[i] = all;
+            v[i] = before + x[i] - v[i];
+        }
     }
-    *total = all;
-    return before + x - v;
 }
 
 // Last index i of the non-decreasing p[0..n-1] with p[i] <= v (p[0] <= v).
@@ -55,15 +66,18 @@ struct PlanArgs {
     ft_kv_batch b;
     uint32_t* counter;
     int page_shift;
+    bool shared;                                       // kv_len or counts lies over an input
 };
 
-__global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a) {
     const ft_kv_batch& c = a.b;
-    __shared__ int first[kv::kMaxRequests + 1];        // token row of each request
-    __shared__ int lack[kv::kMaxRequests + 1];         // pages lacked before it
-    __shared__ int back[kv::kMaxRequests + 1];         // pages returned before it
-    __shared__ uint8_t served[kv::kMaxRequests];
-    __shared__ int scan_lds[kThreads / 64];
+    constexpr int kMost = THREADS * kPer;
+    __shared__ int first[kMost + 1];                   // token row of each request
+    __shared__ int lack[kMost + 1];                    // pages lacked before it
+    __shared__ int back[kMost + 1];                    // pages returned before it
+    __shared__ uint8_t served[kMost];
+    __shared__ int scan_lds[3][THREADS / 64];
     __shared__ uint32_t flag;
     const int B = c.requests, tid = threadIdx.x, P = 1 << a.page_shift, room = c.width << a.page_shift;
     const int b0 = tid * kPer;
@@ -71,17 +85,17 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
     auto pages_of = [&](int n) { return (n + P - 1) >> a.page_shift; };
     const int free_in = *c.free_count, F = free_in < 0 ? 0 : free_in > c.pages ? c.pages : free_in;
 
-    int ctx[kPer], n[kPer], sum = 0;
+    int ctx[kPer], n[kPer], sum[1] = {0}, all[1];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const bool on = b0 + i < B;
         ctx[i] = on ? context(b0 + i) : 0;
         n[i] = on ? c.add[b0 + i] : 0;
         n[i] = n[i] > c.tokens ? c.tokens + 1 : n[i];  // (one more than fits: the sums stay within 32 bits)
-        sum += n[i] > 0 ? n[i] : 0;
+        sum[0] += n[i] > 0 ? n[i] : 0;
     }
-    int all, at = block_scan(sum, scan_lds, &all);
-    int want[kPer], returned[kPer], wants = 0, returns = 0;
+    block_scan<THREADS>(sum, all, scan_lds);
+    int at = sum[0], want[kPer], returned[kPer], pages[2] = {0, 0}, pages_all[2];     // lacked and returned
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int m = n[i] > 0 ? n[i] : 0;
@@ -89,14 +103,14 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
         const int have = pages_of(ctx[i]);
         want[i] = !fits || n[i] < 0 ? -1 : pages_of(ctx[i] + m) - have;     // -1: not to be served
         returned[i] = n[i] < 0 ? have : 0;
-        wants += want[i] > 0 ? want[i] : 0;
-        returns += returned[i];
+        pages[0] += want[i] > 0 ? want[i] : 0;
+        pages[1] += returned[i];
         if (b0 + i <= B) first[b0 + i] = c.row_tokens ? (b0 + i) * c.row_tokens : at < c.tokens ? at : c.tokens;
         at += m;
     }
-    int R, unused;
-    int w = block_scan(wants, scan_lds, &unused), r = block_scan(returns, scan_lds, &R);
-    int taken = 0, placed = 0, refused = 0;
+    block_scan<THREADS>(pages, pages_all, scan_lds);
+    const int R = pages_all[1];
+    int w = pages[0], r = pages[1], count[3] = {0, 0, 0}, total[3];    // pages taken, tokens served, requests refused
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         if (b0 + i <= B) {
@@ -106,22 +120,19 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
         if (b0 + i < B) {
             const bool ok = want[i] == 0 || (want[i] > 0 && w + want[i] <= F + R);
             served[b0 + i] = ok;
-            taken += ok ? want[i] : 0;
-            placed += ok ? n[i] : 0;
-            refused += !ok && n[i] > 0;
+            count[0] += ok ? want[i] : 0;
+            count[1] += ok ? n[i] : 0;
+            count[2] += !ok && n[i] > 0;
         }
         w += want[i] > 0 ? want[i] : 0;
         r += returned[i];
     }
-    if (B == kv::kMaxRequests && tid == kThreads - 1) {
+    if (B == kMost && tid == THREADS - 1) {
         first[B] = c.row_tokens ? B * c.row_tokens : at < c.tokens ? at : c.tokens;
         lack[B] = w;
         back[B] = r;
     }
-    int total_taken, total_placed, total_refused;
-    block_scan(taken, scan_lds, &total_taken);
-    block_scan(placed, scan_lds, &total_placed);
-    block_scan(refused, scan_lds, &total_refused);
+    block_scan<THREADS>(count, total, scan_lds);
     __syncthreads();
 
     // entry i of the stack; i < F + R
@@ -130,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
         return c.table[(int64_t)b * c.width + (i - back[b])];
     };
     auto stack = [&](int i) { return i < F ? c.free_pages[i] : returned_page(i - F); };
-    const int top = F + R - 1, stride = gridDim.x * kThreads, self = blockIdx.x * kThreads + tid;
+    const int top = F + R - 1, stride = gridDim.x * THREADS, self = blockIdx.x * THREADS + tid;
 
     for (int t = self; t < c.tokens; t += stride) {
         int b = c.row_tokens ? t / c.row_tokens : t < first[B] ? last_at_most(first, B + 1, t) : B;
@@ -147,27 +158,28 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
         c.pos[t] = pos;
         c.slot[t] = slot;
     }
-    for (int i = self; i < total_taken; i += stride) {
+    for (int i = self; i < total[0]; i += stride) {
         const int b = last_at_most(lack, B, i);
         c.table[(int64_t)b * c.width + pages_of(context(b)) + (i - lack[b])] = stack(top - i);
     }
     // returned pages that nobody took: the free list grows (never past its `pages` entries, whatever a
     // table that names pages twice returns)
-    const int left = min(F + R - total_taken, c.pages);
+    const int left = min(F + R - total[0], c.pages);
     for (int i = F + self; i < left; i += stride) c.free_pages[i] = returned_page(i - F);
 
-    if (gridDim.x > 1 && !rs::last_arrival(a.counter, gridDim.x, &flag)) return;
+    // What may lie over an input is written when nobody reads those any more: by the last workgroup to arrive.
+    if (gridDim.x > 1 && (a.shared ? !rs::last_arrival(a.counter, gridDim.x, &flag) : blockIdx.x != 0)) return;
     __syncthreads();
-    for (int b = tid; b < B; b += kThreads) {
+    for (int b = tid; b < B; b += THREADS) {
         const int cb = context(b), m = c.add[b];
         c.kv_len[b] = m < 0 ? 0 : served[b] ? cb + m : cb;
     }
-    for (int b = tid; b <= B; b += kThreads) c.start[b] = first[b];
+    for (int b = tid; b <= B; b += THREADS) c.start[b] = first[b];
     if (tid == 0) {
-        c.counts[0] = total_placed;
-        c.counts[1] = total_taken;
+        c.counts[0] = total[1];
+        c.counts[1] = total[0];
         c.counts[2] = left;
-        c.counts[3] = total_refused;
+        c.counts[3] = total[2];
     }
 }
 
@@ -178,8 +190,14 @@ hipError_t launch_kv_plan(const ft_kv_batch& b, ft_workspace* ws, hipStream_t st
     a.b = b;
     a.counter = reinterpret_cast<uint32_t*>(ws->mem);
     a.page_shift = __builtin_ctz(b.page_tokens);
-    const int groups = (b.tokens + b.requests + kRowsPerGroup - 1) / kRowsPerGroup;
-    return launch(plan_kernel, dim3(groups), dim3(kThreads), 0, st, a);
+    auto over = [](const int32_t* p, int64_t n, const int32_t* q, int64_t m) { return p < q + m && q < p + n; };
+    a.shared = false;
+    for (const int32_t* in : {b.context, b.add})
+        a.shared |= over(b.kv_len, b.requests, in, b.requests) || over(b.counts, 4, in, b.requests);
+    a.shared |= over(b.kv_len, b.requests, b.free_count, 1) || over(b.counts, 4, b.free_count, 1);
+    const int rows = b.tokens + b.requests;
+    if (b.requests <= kFew * kPer && rows <= 4 * kFew) return launch(plan_kernel<kFew>, dim3(1), dim3(kFew), 0, st, a);
+    return launch(plan_kernel<kThreads>, dim3((rows + kThreads - 1) / kThreads), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace ftmoe

@@ -111,7 +111,7 @@ inline int grid_of(int64_t items, int64_t steps) {
 }
 
 // Items of at most this many steps are not cut, so they need no division: a workgroup each.
-constexpr int kDirectSteps = 4 * kWaves;
+constexpr int kDirectSteps = 8 * kWaves;
 
 }  // namespace kv
 }  // namespace ftmoe
