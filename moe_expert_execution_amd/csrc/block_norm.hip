@@ -34,10 +34,13 @@ __device__ __forceinline__ float element(const u32x4_t u, int i) {
 
 __device__ __forceinline__ float sigmoid_of(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
-// R threads per row, U units of 8 elements per thread; workgroups of max(R, 256) threads.
+// R threads per row, U units of 8 elements per thread; a workgroup is one row, or 256 threads where rows are
+// a wave's or smaller.
+constexpr int threads_of(int R) { return R > 64 ? R : 256; }
+
 template <int R, int U, bool STREAM>
-__global__ void __launch_bounds__(R > 256 ? R : 256) norm_kernel(ft_norm a) {
-    constexpr int kThreads = R > 256 ? R : 256;
+__global__ void __launch_bounds__(threads_of(R)) norm_kernel(ft_norm a) {
+    constexpr int kThreads = threads_of(R);
     __shared__ float lds[2][R > 64 ? R / 64 : 1];
     const int64_t t = (int64_t)blockIdx.x * (kThreads / R) + threadIdx.x / R;
     const int lane = threadIdx.x % R, units = a.d >> 3;
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(R > 256 ? R : 256) norm_kernel(ft_norm a) {
 
 template <int R, int U>
 hipError_t go(const ft_norm& a, hipStream_t st) {
-    constexpr int kThreads = R > 256 ? R : 256;
+    constexpr int kThreads = threads_of(R);
     const int64_t rows = kThreads / R;
     const dim3 grid((unsigned)((a.T + rows - 1) / rows));
     // Calls that move more than the L2s hold stream past them (4,096 rows of 7,168, a gate of every element:
@@ -128,13 +131,25 @@ hipError_t go(const ft_norm& a, hipStream_t st) {
 
 }  // namespace
 
+// Many rows: few threads a row, two units each, so that a compute unit has several rows under way between
+// their sums.  Few rows: a thread a unit (64 rows of 4,096: 4.6 us, 6.0 in the other form; 4,096 of 7,168: 55 us in
+// the other, 65 so).
+constexpr int kFewRows = 1024;
+
 hipError_t launch_block_norm(const ft_norm& a, hipStream_t st) {
     const int units = a.d >> 3;
+    if (units <= 8) return go<8, 1>(a, st);
     if (units <= 16) return go<16, 1>(a, st);
     if (units <= 64) return go<64, 1>(a, st);
-    if (units <= 256) return go<256, 1>(a, st);
-    if (units <= 512) return go<256, 2>(a, st);
-    if (units <= 1024) return go<512, 2>(a, st);
+    if (a.T <= kFewRows) {
+        if (units <= 256) return go<256, 1>(a, st);
+        if (units <= 512) return go<512, 1>(a, st);
+        if (units <= 1024) return go<1024, 1>(a, st);
+    } else {
+        if (units <= 256) return go<128, 2>(a, st);
+        if (units <= 512) return go<256, 2>(a, st);
+        if (units <= 1024) return go<512, 2>(a, st);
+    }
     return go<1024, 4>(a, st);
 }
 

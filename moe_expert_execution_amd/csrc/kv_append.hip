@@ -98,7 +98,7 @@ constexpr int kThreads = 256;
 constexpr int lanes_of(int D) { return D == 64 ? 4 : 8; }
 constexpr int kAhead = 2;                 // heads whose loads are under way
 
-template <int D, int FMT, bool STREAM>
+template <int D, int FMT, int STREAM>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     constexpr int E = FMT == FT_KV_BF16 ? 2 : 1;
     constexpr int kLanes = lanes_of(D), kTokens = 64 / kLanes, kGroups = D / 16 / kLanes;
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
             const uint16_t* src = kh < 0   ? a.a.q + t * a.a.q_stride + h * D
                                   : vh < 0 ? a.a.k + t * a.a.k_stride + kh * D
                                            : a.a.v + t * a.a.v_stride + vh * D;
-            raw[i][0] = kv::load16<STREAM>(src + e0);
-            raw[i][1] = kv::load16<STREAM>(src + e1);
+            raw[i][0] = kv::load16<(STREAM > 1)>(src + e0);
+            raw[i][1] = kv::load16<(STREAM > 1)>(src + e1);
         }
     };
     load(h0);                                          // (under way while slot and position come)
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
             }
             if (kh < 0) {
                 uint16_t* to = a.a.q_out + t * a.a.q_out_stride + h * D;
-                kv::store16<STREAM>(to + e0, to_bf16(x[i]));
-                kv::store16<STREAM>(to + e1, to_bf16(y[i]));
+                kv::store16<(STREAM > 0)>(to + e0, to_bf16(x[i]));
+                kv::store16<(STREAM > 0)>(to + e1, to_bf16(y[i]));
             } else if (vh < 0) {
                 const float scale = FMT == FT_KV_E4M3 ? a.c.k_scale[kh] : 1.0f;
                 uint8_t* to = a.c.k + place + kh * head_bytes;
@@ -185,20 +185,23 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     }
 }
 
-template <int D, bool STREAM>
+template <int D, int STREAM>
 hipError_t go(const AppendArgs& a, int64_t waves, hipStream_t st) {
     const dim3 grid((unsigned)((waves + kThreads / 64 - 1) / (kThreads / 64))), block(kThreads);
     if (a.c.fmt == FT_KV_BF16) return launch(append_kernel<D, FT_KV_BF16, STREAM>, grid, block, 0, st, a);
     return launch(append_kernel<D, FT_KV_E4M3, STREAM>, grid, block, 0, st, a);
 }
 
-// Rows of more than the L2s hold stream past them (8,192 tokens, 40 heads and 8 of values: 42 us, 50 through
-// them; 777 tokens of 20 heads of 256: 6.7, 6.3 through them), the cache's stay: the attention that follows
-// reads them.
+// Where the rows are more than the L2s hold, queries are written past them, and the rows are read past them if a
+// wave's loads take whole lines, that is where heads of 128 or more rotate whole (elsewhere two loads share a
+// line): 8,192 tokens of 40 heads and 8 of values 42 us, 50 through the L2s; of 72 heads of 64 and 8 of values 43
+// with cached loads, 49 without.  The cache's lines stay: the attention that follows reads them.
 template <int D>
 hipError_t pick(const AppendArgs& a, int64_t waves, hipStream_t st) {
     const int64_t moved = (int64_t)a.a.tokens * (2 * a.a.q_heads + 2 * a.c.heads) * D * 2;
-    return moved > kv::kStreamBytes ? go<D, true>(a, waves, st) : go<D, false>(a, waves, st);
+    if (moved <= kv::kStreamBytes) return go<D, 0>(a, waves, st);
+    if (D == 64 || a.a.rot < D) return go<D, 1>(a, waves, st);
+    return go<D, 2>(a, waves, st);
 }
 
 }  // namespace
