@@ -32,7 +32,6 @@ struct AttendArgs {
     CacheView c;
     ft_attend a;
     int g, blocks;            // query heads per KV head, items per KV head
-    bool direct;              // a workgroup is an item
     float* part;              // partial results: two per team
     uint32_t part_bytes;
     uint32_t* counters;       // one per team for its run, one for its item
@@ -275,8 +274,11 @@ __device__ __forceinline__ void store_out(uint16_t* to, const f32x4_t o, float l
     *reinterpret_cast<u32x2_t*>(to) = u32x2_t{kv::pack_bf16(x[0], x[1]), kv::pack_bf16(x[2], x[3])};
 }
 
-template <int D, int FMT, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 2) attend_kernel(AttendArgs a) {
+// Waves of a SIMD whose registers the kernel fits: teams are two to a compute unit, whole items as many as can be.
+constexpr int waves_of(int D, int fmt, bool direct) { return direct && (D < 256 || fmt == FT_KV_E4M3) ? 3 : 2; }
+
+template <int D, int FMT, bool WIDE, bool DIRECT>
+__global__ void __launch_bounds__(kThreads, waves_of(D, FMT, DIRECT)) attend_kernel(AttendArgs a) {
     using T = Kv<D, FMT>;
     constexpr int kUnit = WIDE ? 4 : T::cv, kHalves = T::cv / kUnit;  // dimensions of a value unit that a round takes
     constexpr int kChunk = 16 * kUnit, kRow = kChunk + 4;        // dimensions of a round; padded in LDS
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(AttendArgs a) {
     const int B = a.a.requests, tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     int* pre = lds;                                              // [B + 1] length of an item of each request before
     int* lens = pre + B + 1;                                     // [B] visible lengths' ends
-    float* wm = reinterpret_cast<float*>(lds + (a.direct ? 0 : (2 * B + 1 + 3) & ~3));   // [kWaves][16]
+    float* wm = reinterpret_cast<float*>(lds + (DIRECT ? 0 : (2 * B + 1 + 3) & ~3));   // [kWaves][16]
     float* wl = wm + kWaves * kv::kCols;
     float* wo = wl + kWaves * kv::kCols;                         // [kWaves][heads][kRow]
     __shared__ uint32_t flag;
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(AttendArgs a) {
     const int g = a.g, heads_all = a.c.heads * a.blocks;
     // the lengths of the requests' items, summed in slices of the workgroup's width, and how many have any
     int carry = 0, busy = 0;
-    for (int b0 = 0; b0 < B && !a.direct; b0 += kThreads) {
+    for (int b0 = 0; b0 < B && !DIRECT; b0 += kThreads) {
         const int b = b0 + tid;
         const int hi = b < B ? end_of(b) : 0, own = kv::item_length(steps_of(hi));
         const int x = kv::wave_scan(own);
@@ -328,9 +330,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(AttendArgs a) {
         }
     }
     kv::Division div = {};
-    const int self = a.direct ? 0 : blockIdx.x;
+    const int self = DIRECT ? 0 : blockIdx.x;
     int b = 0, item;
-    if (a.direct) {
+    if constexpr (DIRECT) {
         b = blockIdx.x / heads_all;
         item = blockIdx.x % heads_all;
     } else {
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(AttendArgs a) {
     for (;; ++item) {
         int hi, nb, first = 0, n;                                // the request's length, the item's steps, this segment's
         kv::Teams who = {0, 0};
-        if (a.direct) {
+        if constexpr (DIRECT) {
             hi = uniform(end_of(b));
             n = nb = steps_of(hi);
         } else {
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(AttendArgs a) {
         const int waves = min(n, kWaves);                        // those that had steps
 
         const int tf = who.first, tl = who.last;
-        const bool whole = tf == tl;
+        const bool whole = DIRECT || tf == tl;
         const uint32_t slot = kv::part_slot(who, self) * part_stride, stats_at = (uint32_t)(kv::item_heads(g) * D) * 4;
         uint16_t* out = a.a.out + b * a.a.out_stride + (int64_t)q0 * D;
 
@@ -617,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(AttendArgs a) {
                 }
             }
         }
-        if (!whole) {
+        if (!DIRECT && !whole) {
             // statistics behind the sums: maxima, then totals
             if (tid < kv::kCols) {
                 float m = -INFINITY, lt = 0.0f;
@@ -645,28 +647,36 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(AttendArgs a) {
             if (go_on && last_arrival(a.counters + kv::kMaxTeams + tf, (uint32_t)(runs > 1 ? runs : rn), &flag))
                 join(tf, runs > 1 ? runs : rn, runs > 1 ? run : 1, true);
         }
-        if (a.direct) return;
+        if constexpr (DIRECT) return;
         __syncthreads();                                         // the next segment writes wm, wl and wo
     }
 }
 
-template <int D, int FMT, bool WIDE>
-hipError_t go(const AttendArgs& a, int grid, hipStream_t st) {
+template <int D, int FMT, bool WIDE, bool DIRECT>
+hipError_t start(const AttendArgs& a, int grid, hipStream_t st) {
     // (the join's shares take 6 floats a thread)
     const size_t row = 16 * (WIDE ? 4 : Kv<D, FMT>::cv) + 4;
     const size_t waves = (size_t)kWaves * kv::item_heads(a.g) * row * 4, join = kThreads * 6 * 4;
-    const size_t list = a.direct ? 0 : ((size_t)2 * a.a.requests + 1 + 3) & ~(size_t)3;
+    const size_t list = DIRECT ? 0 : ((size_t)2 * a.a.requests + 1 + 3) & ~(size_t)3;
     const size_t lds = list * 4 + 2 * kWaves * kv::kCols * 4 +
                        (waves > join ? waves : join);
-    return launch(attend_kernel<D, FMT, WIDE>, dim3(grid), dim3(kThreads), lds, st, a);
+    return launch(attend_kernel<D, FMT, WIDE, DIRECT>, dim3(grid), dim3(kThreads), lds, st, a);
+}
+
+// `steps`: the most that an item can have.
+template <int D, int FMT, bool WIDE>
+hipError_t go(const AttendArgs& a, int64_t steps, hipStream_t st) {
+    const int64_t items = (int64_t)a.a.requests * a.c.heads * a.blocks;
+    if (steps <= kv::kDirectSteps) return start<D, FMT, WIDE, true>(a, (int)items, st);
+    return start<D, FMT, WIDE, false>(a, kv::grid_of(items, items * steps), st);
 }
 
 template <int D>
-hipError_t pick(const AttendArgs& a, int grid, hipStream_t st) {
+hipError_t pick(const AttendArgs& a, int64_t steps, hipStream_t st) {
     const bool wide = a.g > kv::kCols / 2;
     if (a.c.fmt == FT_KV_BF16)
-        return wide ? go<D, FT_KV_BF16, true>(a, grid, st) : go<D, FT_KV_BF16, false>(a, grid, st);
-    return wide ? go<D, FT_KV_E4M3, true>(a, grid, st) : go<D, FT_KV_E4M3, false>(a, grid, st);
+        return wide ? go<D, FT_KV_BF16, true>(a, steps, st) : go<D, FT_KV_BF16, false>(a, steps, st);
+    return wide ? go<D, FT_KV_E4M3, true>(a, steps, st) : go<D, FT_KV_E4M3, false>(a, steps, st);
 }
 
 }  // namespace
@@ -684,12 +694,10 @@ hipError_t launch_kv_attend(const CacheView& c, const ft_attend& q, ft_workspace
     a.counters = reinterpret_cast<uint32_t*>(ws->mem);
     const int64_t most = (((int64_t)q.width << c.page_shift) + kv::kStep - 1) / kv::kStep + (q.window ? 1 : 0);
     const int64_t seen = q.window ? q.window / kv::kStep + 2 : most;
-    const int64_t items = (int64_t)q.requests * c.heads * a.blocks, steps = seen < most ? seen : most;
-    a.direct = steps <= kv::kDirectSteps;
-    const int grid = a.direct ? (int)items : kv::grid_of(items, items * steps);
-    if (c.D == 64) return pick<64>(a, grid, st);
-    if (c.D == 128) return pick<128>(a, grid, st);
-    return pick<256>(a, grid, st);
+    const int64_t steps = seen < most ? seen : most;
+    if (c.D == 64) return pick<64>(a, steps, st);
+    if (c.D == 128) return pick<128>(a, steps, st);
+    return pick<256>(a, steps, st);
 }
 
 }  // namespace ftmoe

@@ -35,8 +35,8 @@ FT_HD constexpr int value_tokens(int D, int esize) { return 16 / (esize * value_
 constexpr int kWaves = 4;                  // of a team; they share a segment's steps
 constexpr int kMaxTeams = 512;             // two for each of 256 compute units: all are resident, as one that starts late ends late
 constexpr int kSlack = 8;
-constexpr int kItemCost = 6;               // what an item takes beside its steps, in steps
-constexpr int kJoin = 16;                  // parts of a run
+constexpr int kItemCost = 8;               // what an item takes beside its steps, in steps
+constexpr int kJoin = 8;                  // parts of a run
 
 constexpr int64_t kMaxSteps = 1ll << 30;   // of a call: all lengths below are 32-bit
 
