@@ -167,3 +167,21 @@ def test_captured_and_on_another_stream():
         M.ft_block_norm(a, other.cuda_stream)
         torch.cuda.synchronize()
         assert torch.equal(n.sum, want[0]) and torch.equal(n.normed, want[1])
+
+
+@pytest.mark.parametrize("T,d,kind", [(70000, 64, "token"), (40000, 128, "full"), (9000, 512, "none"), (3000, 2048, "full"),
+                                      (1025, 4096, "channel"), (1500, 7168, "none"), (700, 16384, "full")])
+def test_calls_that_stream(T, d, kind):
+    """More than the L2s hold, in every division of a row over threads; in place too."""
+    cuda()
+    n = Norm(T, d, kind=kind, seed=12)
+    n.check()
+    if T <= 3000:
+        Norm(T, d, kind=kind, seed=13).check(("residual", "block"))
+
+
+@pytest.mark.parametrize("T", [1023, 1024, 1025])
+@pytest.mark.parametrize("d", [520, 2048, 2304, 4104, 8192])
+def test_few_and_many_rows(T, d):
+    cuda()
+    Norm(T, d, kind="token", sigmoid=True, scale=0.5, seed=14).check()

@@ -170,3 +170,19 @@ def test_pages_beyond_32_bits():
         got = torch.stack([pool[w][i * stride:i * stride + small.page] for i in range(6)])
         assert torch.equal(got, small.dev[w].view(6, small.page))
         assert int(pool[w].count_nonzero()) == int(got.count_nonzero())
+
+
+@pytest.mark.parametrize("fmt,D,hq,hkv,rot", [("bf16", 128, 40, 4, 128), ("e4m3", 128, 40, 4, 128), ("bf16", 128, 40, 4, 32),
+                                              ("bf16", 64, 90, 3, 64), ("e4m3", 64, 90, 3, 0), ("bf16", 256, 20, 2, 256),
+                                              ("e4m3", 256, 20, 2, 64)])
+def test_calls_that_stream(fmt, D, hq, hkv, rot):
+    """Rows of more than the L2s hold: other loads and stores, the same results; in place too."""
+    cuda()
+    T = 4001
+    assert T * (2 * hq + 2 * hkv) * D * 2 > 32 << 20
+    cache = Cache(fmt, 64, 64, hkv, D, 8)
+    rng = np.random.default_rng(8)
+    slots, pos = (np.arange(T) + 30) % 4096, rng.integers(0, 512, T)
+    slots[::501] = -1
+    call = Call(cache, T, hq, rot, slots, pos, seed=8)
+    call.check(in_place=rot == D)
