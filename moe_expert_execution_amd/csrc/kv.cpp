@@ -165,6 +165,7 @@ ft_status ft_kv_attend(const ft_kv_cache* cache, const ft_attend* a, ft_workspac
     s = check_rows(a->q, a->q_stride, row, "q");
     if (s == FT_OK) s = check_rows(a->out, a->out_stride, row, "out");
     if (s != FT_OK) return s;
+    FT_REQUIRE(a->out != a->q, "out must not be q");
     FT_REQUIRE(a->table && a->kv_len && aligned(a->table, 4) && aligned(a->kv_len, 4) && aligned(a->sinks, 4),
                "table or kv_len is null, or one of table, kv_len and sinks misaligned");
     s = check_workspace(ws, kv_attend_workspace(a->q_heads / c.heads, c.D), stream);

@@ -103,10 +103,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     constexpr int E = FMT == FT_KV_BF16 ? 2 : 1;
     constexpr int kLanes = lanes_of(D), kTokens = 64 / kLanes, kGroups = D / 16 / kLanes;
     const int lane = threadIdx.x & 63;
-    const int64_t wave = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+    const uint32_t wave = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);      // (below 2^26)
     const int heads = a.a.q_heads + 2 * a.c.heads, parts = (heads + a.per - 1) / a.per;
     const int group = (int)(wave % kGroups), part = (int)(wave / kGroups % parts);
-    const int64_t t = wave / kGroups / parts * kTokens + lane % kTokens;
+    const int64_t t = (int)(wave / kGroups / parts) * kTokens + lane % kTokens;
     if (t >= a.a.tokens) return;
     const int half = a.a.rot >> 1, pair = group * kLanes + lane / kTokens;
     // the pair's first dimensions: rotating ones come first, the rest are neighbours

@@ -7,7 +7,7 @@ import numpy as np
 import torch
 
 from . import (FtClassifyOut, FtLora, ft_cache_create, ft_cache_create_layers, ft_cache_destroy, ft_host_alloc,
-               ft_host_free, ft_workspace_create, ft_workspace_destroy, host_array, profile, shape)
+               ft_host_free, ft_workspace_create, ft_workspace_destroy, host_array, kv_cache, profile, shape)
 
 
 class ClassifyBuffers:
@@ -128,3 +128,23 @@ class LoraPool:
                 raise ValueError("pools are contiguous device tensors: a and b bf16, rank int32, scale fp32")
         self.a, self.b, self.rank, self.scale = a, b, rank, scale
         self.struct = FtLora(count, max_rank, rank.data_ptr(), scale.data_ptr(), a.data_ptr(), b.data_ptr())
+
+
+class KvPool:
+    """A layer's paged key-value cache as device tensors, kept alive with its ft_kv_cache: k and v
+    [pages, kv_heads * page_tokens * head_dim] in the layout of the C header, bf16 or e4m3 (then with
+    k_scale, v_scale [kv_heads] fp32).  Uninitialised: what no token was appended to is not read."""
+
+    def __init__(self, pages, page_tokens, kv_heads, head_dim, fmt="bf16", k_scale=None, v_scale=None, device="cuda"):
+        dt = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+        self.k, self.v = (torch.empty(pages, kv_heads * page_tokens * head_dim, dtype=dt, device=device)
+                          for _ in range(2))
+        for t in (k_scale, v_scale):
+            if (t is None) != (fmt == "bf16"):
+                raise ValueError("an e4m3 cache has scales, a bf16 one has none")
+            if t is not None and (t.shape != (kv_heads,) or t.dtype != torch.float32 or not t.is_contiguous() or
+                                  t.device != self.k.device):
+                raise ValueError("scales are contiguous fp32 [kv_heads] on the cache's device")
+        self.k_scale, self.v_scale = k_scale, v_scale
+        p = [t.data_ptr() if t is not None else 0 for t in (self.k, self.v, k_scale, v_scale)]
+        self.struct = kv_cache(pages, page_tokens, kv_heads, head_dim, fmt, *p)

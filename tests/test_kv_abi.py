@@ -47,7 +47,7 @@ def append(**kw):
 
 
 def attend(**kw):
-    a = dict(requests=3, q_heads=4, width=5, scale=0.1, q=16, q_stride=512, table=16, kv_len=16, out=16,
+    a = dict(requests=3, q_heads=4, width=5, scale=0.1, q=16, q_stride=512, table=16, kv_len=16, out=32,
              out_stride=512)
     a.update(kw)
     return M.kv_attend(**a)
@@ -86,7 +86,7 @@ def test_streams_refused():
     (dict(width=131073), "width"), (dict(window=-1), "window"), (dict(scale=NAN), "scale"), (dict(scale=INF), "scale"),
     (dict(q=0), "null pointer: q"), (dict(out=0), "null pointer: out"), (dict(q=8), "aligned"),
     (dict(out_stride=504), "stride"), (dict(q_stride=516), "stride"), (dict(table=0), "table"),
-    (dict(kv_len=0), "kv_len"), (dict(kv_len=18), "misaligned"), (dict(sinks=17), "misaligned"),
+    (dict(out=16), "out must not be q"), (dict(kv_len=0), "kv_len"), (dict(kv_len=18), "misaligned"), (dict(sinks=17), "misaligned"),
     (dict(), "workspace is null")])
 def test_attends_refused(kw, msg):
     check(M.ft_kv_attend, cache(), attend(**kw), 0, msg=msg)
