@@ -25,7 +25,6 @@ namespace ftmoe {
 namespace {
 
 using rs::last_arrival;
-constexpr int kWaves = kv::kWaves, kThreads = kWaves * 64;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct AttendArgs {
@@ -277,9 +276,12 @@ __device__ __forceinline__ void store_out(uint16_t* to, const f32x4_t o, float l
 // Waves of a SIMD whose registers the kernel fits: teams are two to a compute unit, whole items as many as can be.
 constexpr int waves_of(int D, int fmt, bool direct) { return direct && (D < 256 || fmt == FT_KV_E4M3) ? 3 : 2; }
 
+constexpr int workgroup(int D, bool direct) { return 64 * (direct ? kv::kDirectWaves : kv::team_waves(D)); }
+
 template <int D, int FMT, bool WIDE, bool DIRECT>
-__global__ void __launch_bounds__(kThreads, waves_of(D, FMT, DIRECT)) attend_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(workgroup(D, DIRECT), waves_of(D, FMT, DIRECT)) attend_kernel(AttendArgs a) {
     using T = Kv<D, FMT>;
+    constexpr int kThreads = workgroup(D, DIRECT), kWaves = kThreads / 64;
     constexpr int kUnit = WIDE ? 4 : T::cv, kHalves = T::cv / kUnit;  // dimensions of a value unit that a round takes
     constexpr int kChunk = 16 * kUnit, kRow = kChunk + 4;        // dimensions of a round; padded in LDS
     extern __shared__ int lds[];
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, waves_of(D, FMT, DIRECT)) attend_ker
                 for (int i = tid * 8; i < a.a.q_heads * D; i += kThreads * 8)
                     *reinterpret_cast<u32x4_t*>(a.a.out + r * a.a.out_stride + i) = u32x4_t{0, 0, 0, 0};
         if (carry == 0) return;
-        div = kv::divide((uint32_t)busy * heads_all, (uint32_t)carry * heads_all, gridDim.x);
+        div = kv::divide((uint32_t)busy * heads_all, (uint32_t)carry * heads_all, kWaves, gridDim.x);
         if (self >= div.teams) return;
         // the item that this team's cut falls into, before it moves (64 requests a look); then on from item to
         // item
@@ -654,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, waves_of(D, FMT, DIRECT)) attend_ker
 
 template <int D, int FMT, bool WIDE, bool DIRECT>
 hipError_t start(const AttendArgs& a, int grid, hipStream_t st) {
+    constexpr int kThreads = workgroup(D, DIRECT), kWaves = kThreads / 64;
     // (the join's shares take 6 floats a thread)
     const size_t row = 16 * (WIDE ? 4 : Kv<D, FMT>::cv) + 4;
     const size_t waves = (size_t)kWaves * kv::item_heads(a.g) * row * 4, join = kThreads * 6 * 4;
@@ -668,7 +671,7 @@ template <int D, int FMT, bool WIDE>
 hipError_t go(const AttendArgs& a, int64_t steps, hipStream_t st) {
     const int64_t items = (int64_t)a.a.requests * a.c.heads * a.blocks;
     if (steps <= kv::kDirectSteps) return start<D, FMT, WIDE, true>(a, (int)items, st);
-    return start<D, FMT, WIDE, false>(a, kv::grid_of(items, items * steps), st);
+    return start<D, FMT, WIDE, false>(a, kv::grid_of(items, items * steps, D), st);
 }
 
 template <int D>

@@ -32,8 +32,14 @@ FT_HD constexpr int value_tokens(int D, int esize) { return 16 / (esize * value_
 // steps and kItemCost, are cut into `teams` ranges of equal length, one workgroup each, so
 // ragged lengths balance by themselves.  An item that is cut is joined by the last of its teams to
 // arrive, so a cut within `slack` steps of an item's end moves there.
-constexpr int kWaves = 4;                  // of a team; they share a segment's steps
-constexpr int kMaxTeams = 512;             // two for each of 256 compute units: all are resident, as one that starts late ends late
+constexpr int kMaxTeams = 512;
+// Waves of a team, which share a segment's steps, and teams of a call: eight waves to each of 256 compute units,
+// as registers allow, so all teams are resident (one that starts late ends late).  Two teams of four overlap one
+// another's ends (64 requests of up to 8,192 tokens, 128 dimensions: 111 us, 113 with one of eight; e4m3 57, 69); heads of
+// 256 have twice the partial sums, and one team of eight halves those (13 requests of up to 65,536, e4m3: 56 us,
+// 60 with two of four; bf16, 32 of up to 8,192: 34, 39).
+FT_HD constexpr int team_waves(int D) { return D == 256 ? 8 : 4; }
+FT_HD constexpr int most_teams(int D) { return 8 * 256 / team_waves(D); }
 constexpr int kSlack = 8;
 constexpr int kItemCost = 8;               // what an item takes beside its steps, in steps
 constexpr int kJoin = 8;                  // parts of a run
@@ -51,8 +57,8 @@ FT_HD inline int item_length(int steps) { return steps ? steps + kItemCost : 0; 
 
 // `items` that have steps, `total` length, at most `grid` teams: one for as many steps as it has
 // waves, or for an item where items are shorter.
-FT_HD inline Division divide(uint32_t items, uint32_t total, int grid) {
-    uint32_t t = (total - items * kItemCost + kWaves - 1) / kWaves;
+FT_HD inline Division divide(uint32_t items, uint32_t total, int waves, int grid) {
+    uint32_t t = (total - items * kItemCost + waves - 1) / waves;
     if (t < items) t = items;
     if (t > (uint32_t)grid) t = grid;
     const uint32_t base = total / t, half = (base - 1) / 2;      // less than half a range: few teams stay idle
@@ -106,12 +112,13 @@ FT_HD inline int head_blocks(int g) { return (g + kCols - 1) / kCols; }
 FT_HD inline int64_t part_floats(int g, int D) { return (int64_t)item_heads(g) * D + 4 * kCols; }
 
 // Workgroups of a launch of at most so many items and steps (up to kMaxSteps).
-inline int grid_of(int64_t items, int64_t steps) {
-    return divide((uint32_t)items, (uint32_t)(steps + items * kItemCost), kMaxTeams).teams;
+inline int grid_of(int64_t items, int64_t steps, int D) {
+    return divide((uint32_t)items, (uint32_t)(steps + items * kItemCost), team_waves(D), most_teams(D)).teams;
 }
 
 // Items of at most this many steps are not cut, so they need no division: a workgroup each.
-constexpr int kDirectSteps = 8 * kWaves;
+constexpr int kDirectWaves = 4;
+constexpr int kDirectSteps = 8 * kDirectWaves;
 
 }  // namespace kv
 }  // namespace ftmoe

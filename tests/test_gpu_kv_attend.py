@@ -216,6 +216,9 @@ def test_many_requests():
     for B in (255, 256, 257, 1000):
         make("bf16", 64, 1, 2, 16, rng.integers(0, 40, B).tolist(), seed=17).check()
     make("e4m3", 64, 1, 1, 16, [3] * 4096, seed=18).check()
+    # lists and sums of more than 64 KiB of LDS, items that are cut
+    for fmt, g in (("bf16", 16), ("e4m3", 8)):
+        make(fmt, 256, 1, g, 16, [2] * 3000 + [1500, 0] + [40] * 1094, seed=19).check()
 
 
 def test_pages_beyond_32_bits():
