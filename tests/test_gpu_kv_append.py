@@ -25,25 +25,31 @@ class Call:
         self.cos_sin = np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)
         self.slots, self.pos = np.asarray(slots, np.int64), np.asarray(pos, np.int64)
 
-    def run(self, in_place=False, on=None):
-        c, T, hq, D, hkv = self.cache, self.T, self.hq, self.cache.D, self.cache.heads
+    def args(self, in_place=False):
+        T, hq, D, hkv = self.T, self.hq, self.cache.D, self.cache.heads
         self.x = dev(self.bits.view(np.int16))
         self.q = torch.full((T, hq * D), 0x4321, dtype=torch.int16, device="cuda")
         self.keep = [dev(self.slots.astype(np.int32)), dev(self.pos.astype(np.int32)), dev(self.cos_sin)]
         p = self.x.data_ptr()
         out, out_stride = (p, self.row) if in_place else (self.q.data_ptr(), hq * D)
-        a = M.kv_append(T, p + 2 * hq * D, self.row, p + 2 * (hq + hkv) * D, self.row, self.keep[0].data_ptr(),
-                        self.keep[1].data_ptr() if self.rot else 0, self.rot, len(self.cos_sin) if self.rot else 0,
-                        self.keep[2].data_ptr() if self.rot else 0, hq, p if hq else 0, self.row, out if hq else 0,
-                        out_stride)
-        M.ft_kv_append(c.struct(), a, stream() if on is None else on)
+        return M.kv_append(T, p + 2 * hq * D, self.row, p + 2 * (hq + hkv) * D, self.row, self.keep[0].data_ptr(),
+                           self.keep[1].data_ptr() if self.rot else 0, self.rot, len(self.cos_sin) if self.rot else 0,
+                           self.keep[2].data_ptr() if self.rot else 0, hq, p if hq else 0, self.row, out if hq else 0,
+                           out_stride)
+
+    def run(self, in_place=False, around=lambda call: call()):
+        """`around` makes the call: for what happens beside it."""
+        a, T, hq, D = self.args(in_place), self.T, self.hq, self.cache.D
+        c = self.cache.struct()
+        torch.cuda.synchronize()
+        around(lambda: M.ft_kv_append(c, a, stream()))
         torch.cuda.synchronize()
         q = self.x.cpu().numpy()[:, :hq * D] if in_place else self.q.cpu().numpy()
         return q.view(np.uint16).reshape(T, hq, D)
 
-    def check(self, in_place=False):
+    def check(self, in_place=False, **kw):
         c, T, hq, D, hkv = self.cache, self.T, self.hq, self.cache.D, self.cache.heads
-        q = self.run(in_place)
+        q = self.run(in_place, **kw)
         x = OF.bf16_to_f64(self.bits[:, :(hq + 2 * hkv) * D]).reshape(T, hq + 2 * hkv, D)
         live = (self.slots >= 0) & (self.slots < c.pages * c.P)
         if self.rot:

@@ -38,13 +38,14 @@ class Attend:
     def bits(self):
         return self.out.cpu().numpy().view(np.uint16)
 
-    def run(self, ws=None, times=1):
+    def run(self, ws=None, times=1, around=lambda call: call()):
         c = self.cache.struct()
         own = ws is None
         ws = ws or Workspace(M.ft_kv_attend_workspace(c, self.hq, max(self.B, 1)))
         a = self.args()
+        torch.cuda.synchronize()
         for _ in range(times):
-            M.ft_kv_attend(c, a, ws.handle, stream())
+            around(lambda: M.ft_kv_attend(c, a, ws.handle, stream()))
         torch.cuda.synchronize()
         if own:
             ws.close()
@@ -52,8 +53,8 @@ class Attend:
         assert (out[self.B:] == 0x5A5A).all() and (out[:, self.hq * self.D:] == 0x5A5A).all()
         return out[:self.B, :self.hq * self.D].reshape(self.B, self.hq, self.D)
 
-    def check(self, raw=None, ws=None, what=""):
-        got = self.run(ws)
+    def check(self, raw=None, ws=None, what="", **kw):
+        got = self.run(ws, **kw)
         q = self.q[:, :self.hq * self.D].reshape(self.B, self.hq, self.D)
         ref, bound = attend_reference(self.cache, q, self.table, self.lens, self.scale, self.window, self.sinks, raw)
         assert_within(OF.bf16_to_f64(got), ref, bound, what)
