@@ -688,7 +688,7 @@ ft_status ft_kv_append(const ft_kv_cache* cache, const ft_append* args, void* st
  *   width * page_tokens at most 2^35.  q, out [requests x q_heads x head_dim]
  *   bf16.  scale is finite.
  * A position whose page id is outside 0..pages - 1 is left out.  A request that
- * sees no position gets zeros.  What pages hold beyond the visible positions,
+ * sees no position, or none whose logit is above minus infinity, gets zeros.  What pages hold beyond the visible positions,
  * and table entries beyond them, reaches no result.
  * Sums and softmax statistics are fp32; probabilities keep 16 significant bits
  * for the product with the values.  The work of all requests is divided evenly

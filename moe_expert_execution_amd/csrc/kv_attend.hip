@@ -258,9 +258,9 @@ __device__ __forceinline__ float other_half(float v) {
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x128, 0xF, 0xF, true));
 }
 
-// Weight of a part whose maximum is m, beside the whole's maximum.
+// Weight of a part whose maximum is m, beside the whole's maximum (1 for the largest, an infinite one too).
 __device__ __forceinline__ float part_weight(float m, float whole) {
-    return whole == -INFINITY ? 0.0f : exp2_of(m - whole);
+    return whole == -INFINITY ? 0.0f : m == whole ? 1.0f : exp2_of(m - whole);
 }
 
 // out[0..3] of one head: o / l, zeros where nothing was visible.
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(workgroup(D, DIRECT), waves_of(D, FMT, DIRECT)
     constexpr int kThreads = workgroup(D, DIRECT), kWaves = kThreads / 64;
     constexpr int kUnit = WIDE ? 4 : T::cv, kHalves = T::cv / kUnit;  // dimensions of a value unit that a round takes
     constexpr int kChunk = 16 * kUnit, kRow = kChunk + 4;        // dimensions of a round; padded in LDS
-    extern __shared__ int lds[];
+    extern __shared__ __align__(16) int lds[];
     const int B = a.a.requests, tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     int* pre = lds;                                              // [B + 1] length of an item of each request before
     int* lens = pre + B + 1;                                     // [B] visible lengths' ends

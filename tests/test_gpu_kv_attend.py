@@ -8,7 +8,7 @@ import synth
 from moe_expert_execution_amd.tensors import Workspace
 from oracle import formats as OF
 from tests.gpu_util import cuda, dev
-from tests.kv_util import Cache, attend_reference, random_table, stream
+from tests.kv_util import Cache, attend_reference, attend_row, random_table, stream
 from tests.resident_util import assert_within
 
 pytestmark = pytest.mark.gpu
@@ -61,26 +61,48 @@ class Attend:
         return got
 
 
-def make(fmt, D, hkv, g, P, lens, seed=0, spare=3, **kw):
-    table, pages = random_table(lens, P, spare, seed)
+# A table for more than 1,024 tokens a request: the work is divided and cut; without, a workgroup takes a whole item.
+WIDE = [False, True]
+
+
+def extra(wide, P):
+    return 1 + 1024 // P if wide else 2
+
+
+def make(fmt, D, hkv, g, P, lens, seed=0, spare=3, wide=False, **kw):
+    table, pages = random_table(lens, P, spare, seed, extra(wide, P))
     return Attend(Cache(fmt, pages, P, hkv, D, seed), table, lens, hkv * g, seed=seed, **kw)
 
 
 @pytest.mark.parametrize("fmt,D", FORMS)
 @pytest.mark.parametrize("g", [1, 3, 8, 9, 16, 17, 33])
-def test_head_groups(fmt, D, g):
+@pytest.mark.parametrize("wide", WIDE)
+def test_head_groups(fmt, D, g, wide):
     cuda()
-    make(fmt, D, 2, g, 16, [1, 0, 77, 300], seed=g).check()
+    make(fmt, D, 2, g, 16, [1, 0, 77, 300], seed=g, wide=wide).check()
+    if wide:                                                  # cut and joined
+        make(fmt, D, 1, g, 16, [2500], seed=g).check()
 
 
 @pytest.mark.parametrize("fmt,D", FORMS)
 @pytest.mark.parametrize("P", [16, 32, 64, 128, 256])
-def test_lengths(fmt, D, P):
+@pytest.mark.parametrize("wide", WIDE)
+def test_lengths(fmt, D, P, wide):
     """Lengths round every border: a block, a step, a team's steps, a page."""
     cuda()
     lens = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 513]
-    make(fmt, D, 1, 4, P, lens, seed=P).check()
-    make(fmt, D, 3, 12, P, lens[::-1], seed=P + 1).check()
+    make(fmt, D, 1, 4, P, lens, seed=P, wide=wide).check()
+    make(fmt, D, 3, 12, P, lens[::-1], seed=P + 1, wide=wide).check()
+
+
+@pytest.mark.parametrize("n", [1007, 1008, 1009, 1023, 1024, 1025, 1040])
+def test_either_side_of_whole_items(n):
+    """Tables of 64 and 65 pages: the longest whole items and the shortest that are cut."""
+    cuda()
+    for fmt, D in (("bf16", 128), ("e4m3", 256)):
+        a = make(fmt, D, 2, 6, 16, [n, 3, 0, n // 2], seed=n)
+        a.table = a.table[:, :max(64, -(-n // 16))].copy()
+        a.check()
 
 
 @pytest.mark.parametrize("fmt,D", FORMS)
@@ -109,8 +131,16 @@ def test_extreme_sinks():
     """A sink far above every logit, and of minus infinity (no term)."""
     cuda()
     lens = [0, 5, 900]
-    for s in (80.0, -np.inf, -3.0e38):
-        make("bf16", 128, 1, 4, 16, lens, seed=10, sinks=np.full(4, s, np.float32)).check()
+    for wide in WIDE:
+        for s in (80.0, -np.inf, -3.0e38):
+            make("bf16", 128, 1, 4, 16, lens, seed=10, sinks=np.full(4, s, np.float32), wide=wide).check()
+        # an infinite sink takes everything, as the formula's limit; a NaN one is NaN in its own head
+        for lens in ([0, 5, 900], [3000, 2, 1]):
+            got = make("bf16", 128, 1, 4, 16, lens, seed=10, sinks=np.array([np.inf, 0, np.nan, 1], np.float32),
+                       wide=wide).run()
+            out = OF.bf16_to_f64(got)
+            assert (out[:, 0] == 0).all() and np.isfinite(out[:, [1, 3]]).all()
+            assert all(np.isnan(out[b, 2]).all() for b in range(3) if lens[b])
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
@@ -119,17 +149,19 @@ def test_peaked_and_flat_logits(fmt):
     cuda()
     for q_scale in (60.0, 0.0, 1e-3):
         make(fmt, 128, 2, 4, 16, [1, 50, 2500], seed=11, q_scale=q_scale).check()
+        make(fmt, 128, 2, 4, 16, [1, 50, 700], seed=11, q_scale=q_scale).check()
 
 
 @pytest.mark.parametrize("fmt,D", FORMS)
-def test_what_lies_beside_the_visible_tokens(fmt, D):
+@pytest.mark.parametrize("wide", WIDE)
+def test_what_lies_beside_the_visible_tokens(fmt, D, wide):
     """NaN in the cache everywhere but in the visible tokens: the rest of the last page, pages of others, and tokens
     before a window reach nothing."""
     cuda()
     P = 64
     lens = [1, 15, 33, 64, 65, 200, 0, 350]
     for window in (0, 40):
-        table, pages = random_table(lens, P, 2, 12)
+        table, pages = random_table(lens, P, 2, 12, extra(wide, P))
         cache = Cache(fmt, pages, P, 2, D, 12, fill="nan")
         rng = np.random.default_rng(12)
         for b, n in enumerate(lens):
@@ -146,11 +178,12 @@ def test_what_lies_beside_the_visible_tokens(fmt, D):
 
 
 @pytest.mark.parametrize("fmt,D", FORMS)
-def test_pages_outside_the_pool_are_left_out(fmt, D):
+@pytest.mark.parametrize("wide", WIDE)
+def test_pages_outside_the_pool_are_left_out(fmt, D, wide):
     cuda()
     for P in (16, 32):
         lens = [40, 100, 16, 48]
-        table, pages = random_table(lens, P, 1, 13)
+        table, pages = random_table(lens, P, 1, 13, extra(wide, P))
         table[0, 0] = -1
         table[1, 1] = pages
         table[1, 2] = 2 ** 31 - 1
@@ -162,19 +195,22 @@ def test_pages_outside_the_pool_are_left_out(fmt, D):
             assert (got[2:] == 0).all()
 
 
-def test_lengths_out_of_range():
+@pytest.mark.parametrize("full", [32, 1200])
+def test_lengths_out_of_range(full):
     cuda()
-    table, pages = random_table([32, 32, 32], 16, 1, 14, extra_width=0)
+    table, pages = random_table([32, full, 32], 16, 1, 14, extra_width=0)
     cache = Cache("bf16", pages, 16, 1, 128, 14)
     Attend(cache, table, [-5, 2 ** 31 - 1, -2 ** 31], 4, seed=14).check()
+    Attend(cache, table, [-5, full + 1, 2 ** 31 - 16], 4, seed=14).run()
 
 
-def test_infinite_and_nan_values():
+@pytest.mark.parametrize("wide", WIDE)
+def test_infinite_and_nan_values(wide):
     """What the formula gives: a NaN key or value makes its heads NaN, an infinite value at a probability above zero
     infinite, and a key of minus infinity has no share."""
     cuda()
     P, D = 16, 64
-    table, pages = random_table([20, 20, 20, 20], P, 0, 15)
+    table, pages = random_table([20, 20, 20, 20], P, 0, 15, extra(wide, P))
     cache = Cache("bf16", pages, P, 1, D, 15)
     slot = lambda b, t: int(table[b, t // P]) * P + t % P  # noqa: E731
     kn = np.full((1, D), 0x7FC0)
@@ -192,13 +228,11 @@ def test_infinite_and_nan_values():
     assert np.isnan(out[0]).all()
     assert np.isposinf(out[1, :, 5]).all() and np.isfinite(np.delete(out[1], 5, axis=1)).all()
     t = np.arange(1, 20)
-    keep = Attend(cache, table, [20] * 4, 2, seed=15)
     ref_k = cache.read("k", [slot(2, int(i)) for i in t], 0)
     ref_v = cache.read("v", [slot(2, int(i)) for i in t], 0)
-    from tests.kv_util import attend_row
     ref, bound = attend_row(OF.bf16_to_f64(a.q[2].reshape(2, D)), ref_k, ref_v, a.scale)
     assert_within(out[2], ref, bound)
-    assert np.isfinite(out[3]).all() and keep is not None
+    assert np.isfinite(out[3]).all()
 
 
 def test_shared_pages():
@@ -278,10 +312,11 @@ def test_small_workspace_refused():
     ws.close()
 
 
-def test_captured():
-    """A captured call follows lengths, tables and cache contents as they are at each replay."""
+@pytest.mark.parametrize("width", [40, 80])
+def test_captured(width):
+    """A captured call follows lengths, tables and cache contents as they are at each replay; whole items and cut ones."""
     cuda()
-    P, width = 16, 40
+    P = 16
     rng = np.random.default_rng(50)
     table = rng.permutation(5 * width).reshape(5, width).astype(np.int32)
     cache = Cache("bf16", 5 * width, P, 2, 128, 50)
@@ -292,7 +327,8 @@ def test_captured():
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         M.ft_kv_attend(cache.struct(), args, ws.handle, stream())
-    for lens in ([0, 0, 0, 0, 0], [1, 2, 3, 4, 5], [640, 0, 17, 33, 600], [0, 0, 640, 0, 0], [100] * 5):
+    full = P * width
+    for lens in ([0, 0, 0, 0, 0], [1, 2, 3, 4, 5], [full, 0, 17, 33, 600], [0, 0, full, 0, 0], [100] * 5):
         a.lens = np.array(lens)
         a.keep[2].copy_(torch.from_numpy(np.array(lens, np.int32)))
         a.out.fill_(0x5A5A)
