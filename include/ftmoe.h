@@ -688,8 +688,9 @@ ft_status ft_kv_append(const ft_kv_cache* cache, const ft_append* args, void* st
  *   width * page_tokens at most 2^35.  q, out [requests x q_heads x head_dim]
  *   bf16.  scale is finite.
  * A position whose page id is outside 0..pages - 1 is left out.  A request that
- * sees no position, or none whose logit is above minus infinity, gets zeros.  What pages hold beyond the visible positions,
- * and table entries beyond them, reaches no result.
+ * sees no position, or none whose logit is above minus infinity, gets zeros.
+ * What pages hold beyond the visible positions, and table entries beyond them,
+ * reaches no result.
  * Sums and softmax statistics are fp32; probabilities keep 16 significant bits
  * for the product with the values.  The work of all requests is divided evenly
  * over workgroups, so the order of a request's sums depends on the lengths of the
@@ -726,9 +727,9 @@ ft_status ft_kv_attend(const ft_kv_cache* cache, const ft_attend* args, ft_works
  *   normed = sum / sqrt(mean(sum^2) + eps) * (weight_offset + pre_w)
  * per token, in fp32, the second norm from the sum before its rounding.
  * block, residual, sum, normed [T x d] bf16; post_w, pre_w [d] bf16.
- * T 0..2^24 (0 enqueues nothing), d a multiple of 8, 8..32768; strides in
- *   elements, a multiple of 8 and at least d; everything 16-byte aligned (a gate
- *   per token: 2-byte).
+ * T 0..2^24 (0 enqueues nothing), d a multiple of 8, 8..32768, T * d at most
+ *   2^34; strides in elements, a multiple of 8 and at least d; everything 16-byte
+ *   aligned (a gate per token: 2-byte).
  * block NULL: no such term (then post_w and gate are NULL); residual NULL: no
  *   such term; one of them is there.  sum or normed may be NULL: not written;
  *   normed needs pre_w, and pre_w normed.

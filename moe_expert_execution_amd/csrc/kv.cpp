@@ -179,6 +179,7 @@ ft_status ft_block_norm(const ft_norm* a, void* stream) {
     FT_REQUIRE(a, "args is null");
     FT_REQUIRE(a->T >= 0 && a->T <= 1 << 24, "T must be in 0..2^24");
     FT_REQUIRE(a->d >= 8 && a->d <= 32768 && a->d % 8 == 0, "d must be a multiple of 8 in 8..32768");
+    FT_REQUIRE((int64_t)a->T * a->d <= (int64_t)1 << 34, "T * d must be at most 2^34");
     const int kind = a->gate_kind & ~FT_GATE_SIGMOID;
     FT_REQUIRE(a->gate_kind >= 0 && kind <= FT_GATE_FULL && (kind || !a->gate_kind), "bad gate_kind");
     FT_REQUIRE(a->eps >= 0 && isfinite(a->eps) && isfinite(a->residual_scale) && isfinite(a->weight_offset),

@@ -180,7 +180,7 @@ def test_pages_beyond_32_bits():
 
 @pytest.mark.parametrize("fmt,D,hq,hkv,rot", [("bf16", 128, 40, 4, 128), ("e4m3", 128, 40, 4, 128), ("bf16", 128, 40, 4, 32),
                                               ("bf16", 64, 90, 3, 64), ("e4m3", 64, 90, 3, 0), ("bf16", 256, 20, 2, 256),
-                                              ("e4m3", 256, 20, 2, 64)])
+                                              ("e4m3", 256, 20, 2, 64), ("bf16", 128, 41, 3, 128), ("e4m3", 64, 90, 4, 64)])
 def test_calls_that_stream(fmt, D, hq, hkv, rot):
     """Rows of more than the L2s hold: other loads and stores, the same results; in place too."""
     cuda()

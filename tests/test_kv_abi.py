@@ -146,7 +146,8 @@ def norm(**kw):
 
 @pytest.mark.parametrize("kw,msg", [
     (dict(T=-1), "T must"), (dict(T=2 ** 24 + 1), "T must"), (dict(d=0), "d must"), (dict(d=60), "d must"),
-    (dict(d=32776), "d must"), (dict(gate_kind=4), "gate_kind"), (dict(gate_kind=0x10), "gate_kind"),
+    (dict(d=32776), "d must"), (dict(T=2 ** 19 + 1, d=32768), "T * d must"),
+    (dict(T=2 ** 24, d=1032), "T * d must"), (dict(gate_kind=4), "gate_kind"), (dict(gate_kind=0x10), "gate_kind"),
     (dict(gate_kind=-1), "gate_kind"), (dict(gate_kind=0x21), "gate_kind"), (dict(eps=-1.0), "eps"),
     (dict(eps=NAN), "eps"), (dict(eps=INF), "eps"), (dict(residual_scale=NAN), "finite"),
     (dict(weight_offset=INF), "finite"), (dict(block=0, post_w=16), "need block"),
