@@ -277,12 +277,14 @@ __device__ __forceinline__ void store_out(uint16_t* to, const f32x4_t o, float l
 // Waves of a SIMD whose registers the kernel fits: teams are two to a compute unit, whole items as many as can be.
 constexpr int waves_of(int D, int fmt, bool direct) { return direct && (D < 256 || fmt == FT_KV_E4M3) ? 3 : 2; }
 
-constexpr int workgroup(int D, bool direct) { return 64 * (direct ? kv::kDirectWaves : kv::team_waves(D)); }
+constexpr int workgroup(int D, int waves) { return 64 * (waves ? waves : kv::team_waves(D)); }
 
-template <int D, int FMT, bool WIDE, bool DIRECT>
-__global__ void __launch_bounds__(workgroup(D, DIRECT), waves_of(D, FMT, DIRECT)) attend_kernel(AttendArgs a) {
+// WAVES: of a workgroup that takes a whole item, or 0: teams of a divided launch.
+template <int D, int FMT, bool WIDE, int WAVES>
+__global__ void __launch_bounds__(workgroup(D, WAVES), waves_of(D, FMT, WAVES > 0)) attend_kernel(AttendArgs a) {
     using T = Kv<D, FMT>;
-    constexpr int kThreads = workgroup(D, DIRECT), kWaves = kThreads / 64;
+    constexpr bool DIRECT = WAVES > 0;
+    constexpr int kThreads = workgroup(D, WAVES), kWaves = kThreads / 64;
     constexpr int kUnit = WIDE ? 4 : T::cv, kHalves = T::cv / kUnit;  // dimensions of a value unit that a round takes
     constexpr int kChunk = 16 * kUnit, kRow = kChunk + 4;        // dimensions of a round; padded in LDS
     extern __shared__ __align__(16) int lds[];
@@ -655,24 +657,25 @@ __global__ void __launch_bounds__(workgroup(D, DIRECT), waves_of(D, FMT, DIRECT)
     }
 }
 
-template <int D, int FMT, bool WIDE, bool DIRECT>
+template <int D, int FMT, bool WIDE, int WAVES>
 hipError_t start(const AttendArgs& a, int grid, hipStream_t st) {
-    constexpr int kThreads = workgroup(D, DIRECT), kWaves = kThreads / 64;
+    constexpr int kThreads = workgroup(D, WAVES), kWaves = kThreads / 64;
     // (the join's shares take 6 floats a thread)
     const size_t row = 16 * (WIDE ? 4 : Kv<D, FMT>::cv) + 4;
     const size_t waves = (size_t)kWaves * kv::item_heads(a.g) * row * 4, join = kThreads * 6 * 4;
-    const size_t list = DIRECT ? 0 : ((size_t)2 * a.a.requests + 1 + 3) & ~(size_t)3;
+    const size_t list = WAVES ? 0 : ((size_t)2 * a.a.requests + 1 + 3) & ~(size_t)3;
     const size_t lds = list * 4 + 2 * kWaves * kv::kCols * 4 +
                        (waves > join ? waves : join);
-    return launch(attend_kernel<D, FMT, WIDE, DIRECT>, dim3(grid), dim3(kThreads), lds, st, a);
+    return launch(attend_kernel<D, FMT, WIDE, WAVES>, dim3(grid), dim3(kThreads), lds, st, a);
 }
 
 // `steps`: the most that an item can have.
 template <int D, int FMT, bool WIDE>
 hipError_t go(const AttendArgs& a, int64_t steps, hipStream_t st) {
     const int64_t items = (int64_t)a.a.requests * a.c.heads * a.blocks;
-    if (steps <= kv::kDirectSteps) return start<D, FMT, WIDE, true>(a, (int)items, st);
-    return start<D, FMT, WIDE, false>(a, kv::grid_of(items, items * steps, D), st);
+    if (steps > kv::kDirectSteps) return start<D, FMT, WIDE, 0>(a, kv::grid_of(items, items * steps, D), st);
+    if (kv::direct_waves(items, steps) == 2) return start<D, FMT, WIDE, 2>(a, (int)items, st);
+    return start<D, FMT, WIDE, kv::kDirectWaves>(a, (int)items, st);
 }
 
 template <int D>

@@ -125,5 +125,14 @@ inline int grid_of(int64_t items, int64_t steps, int D) {
 constexpr int kDirectWaves = 4;
 constexpr int kDirectSteps = 8 * kDirectWaves;
 
+// Two waves an item where items are short and three or more to each of 256 compute units: a wave's start and the sum over
+// waves are most of a short item's cost.  100 requests, 8 KV heads, a window of 128: heads of 64 / 128 / 256 8.9 / 15.0 /
+// 28.9 us, 9.7 / 16.0 / 34.3 with four; in e4m3 7.4 / 10.9 / 19.6, 7.9 / 12.1 / 21.1.  64 requests: 7.3 / 11.1 / 20.4 with
+// two, 7.2 / 11.0 / 19.4 with four; windows of 256 over 250: 24.6 / 46.5 / 91.8, 23.9 / 43.8 / 93.2.
+constexpr int kShortSteps = 8, kManyItems = 768;
+inline int direct_waves(int64_t items, int64_t steps) {
+    return steps <= kShortSteps && items >= kManyItems ? kDirectWaves / 2 : kDirectWaves;
+}
+
 }  // namespace kv
 }  // namespace ftmoe

@@ -127,6 +127,22 @@ def test_windows_and_sinks(fmt, D, window):
         make(fmt, D, 2, g, 32, lens, seed=9, window=window).check()
 
 
+@pytest.mark.parametrize("fmt,D", FORMS)
+@pytest.mark.parametrize("g", [1, 7, 12])
+def test_many_short_items(fmt, D, g):
+    """12 KV heads of 63 to 65 requests: either side of the number from which short items take two waves, by their
+    table's width (8 steps) or their window."""
+    cuda()
+    rng = np.random.default_rng(g)
+    for B in (63, 64, 65):
+        lens = rng.permutation(np.r_[[0, 1, 31, 32, 33, 64, 65, 96, 97, 255, 256], rng.integers(0, 257, B - 11)])
+        a = make(fmt, D, 12, g, 16, lens, seed=B)
+        a.table = a.table[:, :16].copy()
+        a.check()
+    sinks = (3 * rng.standard_normal(12 * g)).astype(np.float32)
+    make(fmt, D, 12, g, 32, 2 * lens, seed=9, window=127, sinks=sinks, gap=8).check()
+
+
 def test_extreme_sinks():
     """A sink far above every logit, and of minus infinity (no term)."""
     cuda()
