@@ -7,16 +7,12 @@
 // workgroup computes the sums for itself (some 4096 lengths, L2-resident) and
 // takes a share of the rows; the one that arrives last writes what may alias an
 // input (kv_len, counts), when nobody reads those any more.  Latency bounds it: 64
-// requests of a decode step 5.5 us in one wave, 1,000 of 16,384 rows 9.3 us.
+// requests of a decode step 5.2 us, 1,000 of 16,384 rows 8.5 us.
 #include "kv_device.h"
 #include "resident.h"
 
 namespace ftmoe {
 namespace {
-
-constexpr int kPer = 4;                                // requests of a thread
-constexpr int kThreads = kv::kMaxRequests / kPer;
-constexpr int kFew = 64;                               // threads of a call of few requests and rows: one wave
 
 // N exclusive prefix sums over the workgroup, of each thread's own sums v; total: the workgroup's.
 template <int THREADS, int N>
@@ -70,14 +66,16 @@ struct PlanArgs {
     bool shared;                                       // kv_len or counts lies over an input
 };
 
-template <int THREADS>
+template <int THREADS, int PER>
 __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a) {
     const ft_kv_batch& c = a.b;
-    constexpr int kMost = THREADS * kPer;
+    constexpr int kPer = PER, kMost = THREADS * kPer;  // requests of a thread, and of all
+    constexpr bool kKept = PER < 4;                    // (LDS holds no more; 2 to 3% by fewer trips to the L2)
     __shared__ int first[kMost + 1];                   // token row of each request
     __shared__ int lack[kMost + 1];                    // pages lacked before it
     __shared__ int back[kMost + 1];                    // pages returned before it
     __shared__ uint8_t served[kMost];
+    __shared__ int held[kKept ? kMost : 1], added[kKept ? kMost : 1];     // the clamped context, and add
     __shared__ int scan_lds[3][THREADS / 64];
     __shared__ uint32_t flag;
     const int B = c.requests, tid = threadIdx.x, P = 1 << a.page_shift, room = c.width << a.page_shift;
@@ -92,6 +90,10 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a) {
         const bool on = b0 + i < B;
         ctx[i] = on ? context(b0 + i) : 0;
         n[i] = on ? c.add[b0 + i] : 0;
+        if constexpr (kKept) {
+            held[b0 + i] = ctx[i];
+            added[b0 + i] = n[i];
+        }
         n[i] = n[i] > c.tokens ? c.tokens + 1 : n[i];  // (one more than fits: the sums stay within 32 bits)
         sum[0] += n[i] > 0 ? n[i] : 0;
     }
@@ -136,6 +138,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a) {
     block_scan<THREADS>(count, total, scan_lds);
     __syncthreads();
 
+    auto held_by = [&](int b) { return kKept ? held[b] : context(b); };
+    auto added_to = [&](int b) { return kKept ? added[b] : c.add[b]; };
     // entry i of the stack; i < F + R
     auto returned_page = [&](int i) {
         const int b = last_at_most(back, B, i);
@@ -148,8 +152,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a) {
         int b = c.row_tokens ? t / c.row_tokens : t < first[B] ? last_at_most(first, B + 1, t) : B;
         int pos = -1, slot = -1;
         if (b < B && served[b]) {
-            const int k = t - first[b], cb = context(b);
-            if (k < c.add[b]) {
+            const int k = t - first[b], cb = held_by(b);
+            if (k < added_to(b)) {
                 pos = cb + k;
                 const int j = pos >> a.page_shift, have = pages_of(cb);
                 const int page = j < have ? c.table[(int64_t)b * c.width + j] : stack(top - (lack[b] + j - have));
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a) {
     }
     for (int i = self; i < total[0]; i += stride) {
         const int b = last_at_most(lack, B, i);
-        c.table[(int64_t)b * c.width + pages_of(context(b)) + (i - lack[b])] = stack(top - i);
+        c.table[(int64_t)b * c.width + pages_of(held_by(b)) + (i - lack[b])] = stack(top - i);
     }
     // returned pages that nobody took: the free list grows (never past its `pages` entries, whatever a
     // table that names pages twice returns)
@@ -172,7 +176,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a) {
     if (gridDim.x > 1 && (a.shared ? !rs::last_arrival(a.counter, gridDim.x, &flag) : blockIdx.x != 0)) return;
     __syncthreads();
     for (int b = tid; b < B; b += THREADS) {
-        const int cb = context(b), m = c.add[b];
+        const int cb = held_by(b), m = added_to(b);
         c.kv_len[b] = m < 0 ? 0 : served[b] ? cb + m : cb;
     }
     for (int b = tid; b <= B; b += THREADS) c.start[b] = first[b];
@@ -184,7 +188,19 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a) {
     }
 }
 
+template <int THREADS, int PER>
+hipError_t go(const PlanArgs& a, hipStream_t st) {
+    const int rows = a.b.tokens + a.b.requests;
+    return launch(plan_kernel<THREADS, PER>, dim3((rows + THREADS - 1) / THREADS), dim3(THREADS), 0, st, a);
+}
+
 }  // namespace
+
+// The smallest workgroup with a thread a request, for scans of few waves and rows over many compute units (with four
+// requests a thread, in 1,024 threads: 1,000 requests of 16,384 rows 10.0 us, 8.5 so; 16 of 8,000 rows 7.2, 4.9; a wave
+// of four each for 64 decode requests 6.4, 5.2; 2,000 requests take two each: 10.3, 11.7 with four).  Of small ones at most
+// 64, since arrivals at one counter queue: 20 requests of 60,000 rows in place 5.4 us, 14 in 938 workgroups of a wave.
+constexpr int kMostGroups = 64;
 
 hipError_t launch_kv_plan(const ft_kv_batch& b, ft_workspace* ws, hipStream_t st) {
     PlanArgs a;
@@ -197,8 +213,12 @@ hipError_t launch_kv_plan(const ft_kv_batch& b, ft_workspace* ws, hipStream_t st
         a.shared |= over(b.kv_len, b.requests, in, b.requests) || over(b.counts, 4, in, b.requests);
     a.shared |= over(b.kv_len, b.requests, b.free_count, 1) || over(b.counts, 4, b.free_count, 1);
     const int rows = b.tokens + b.requests;
-    if (b.requests <= kFew * kPer && rows <= 4 * kFew) return launch(plan_kernel<kFew>, dim3(1), dim3(kFew), 0, st, a);
-    return launch(plan_kernel<kThreads>, dim3((rows + kThreads - 1) / kThreads), dim3(kThreads), 0, st, a);
+    if (b.requests <= 64 && rows <= 64 * kMostGroups) return go<64, 1>(a, st);
+    if (b.requests <= 256 && rows <= 256 * kMostGroups) return go<256, 1>(a, st);
+    if (b.requests <= 512) return go<512, 1>(a, st);
+    if (b.requests <= 1024) return go<1024, 1>(a, st);
+    if (b.requests <= 2048) return go<1024, 2>(a, st);
+    return go<1024, kv::kMaxRequests / 1024>(a, st);
 }
 
 }  // namespace ftmoe

@@ -62,6 +62,15 @@ def test_batches(B, P, width, tokens, row_tokens, free, in_place):
     compare(random_batch(B, P, width, tokens, row_tokens, 1, free=free), in_place)
 
 
+@pytest.mark.parametrize("B,tokens,row_tokens", [(64, 4032, 0), (64, 4033, 0), (256, 16128, 0), (256, 16129, 0), (256, 256, 1),
+                                                 (512, 512, 1), (513, 3000, 0), (2048, 2048, 1), (2049, 9000, 0), (7, 65535, 0)])
+def test_borders_of_the_workgroups(B, tokens, row_tokens):
+    """Either side of the sizes at which a call takes other workgroups."""
+    cuda()
+    for in_place in (False, True):
+        compare(random_batch(B, 16, 12, tokens, row_tokens, B, free=0.6), in_place)
+
+
 @pytest.mark.parametrize("ended,idle", [(1.0, 0.0), (0.0, 1.0), (0.9, 0.5), (0.0, 0.0)])
 def test_ended_and_idle(ended, idle):
     cuda()
