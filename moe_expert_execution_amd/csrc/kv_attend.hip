@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(workgroup(D, WAVES), waves_of(D, FMT, WAVES > 
                 for (int i = tid * 8; i < a.a.q_heads * D; i += kThreads * 8)
                     *reinterpret_cast<u32x4_t*>(a.a.out + r * a.a.out_stride + i) = u32x4_t{0, 0, 0, 0};
         if (carry == 0) return;
-        div = kv::divide((uint32_t)busy * heads_all, (uint32_t)carry * heads_all, kWaves, gridDim.x);
+        div = kv::divide((uint32_t)busy * heads_all, (uint32_t)carry * heads_all, kv::team_steps(D), gridDim.x);
         if (self >= div.teams) return;
         // the item that this team's cut falls into, before it moves (64 requests a look); then on from item to
         // item

@@ -40,11 +40,19 @@ constexpr int kMaxTeams = 512;
 // 60 with two of four; bf16, 32 of up to 8,192: 34, 39).
 FT_HD constexpr int team_waves(int D) { return D == 256 ? 8 : 4; }
 FT_HD constexpr int most_teams(int D) { return 8 * 256 / team_waves(D); }
+// Steps for which a call takes one more team: more teams read sooner, fewer have fewer parts to join (one request of 8,192
+// tokens, 32/4 heads of 128: 14.4 us, 14.8 with 4, 15.2 with 8; heads of 256, whose steps are longer, 16/2 of them: 17.5,
+// 19.7 with 6).
+// More than one team and less than two to a compute unit: where the second would be missing from an eighth or more,
+// all have one, since those with two end last (one request of 12,000 / 16,384, 32/4 heads of 128: 15.2 / 16.6 us with 256
+// teams, 17.4 / 19.2 with 375 and 512; 32 of up to 2,048 15.4 with 512, 19.1 with 460).
+constexpr int kUnits = 256;
+FT_HD constexpr int team_steps(int D) { return D == 256 ? 3 : 6; }
 // Steps that a cut moves, at most (32 ragged requests of up to 2,048 tokens, 16 KV heads: 32 us, 34 with 4), and what an
 // item takes beside its steps, in steps (64 ragged requests of up to 8,192: 112 us, 115 with 5, 128 with none).
 constexpr int kSlack = 8;
 constexpr int kItemCost = 8;
-// Parts of a run (8,192 tokens of one request, 62 parts an item: 14.3 us, 15.0 with 16).
+// Parts of a run (8,192 tokens of one request in 62 parts an item: 14.3 us, 15.0 with 16).
 constexpr int kJoin = 8;
 
 constexpr int64_t kMaxSteps = 1ll << 30;   // of a call: all lengths below are 32-bit
@@ -58,10 +66,11 @@ struct Division {
 
 FT_HD inline int item_length(int steps) { return steps ? steps + kItemCost : 0; }
 
-// `items` that have steps, `total` length, at most `grid` teams: one for as many steps as it has
-// waves, or for an item where items are shorter.
-FT_HD inline Division divide(uint32_t items, uint32_t total, int waves, int grid) {
-    uint32_t t = (total - items * kItemCost + waves - 1) / waves;
+// `items` that have steps, `total` length, at most `grid` teams: one for so many steps, or for an
+// item where items are shorter.
+FT_HD inline Division divide(uint32_t items, uint32_t total, int steps, int grid) {
+    uint32_t t = (total - items * kItemCost + steps - 1) / steps;
+    if (t > kUnits && t < (uint32_t)grid) t = t <= (uint32_t)grid * 7 / 8 ? kUnits : grid;
     if (t < items) t = items;
     if (t > (uint32_t)grid) t = grid;
     const uint32_t base = total / t, half = (base - 1) / 2;      // less than half a range: few teams stay idle
@@ -116,7 +125,7 @@ FT_HD inline int64_t part_floats(int g, int D) { return (int64_t)item_heads(g) *
 
 // Workgroups of a launch of at most so many items and steps (up to kMaxSteps).
 inline int grid_of(int64_t items, int64_t steps, int D) {
-    return divide((uint32_t)items, (uint32_t)(steps + items * kItemCost), team_waves(D), most_teams(D)).teams;
+    return divide((uint32_t)items, (uint32_t)(steps + items * kItemCost), team_steps(D), most_teams(D)).teams;
 }
 
 // Items of at most this many steps are not cut, so they need no division: a workgroup each (64 ragged requests of up to

@@ -19,7 +19,7 @@ SOURCE = r"""
 using namespace ftmoe::kv;
 #define CHECK(c) do { if (!(c)) { printf("line %d: %s\n", __LINE__, #c); return 1; } } while (0)
 
-int division(const std::vector<int>& items, int waves, int grid) {
+int division(const std::vector<int>& items, int steps, int grid) {
     std::vector<uint32_t> first{0};
     long long busy = 0;
     for (int n : items) {
@@ -27,7 +27,7 @@ int division(const std::vector<int>& items, int waves, int grid) {
         busy += n > 0;
     }
     const uint32_t total = first.back();
-    const Division d = divide(busy, total, waves, grid);
+    const Division d = divide(busy, total, steps, grid);
     CHECK(d.teams >= 1 && d.teams <= grid && (uint32_t)d.teams <= total && d.teams <= kMaxTeams);
     CHECK(cut(d, 0) == 0 && cut(d, d.teams) == total && d.slack >= 0 && 2 * d.slack < (int)(total / d.teams + 1));
     std::vector<int> load(d.teams, 0), length(d.teams, 0);
@@ -89,7 +89,7 @@ int main() {
             const int n = 1 + rand() % 40, big = r % 3 == 0 ? 3000 : r % 3 == 1 ? 40 : 3;
             for (int i = 0; i < n; ++i) items.push_back(rand() % 4 ? 1 + rand() % big : 0);
             items.push_back(1);
-            if (division(items, r % 2 ? 4 : 8, g)) return 1;
+            if (division(items, r % 6 < 2 ? 3 : r % 2 ? 6 : 8, g)) return 1;
         }
     // equal short items are not cut
     for (int n = 1; n <= 40; ++n)
