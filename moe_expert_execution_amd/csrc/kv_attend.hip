@@ -18,7 +18,7 @@
 //
 // Statistics are fp32, one running maximum and sum per column and wave, in base 2.  The
 // work is divided as kv_rules.h says; memory bounds long contexts (64 requests of up to 8,192, 64/8 heads of 128, 650
-// MB: 113 us, 5.8 TB/s; one of 131,072, 32/4 heads, 268 MB: 52 us, 5.1 TB/s), latency short ones (37 tokens 4.4 us).
+// MB: 108 us, 6.0 TB/s; one of 131,072, 32/4 heads, 268 MB: 50 us, 5.4 TB/s), latency short ones (37 tokens 4.4 us).
 #include "kv_device.h"
 #include "resident.h"
 
@@ -349,7 +349,8 @@ __global__ void __launch_bounds__(workgroup(D, WAVES), waves_of(D, FMT, WAVES > 
                 for (int i = tid * 8; i < a.a.q_heads * D; i += kThreads * 8)
                     *reinterpret_cast<u32x4_t*>(a.a.out + r * a.a.out_stride + i) = u32x4_t{0, 0, 0, 0};
         if (carry == 0) return;
-        div = kv::divide((uint32_t)busy * heads_all, (uint32_t)carry * heads_all, kv::team_steps(D), gridDim.x);
+        div = kv::divide((uint32_t)busy * heads_all, (uint32_t)carry * heads_all, kv::team_steps(D), gridDim.x,
+                         kv::many_items(D * (FMT == FT_KV_BF16 ? 2 : 1)));
         if (self >= div.teams) return;
         // the item that this team's cut falls into, before it moves (64 requests a look); then on from item to
         // item
@@ -673,7 +674,7 @@ hipError_t start(const AttendArgs& a, int grid, hipStream_t st) {
 template <int D, int FMT, bool WIDE>
 hipError_t go(const AttendArgs& a, int64_t steps, hipStream_t st) {
     const int64_t items = (int64_t)a.a.requests * a.c.heads * a.blocks;
-    if (steps > kv::kDirectSteps) return start<D, FMT, WIDE, 0>(a, kv::grid_of(items, items * steps, D), st);
+    if (steps > kv::kDirectSteps) return start<D, FMT, WIDE, 0>(a, kv::grid_of(items, items * steps, D, FMT == FT_KV_BF16 ? 2 : 1), st);
     if (kv::direct_waves(items, steps) == 2) return start<D, FMT, WIDE, 2>(a, (int)items, st);
     return start<D, FMT, WIDE, kv::kDirectWaves>(a, (int)items, st);
 }

@@ -33,23 +33,26 @@ FT_HD constexpr int value_tokens(int D, int esize) { return 16 / (esize * value_
 // ragged lengths balance by themselves.  An item that is cut is joined by the last of its teams to
 // arrive, so a cut within `slack` steps of an item's end moves there.
 constexpr int kMaxTeams = 512;
-// Waves of a team, which share a segment's steps, and teams of a call: eight waves to each of 256 compute units,
-// as registers allow, so all teams are resident (one that starts late ends late).  Two teams of four overlap one
-// another's ends (64 requests of up to 8,192 tokens, 128 dimensions: 111 us, 113 with one of eight; e4m3 57, 69); heads of
-// 256 have twice the partial sums, and one team of eight halves those (13 requests of up to 65,536, e4m3: 56 us,
-// 60 with two of four; bf16, 32 of up to 8,192: 34, 39).
+// Waves of a team, which share a segment's steps, and the most teams of a call: eight waves to each of 256 compute units,
+// as registers allow, so all teams are resident (one that starts late ends late).  Heads of 256 have twice the partial
+// sums, and one team of eight halves those (13 requests of up to 65,536, e4m3: 56 us, 60 with two of four; bf16, 32 of up to
+// 8,192: 34, 39).
 FT_HD constexpr int team_waves(int D) { return D == 256 ? 8 : 4; }
 FT_HD constexpr int most_teams(int D) { return 8 * 256 / team_waves(D); }
 // Steps for which a call takes one more team: more teams read sooner, fewer have fewer parts to join (one request of 8,192
 // tokens, 32/4 heads of 128: 14.4 us, 14.8 with 4, 15.2 with 8; heads of 256, whose steps are longer, 16/2 of them: 17.5,
 // 19.7 with 6).
-// More than one team and less than two to a compute unit: where the second would be missing from an eighth or more,
-// all have one, since those with two end last (one request of 12,000 / 16,384, 32/4 heads of 128: 15.2 / 16.6 us with 256
-// teams, 17.4 / 19.2 with 375 and 512; 32 of up to 2,048 15.4 with 512, 19.1 with 460).
-constexpr int kUnits = 256;
 FT_HD constexpr int team_steps(int D) { return D == 256 ? 3 : 6; }
-// Steps that a cut moves, at most (32 ragged requests of up to 2,048 tokens, 16 KV heads: 32 us, 34 with 4), and what an
-// item takes beside its steps, in steps (64 ragged requests of up to 8,192: 112 us, 115 with 5, 128 with none).
+// Above one team to a compute unit a call takes two, and no number between (those with two would end last): two where
+// its items are many, for their parts are few then, and a token's row of a head, `row` bytes, is so small that four
+// waves have too little under way.  Rows of 256 bytes: one team is as fast throughout, with half the parts (131,072
+// tokens of one request, 4 KV heads: 50.0 us, 53.0 with two; 64 ragged ones of up to 8,192, 8 KV heads: 108, 112).  128
+// bytes: 64 items 21.1 / 19.8 us (e4m3 of 128 / bf16 of 64) with one, 21.9 / 22.0 with two; 256 items 40 / 31.6 and 36 / 30.7;
+// 512 items 65.7 / 47.8 and 55.9 / 45.9.  64 bytes: 32 items 19.8 and 17.7, 512 items 28.7 and 23.1.
+constexpr uint32_t kUnits = 256;
+FT_HD constexpr uint32_t many_items(int row) { return row >= 256 ? UINT32_MAX : row >= 128 ? 192 : 16; }
+// Steps that a cut moves, at most (32 ragged requests of up to 2,048 tokens, 16 KV heads: 30.8 us, 32.5 with 16), and what
+// an item takes beside its steps, in steps (64 ragged requests of up to 8,192: 108 us, 109 with 12, 115 with 5).
 constexpr int kSlack = 8;
 constexpr int kItemCost = 8;
 // Parts of a run (8,192 tokens of one request in 62 parts an item: 14.3 us, 15.0 with 16).
@@ -67,11 +70,12 @@ struct Division {
 FT_HD inline int item_length(int steps) { return steps ? steps + kItemCost : 0; }
 
 // `items` that have steps, `total` length, at most `grid` teams: one for so many steps, or for an
-// item where items are shorter.
-FT_HD inline Division divide(uint32_t items, uint32_t total, int steps, int grid) {
+// item where items are shorter; kUnits where that is more and items fewer than `many`.
+FT_HD inline Division divide(uint32_t items, uint32_t total, int steps, int grid, uint32_t many) {
     uint32_t t = (total - items * kItemCost + steps - 1) / steps;
-    if (t > kUnits && t < (uint32_t)grid) t = t <= (uint32_t)grid * 7 / 8 ? kUnits : grid;
+    if (t > kUnits && items >= many) t = kMaxTeams;
     if (t < items) t = items;
+    if (t > kUnits && items < many) t = kUnits;
     if (t > (uint32_t)grid) t = grid;
     const uint32_t base = total / t, half = (base - 1) / 2;      // less than half a range: few teams stay idle
     return Division{total, base, ((total - base * t) << 16) / t, (float)t / (float)total, (int)t,
@@ -124,8 +128,9 @@ FT_HD inline int head_blocks(int g) { return (g + kCols - 1) / kCols; }
 FT_HD inline int64_t part_floats(int g, int D) { return (int64_t)item_heads(g) * D + 4 * kCols; }
 
 // Workgroups of a launch of at most so many items and steps (up to kMaxSteps).
-inline int grid_of(int64_t items, int64_t steps, int D) {
-    return divide((uint32_t)items, (uint32_t)(steps + items * kItemCost), team_steps(D), most_teams(D)).teams;
+inline int grid_of(int64_t items, int64_t steps, int D, int esize) {
+    return divide((uint32_t)items, (uint32_t)(steps + items * kItemCost), team_steps(D), most_teams(D),
+                  many_items(D * esize)).teams;
 }
 
 // Items of at most this many steps are not cut, so they need no division: a workgroup each (64 ragged requests of up to

@@ -19,7 +19,7 @@ SOURCE = r"""
 using namespace ftmoe::kv;
 #define CHECK(c) do { if (!(c)) { printf("line %d: %s\n", __LINE__, #c); return 1; } } while (0)
 
-int division(const std::vector<int>& items, int steps, int grid) {
+int division(const std::vector<int>& items, int steps, int grid, uint32_t many) {
     std::vector<uint32_t> first{0};
     long long busy = 0;
     for (int n : items) {
@@ -27,7 +27,7 @@ int division(const std::vector<int>& items, int steps, int grid) {
         busy += n > 0;
     }
     const uint32_t total = first.back();
-    const Division d = divide(busy, total, steps, grid);
+    const Division d = divide(busy, total, steps, grid, many);
     CHECK(d.teams >= 1 && d.teams <= grid && (uint32_t)d.teams <= total && d.teams <= kMaxTeams);
     CHECK(cut(d, 0) == 0 && cut(d, d.teams) == total && d.slack >= 0 && 2 * d.slack < (int)(total / d.teams + 1));
     std::vector<int> load(d.teams, 0), length(d.teams, 0);
@@ -89,12 +89,12 @@ int main() {
             const int n = 1 + rand() % 40, big = r % 3 == 0 ? 3000 : r % 3 == 1 ? 40 : 3;
             for (int i = 0; i < n; ++i) items.push_back(rand() % 4 ? 1 + rand() % big : 0);
             items.push_back(1);
-            if (division(items, r % 6 < 2 ? 3 : r % 2 ? 6 : 8, g)) return 1;
+            if (division(items, r % 6 < 2 ? 3 : r % 2 ? 6 : 8, g, r % 4 ? 16 : UINT32_MAX)) return 1;
         }
     // equal short items are not cut
     for (int n = 1; n <= 40; ++n)
         for (int items : {1, 3, 64, 100, 500}) {
-            const Division d = divide(items, items * item_length(n), 4, kMaxTeams);
+            const Division d = divide(items, items * item_length(n), 4, kMaxTeams, 192);
             for (int i = 0; i < items && n <= 4; ++i) {
                 const Teams who = teams_of(d, i * item_length(n), n);
                 CHECK(who.first == who.last);
@@ -102,7 +102,7 @@ int main() {
         }
     // the largest calls
     for (long long total : {(1ll << 24) + 1, (1ll << 30) + 12345, (1ll << 30) + (4096ll * 1024 * kItemCost)}) {
-        const Division d = divide(1 << 20, (uint32_t)total, 8, kMaxTeams);
+        const Division d = divide(1 << 20, (uint32_t)total, 8, kMaxTeams, 16);
         CHECK(cut(d, 0) == 0 && cut(d, d.teams) == total);
         for (int t = 0; t < d.teams; ++t) {
             const uint32_t b = cut(d, t), e = cut(d, t + 1);
@@ -115,7 +115,8 @@ int main() {
         CHECK(n == g && item_heads(g) <= kCols);
     }
     for (int D : {64, 128, 256})
-        CHECK(grid_of(1, 1, D) == 1 && grid_of(4096 * 1024, kMaxSteps, D) == most_teams(D) && most_teams(D) <= kMaxTeams);
+        for (int e : {1, 2})
+            CHECK(grid_of(1, 1, D, e) == 1 && grid_of(4096 * 1024, kMaxSteps, D, e) == (D * e < 256 ? 512 : 256) && most_teams(D) <= kMaxTeams);
     printf("ok\n");
     return 0;
 }
