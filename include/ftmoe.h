@@ -692,7 +692,10 @@ ft_status ft_kv_append(const ft_kv_cache* cache, const ft_append* args, void* st
  * What pages hold beyond the visible positions, and table entries beyond them,
  * reaches no result.
  * Sums and softmax statistics are fp32; probabilities keep 16 significant bits
- * for the product with the values.  The work of all requests is divided evenly
+ * for the product with the values.  An infinite value makes its dimension
+ * infinite in every head that gives it a weight exp(s_t - max s) of 2^-100 or
+ * more (NaN beside one of the other sign); a lesser weight may count as zero,
+ * and makes NaN of an infinite value.  The work of all requests is divided evenly
  * over workgroups, so the order of a request's sums depends on the lengths of the
  * others.
  * Errors: FT_ERR_ARG (shape, strides, null or misaligned pointers, a workspace

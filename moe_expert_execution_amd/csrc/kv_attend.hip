@@ -12,7 +12,7 @@
 // keys, values nor probabilities pass through LDS.
 //
 // Up to 8 query heads the operand's other 8 columns hold the same heads: columns 0 .. 7
-// take each probability's nearest bf16, 8 .. 15 the rest's, and the two sums add up to
+// take each probability as bf16, 8 .. 15 its rest, and the two sums add up to
 // 16 significant bits at no cost; wider groups take two products.  e4m3 codes become bf16
 // exactly; the heads' scales multiply the logits and the result.
 //
@@ -174,6 +174,26 @@ __device__ __forceinline__ float quarters(float v, F&& f) {
     return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// Two probabilities as bf16 pairs, high + low to 16 significant bits.  Beside values that may be infinite (bf16) the high half is
+// cut towards zero and the low one, what is left, not below the least normal number where the probability is not: both products
+// of such a value then have its sign, where a rest of zero or below would make their sum NaN.  That adds at most 2^-126 of a
+// value, no more than fp32 leaves out of any weight below that.  (e4m3fn has no infinities: the nearest.)
+template <int FMT>
+__device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& high, uint32_t& low) {
+    if constexpr (FMT == FT_KV_BF16) {
+        const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+        high = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
+        const float least = 0x1p-126f;
+        const float r0 = fmaxf(p0 - __uint_as_float(u0 & 0xFFFF0000u), fminf(p0, least));
+        const float r1 = fmaxf(p1 - __uint_as_float(u1 & 0xFFFF0000u), fminf(p1, least));
+        low = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)r0, (__bf16)r1});
+    } else {
+        const bf16x2_t h = {(__bf16)p0, (__bf16)p1};
+        high = __builtin_bit_cast(uint32_t, h);
+        low = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(p0 - (float)h[0]), (__bf16)(p1 - (float)h[1])});
+    }
+}
+
 // A step's probabilities as operands (WIDE: high and low halves; else both in `high`), and which halves of
 // value pairs are visible.
 struct Probs {
@@ -217,10 +237,7 @@ __device__ __forceinline__ Probs softmax_step(State<D, FMT, WIDE>& st, float (&s
         for (int p = 0; p < 2; ++p) {
             const float p0 = exp2_of(s[b][2 * p] - base), p1 = exp2_of(s[b][2 * p + 1] - base);
             sum += p0 + p1;
-            const bf16x2_t h = {(__bf16)p0, (__bf16)p1};
-            const bf16x2_t r = {(__bf16)(p0 - (float)h[0]), (__bf16)(p1 - (float)h[1])};
-            hi_p[b * 2 + p] = __builtin_bit_cast(uint32_t, h);
-            lo_p[b * 2 + p] = __builtin_bit_cast(uint32_t, r);
+            split_pair<FMT>(p0, p1, hi_p[b * 2 + p], lo_p[b * 2 + p]);
         }
     st.l = st.l * out.alpha + sum;
 #pragma unroll
