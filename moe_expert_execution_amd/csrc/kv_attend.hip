@@ -177,10 +177,13 @@ __device__ __forceinline__ float quarters(float v, F&& f) {
 // Two probabilities as bf16 pairs, high + low to 16 significant bits.  Beside values that may be infinite (bf16) the high half is
 // cut towards zero and the low one, what is left, not below the least normal number where the probability is not: both products
 // of such a value then have its sign, where a rest of zero or below would make their sum NaN.  That adds at most 2^-126 of a
-// value, no more than fp32 leaves out of any weight below that.  (e4m3fn has no infinities: the nearest.)
+// value, no more than fp32 leaves out of any weight below that.  `down`, the power of two at or below one part of the request's
+// tokens, keeps their sum within the largest value, where it would pass fp32.  (e4m3fn has neither: the nearest.)
 template <int FMT>
-__device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& high, uint32_t& low) {
+__device__ __forceinline__ void split_pair(float p0, float p1, float down, uint32_t& high, uint32_t& low) {
     if constexpr (FMT == FT_KV_BF16) {
+        p0 *= down;
+        p1 *= down;
         const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
         high = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
         const float least = 0x1p-126f;
@@ -205,7 +208,7 @@ struct Probs {
 // Positions t0 + 16 b + 4 (l / 16) + v outside lo .. hi - 1 count for nothing.
 template <int D, int FMT, bool WIDE>
 __device__ __forceinline__ Probs softmax_step(State<D, FMT, WIDE>& st, float (&s)[2][4], bool masked, int t0, int lo,
-                                              int hi, int lane) {
+                                              int hi, float down, int lane) {
     Probs out;
     uint32_t (&keep)[2][2] = out.keep;
     keep[0][0] = keep[0][1] = keep[1][0] = keep[1][1] = ~0u;
@@ -237,7 +240,7 @@ __device__ __forceinline__ Probs softmax_step(State<D, FMT, WIDE>& st, float (&s
         for (int p = 0; p < 2; ++p) {
             const float p0 = exp2_of(s[b][2 * p] - base), p1 = exp2_of(s[b][2 * p + 1] - base);
             sum += p0 + p1;
-            split_pair<FMT>(p0, p1, hi_p[b * 2 + p], lo_p[b * 2 + p]);
+            split_pair<FMT>(p0, p1, down, hi_p[b * 2 + p], lo_p[b * 2 + p]);
         }
     st.l = st.l * out.alpha + sum;
 #pragma unroll
@@ -281,9 +284,9 @@ __device__ __forceinline__ float part_weight(float m, float whole) {
     return whole == -INFINITY ? 0.0f : m == whole ? 1.0f : exp2_of(m - whole);
 }
 
-// out[0..3] of one head: o / l, zeros where nothing was visible.
-__device__ __forceinline__ void store_out(uint16_t* to, const f32x4_t o, float l, float v_scale) {
-    const float f = l == 0.0f ? 0.0f : v_scale / l;
+// out[0..3] of one head: scale o / l, zeros where nothing was visible.
+__device__ __forceinline__ void store_out(uint16_t* to, const f32x4_t o, float l, float scale) {
+    const float f = l == 0.0f ? 0.0f : scale / l;
     typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
     float x[4];
 #pragma unroll
@@ -415,7 +418,10 @@ __global__ void __launch_bounds__(workgroup(D, WAVES), waves_of(D, FMT, WAVES > 
         const int heads = min(kv::kCols, g - (item % a.blocks) * kv::kCols);
         const int step0 = lo / kv::kStep + first;                // in the request's own steps
         const float scale = a.a.scale * kLog2e * (FMT == FT_KV_E4M3 ? a.c.k_scale[h] : 1.0f);
-        const float v_scale = FMT == FT_KV_E4M3 ? a.c.v_scale[h] : 1.0f;
+        // bf16: weights meet values as 2^-ceil(log2(tokens)) of themselves, so that the sum is finite where the mean is
+        const int halvings = hi - lo > 1 ? 32 - __builtin_clz(hi - lo - 1) : 0;
+        const float down = __uint_as_float((uint32_t)(127 - halvings) << 23);
+        const float out_scale = FMT == FT_KV_E4M3 ? a.c.v_scale[h] : __uint_as_float((uint32_t)(127 + halvings) << 23);
 
         Queries<D, FMT> q;
         q.lds = wq;
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(workgroup(D, WAVES), waves_of(D, FMT, WAVES > 
             keys();
             // blocks without a page are left out: the visible range shrinks to the other one, or to nothing
             const int from = on[0] ? lo : max(lo, t0 + 16), to = on[1] ? hi : min(hi, t0 + 16);
-            const Probs p = softmax_step<D, FMT, WIDE>(st, s, from > t0 || to < t0 + kv::kStep, t0, from, to, lane);
+            const Probs p = softmax_step<D, FMT, WIDE>(st, s, from > t0 || to < t0 + kv::kStep, t0, from, to, down, lane);
             add_values<D, FMT, WIDE>(st, x, p);
             __builtin_amdgcn_sched_barrier(0);
             values();
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(workgroup(D, WAVES), waves_of(D, FMT, WAVES > 
                     if (final) {
                         const float sink = a.a.sinks ? a.a.sinks[q0 + c] * kLog2e : -INFINITY, mn = fmaxf(m, sink);
                         const float f1 = part_weight(m, mn);
-                        store_out(out + (int64_t)c * D + e, o * f1, lt * f1 + part_weight(sink, mn), v_scale);
+                        store_out(out + (int64_t)c * D + e, o * f1, lt * f1 + part_weight(sink, mn), out_scale);
                     } else {
                         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), parts,
                                                                first_at + (uint32_t)(c * D + e) * 4, 0, kAgent);
@@ -635,7 +641,7 @@ __global__ void __launch_bounds__(workgroup(D, WAVES), waves_of(D, FMT, WAVES > 
                         lt += wl[w * kv::kCols + c] * part_weight(wm[w * kv::kCols + c], mm);
                     lt += part_weight(sink, mm);
                     o *= part_weight(m, mm);
-                    store_out(out + (int64_t)c * D + dim, o, lt, v_scale);
+                    store_out(out + (int64_t)c * D + dim, o, lt, out_scale);
                 } else {
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), parts,
                                                            slot + (uint32_t)(c * D + dim) * 4, 0, kAgent);
