@@ -740,7 +740,9 @@ ft_status ft_kv_attend(const ft_kv_cache* cache, const ft_attend* args, ft_works
  *   FT_GATE_FULL gate [T x d], rows gate_stride apart; | FT_GATE_SIGMOID: the
  *   sigmoid of the given values is the gate.
  * sum may be residual or block, and normed block or residual, with equal
- * strides.  Squares are summed in fp32 (values up to 2^56).
+ * strides.  Squares are summed in fp32, scaled where they would leave its range:
+ * rows of any finite values have their norm, eps = 0 included, but for rows of
+ * zeros (0 / 0 is NaN) and sums that themselves pass fp32.
  * Errors: FT_ERR_ARG, FT_ERR_HIP.
  * ------------------------------------------------------------------------- */
 enum { FT_GATE_NONE = 0, FT_GATE_CHANNEL = 1, FT_GATE_TOKEN = 2, FT_GATE_FULL = 3, FT_GATE_SIGMOID = 0x10 };

@@ -8,6 +8,8 @@
 // sum; rounding it first would feed the next block the residual's bf16 error
 // twice.  Memory bounds it, or the launch where there are few rows: 4,096 rows of 7,168 with
 // both norms and a gate per element 54 us, 5.4 TB/s (a large copy: 5.1 to 5.3), one row of 2,048 2.9 us.
+#include <float.h>
+
 #include "kv_device.h"
 
 namespace ftmoe {
@@ -35,6 +37,14 @@ __device__ __forceinline__ float element(const u32x4_t u, int i) {
 
 __device__ __forceinline__ float sigmoid_of(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
+// Rows whose squares leave fp32's range (below 2^-50 or above 2^56 in size, where eps does not carry them) are summed again,
+// scaled by a power of two; all threads of a row see the same mean, so they go there together.  The first choice makes the
+// square of any bf16 below 2^-42 a normal number, the second keeps 32,768 squares of the largest finite.
+constexpr float kLeastMean = 0x1p-100f, kUp = 0x1p96f, kDown = 0x1p-72f;
+__device__ __forceinline__ bool leaves_range(float mean) {
+    return __builtin_expect(mean < kLeastMean || mean > FLT_MAX, false);
+}
+
 // R threads per row, U units of 8 elements per thread; a workgroup is one row, or 256 threads where rows are
 // a wave's or smaller.
 constexpr int threads_of(int R) { return R > 64 ? R : 256; }
@@ -42,7 +52,7 @@ constexpr int threads_of(int R) { return R > 64 ? R : 256; }
 template <int R, int U, bool STREAM>
 __global__ void __launch_bounds__(threads_of(R)) norm_kernel(ft_norm a) {
     constexpr int kThreads = threads_of(R);
-    __shared__ float lds[2][R > 64 ? R / 64 : 1];
+    __shared__ float lds[4][R > 64 ? R / 64 : 1];
     const int64_t t = (int64_t)blockIdx.x * (kThreads / R) + threadIdx.x / R;
     const int lane = threadIdx.x % R, units = a.d >> 3;
     if (t >= a.T) return;                   // (rows of a workgroup-wide reduction have one row a workgroup)
@@ -73,7 +83,23 @@ __global__ void __launch_bounds__(threads_of(R)) norm_kernel(ft_norm a) {
         for (int i = 0; i < U; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) q = fmaf(element(b[i], e), element(b[i], e), q);
-        s1 = token_gate * (1.0f / sqrtf(row_sum<R>(q, lds[0]) * inv_d + a.eps));
+        float mean = row_sum<R>(q, lds[0]) * inv_d + a.eps, one = 1.0f;
+        if (leaves_range(mean)) {
+            const bool up = mean < kLeastMean;
+            const float f = up ? kUp : kDown;
+            q = 0.0f;
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = bf16lo(b[i][e]) * f, y = bf16hi(b[i][e]) * f;
+                    q = fmaf(x, x, fmaf(y, y, q));
+                    if (up) b[i][e] = pack_bf16_trunc(x, y);             // (exact: the block stays scaled)
+                }
+            mean = row_sum<R>(q, lds[1]) * inv_d + a.eps * f * f;
+            if (!up) one = f;
+        }
+        s1 = token_gate * (one / sqrtf(mean));
     }
     float s[U][8];
     float q = 0.0f;
@@ -102,7 +128,23 @@ __global__ void __launch_bounds__(threads_of(R)) norm_kernel(ft_norm a) {
         }
     }
     if (!a.normed) return;
-    const float s2 = 1.0f / sqrtf(row_sum<R>(q, lds[1]) * inv_d + a.eps);
+    float mean = row_sum<R>(q, lds[2]) * inv_d + a.eps, one = 1.0f;
+    if (leaves_range(mean)) {
+        const bool up = mean < kLeastMean;
+        const float f = up ? kUp : kDown;
+        q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = s[i][e] * f;
+                q = fmaf(x, x, q);
+                if (up) s[i][e] = x;
+            }
+        mean = row_sum<R>(q, lds[3]) * inv_d + a.eps * f * f;
+        if (!up) one = f;
+    }
+    const float s2 = one / sqrtf(mean);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         const int u = lane + i * R;
