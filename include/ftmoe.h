@@ -686,7 +686,7 @@ ft_status ft_kv_append(const ft_kv_cache* cache, const ft_append* args, void* st
  *   most 1024; table [requests x width]; kv_len [requests] (clamped to
  *   0..width * page_tokens); requests * kv_heads * ceil(q_heads / kv_heads / 16) *
  *   width * page_tokens at most 2^35.  q, out [requests x q_heads x head_dim]
- *   bf16.  scale is finite.
+ *   bf16.  |scale| is at most 2^127.
  * A position whose page id is outside 0..pages - 1 is left out.  A request that
  * sees no position, or none whose logit is above minus infinity, gets zeros.
  * What pages hold beyond the visible positions, and table entries beyond them,

@@ -158,7 +158,7 @@ ft_status ft_kv_attend(const ft_kv_cache* cache, const ft_attend* a, ft_workspac
     FT_REQUIRE(items * (((int64_t)a->width << c.page_shift) / kv::kBlock) <= 2 * kv::kMaxSteps,
                "requests * kv_heads * ceil(group / 16) * width * page_tokens must be at most 2^35");
     FT_REQUIRE(a->window >= 0, "window must be >= 0");
-    FT_REQUIRE(isfinite(a->scale), "scale must be finite");
+    FT_REQUIRE(fabsf(a->scale) <= 0x1p127f, "scale must be finite, at most 2^127 in size");   // (times log2 e in fp32)
     FT_REQUIRE(a->reserved == 0, "reserved must be 0");
     if (a->requests == 0) return FT_OK;
     const int64_t row = (int64_t)a->q_heads * c.D;
