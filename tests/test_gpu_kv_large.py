@@ -44,3 +44,25 @@ def test_largest_values(fmt, D, g, n, wide, window):
         ref, bound = attend_reference(cache, call.q.reshape(3, g, D), table, lens, call.scale, window, sinks)
         assert np.isfinite(out).all()
         assert_within(out, ref, bound, f"q {q_scale}")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("g", [2, 12])
+@pytest.mark.parametrize("n,wide", [(2, False), (300, False), (5000, True)])
+def test_smallest_values(D, g, n, wide):
+    """Values of 2^-116 to 2^-112, near the least normal number: their mean has an error of bf16's step and of the least fp32
+    number a token, and is not zero."""
+    cuda()
+    P = 32
+    table, pages = random_table([n], P, 1, 211, extra(wide, P))
+    cache = Cache("bf16", pages, P, 1, D, 211)
+    rng = np.random.default_rng([211, n, D])
+    slots = table[0, np.arange(n) // P].astype(np.int64) * P + np.arange(n) % P
+    cache.write("v", slots, 0, (rng.integers(11, 16, (n, D)) << 7) | rng.integers(0, 128, (n, D)))
+    cache.upload()
+    for q_scale in (0.0, 1.0):
+        call = Attend(cache, table, [n], g, q_scale=q_scale, seed=211)
+        out = OF.bf16_to_f64(call.run())
+        ref, bound = attend_reference(cache, call.q.reshape(1, g, D), table, [n], call.scale)
+        # the definition's bound carries 1e-37 for outputs near zero; here it is 2^-149 of each scaled product and sum
+        assert_within(out, ref, bound - 1e-37 + 2.0 ** -149 * 64 * n, f"q {q_scale}")
