@@ -210,7 +210,7 @@ hipError_t pick(const AppendArgs& a, int64_t waves, hipStream_t st) {
 // A wave's heads share its slot, angles and start, and keep a step's loads ahead, as long as the waves still cover the
 // latency.  Twice the heads where ten waves or more per compute unit are left: 1,000 tokens of 48 heads of 128 9.3 us
 // in 3,000 waves, 10.5 in 6,000; 1,500 tokens 13.3 in 2,256, 12.8 in 4,512; 777 e4m3 tokens 7.2 in 1,960, 6.2 in 3,920.
-// Eight heads a wave: 8,192 tokens 44, 41 with four.
+// Eight heads a wave: 8,192 tokens 44, 41 with four.  (Calls in a captured graph.)
 hipError_t launch_kv_append(const CacheView& c, const ft_append& a, hipStream_t st) {
     AppendArgs k;
     k.c = c;

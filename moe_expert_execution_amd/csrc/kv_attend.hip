@@ -17,8 +17,9 @@
 // exactly; the heads' scales multiply the logits and the result.
 //
 // Statistics are fp32, one running maximum and sum per column and wave, in base 2.  The
-// work is divided as kv_rules.h says; memory bounds long contexts (64 requests of up to 8,192, 64/8 heads of 128, 650
-// MB: 108 us, 6.0 TB/s; one of 131,072, 32/4 heads, 268 MB: 50 us, 5.4 TB/s), latency short ones (37 tokens 4.4 us).
+// work is divided as kv_rules.h says; memory bounds long contexts (64 requests of up to 8,192, 64/8 heads of 128, 649
+// MB: 110 us, 5.9 TB/s; one of 131,072, 32/4 heads, 268 MB: 50 us, 5.4 TB/s), latency short ones (37 tokens in a table of 4
+// pages 4.4 us).  (Times of launches; those in kv_rules.h are of calls in a captured graph.)
 #include "kv_device.h"
 #include "resident.h"
 
@@ -294,7 +295,8 @@ __device__ __forceinline__ void store_out(uint16_t* to, const f32x4_t o, float l
     *reinterpret_cast<u32x2_t*>(to) = u32x2_t{kv::pack_bf16(x[0], x[1]), kv::pack_bf16(x[2], x[3])};
 }
 
-// Waves of a SIMD whose registers the kernel fits: teams are two to a compute unit, whole items as many as can be.
+// Waves of a SIMD whose registers the kernel fits: a divided launch has at most eight waves to a compute unit (two teams, or
+// one where heads have 256 dimensions), whole items as many as can be.
 constexpr int waves_of(int D, int fmt, bool direct) { return direct && (D < 256 || fmt == FT_KV_E4M3) ? 3 : 2; }
 
 constexpr int workgroup(int D, int waves) { return 64 * (waves ? waves : kv::team_waves(D)); }

@@ -140,9 +140,13 @@ constexpr int kDirectWaves = 4;
 constexpr int kDirectSteps = 8 * kDirectWaves;
 
 // Two waves an item where items are short and three or more to each of 256 compute units: a wave's start and the sum over
-// waves are most of a short item's cost.  100 requests, 8 KV heads, a window of 128: heads of 64 / 128 / 256 8.9 / 15.0 /
-// 28.9 us, 9.7 / 16.0 / 34.3 with four; in e4m3 7.4 / 10.9 / 19.6, 7.9 / 12.1 / 21.1.  64 requests: 7.3 / 11.1 / 20.4 with
-// two, 7.2 / 11.0 / 19.4 with four; windows of 256 over 250: 24.6 / 46.5 / 91.8, 23.9 / 43.8 / 93.2.
+// waves are most of a short item's cost.  us with two, four waves; a window of 128, heads of 64 / 128 / 256:
+//   512 items    7.5, 7.4 / 10.8, 11.1 / 20.4, 20.0    e4m3  7.1, 6.5 /  9.5,  8.8 / 16.1, 14.6
+//   640          7.9, 8.7 / 13.1, 13.7 / 23.3, 29.1          7.2, 7.4 / 10.2, 10.3 / 18.2, 17.6
+//   768          8.5, 9.5 / 14.3, 14.1 / 26.1, 32.6          7.4, 7.7 / 10.7, 11.1 / 19.1, 18.4
+//   800          8.9, 9.7 / 15.0, 16.0 / 28.9, 34.3          7.4, 7.9 / 10.9, 12.1 / 19.6, 21.1
+// So the border is where the last form begins to gain.  Above eight steps two waves lose: windows of 256, 2,000 items 24.6,
+// 23.9 / 46.5, 43.8 / 91.8, 93.2.
 constexpr int kShortSteps = 8, kManyItems = 768;
 inline int direct_waves(int64_t items, int64_t steps) {
     return steps <= kShortSteps && items >= kManyItems ? kDirectWaves / 2 : kDirectWaves;

@@ -133,7 +133,8 @@ class LoraPool:
 class KvPool:
     """A layer's paged key-value cache as device tensors, kept alive with its ft_kv_cache: k and v
     [pages, kv_heads * page_tokens * head_dim] in the layout of the C header, bf16 or e4m3 (then with
-    k_scale, v_scale [kv_heads] fp32).  Uninitialised: what no token was appended to is not read."""
+    k_scale, v_scale [kv_heads] fp32).  Uninitialised: attention loads blocks of 16 tokens whole, but what
+    no token was appended to reaches no result."""
 
     def __init__(self, pages, page_tokens, kv_heads, head_dim, fmt="bf16", k_scale=None, v_scale=None, device="cuda"):
         dt = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
