@@ -615,6 +615,9 @@ typedef struct {
  * counts [4] = tokens served, pages taken, pages in the free list afterwards
  * (free_pages holds them; entries past that are unspecified), requests refused.
  * free_count may be counts + 2 of the call before, or of this call.
+ * A page that several rows name comes back once for each that ends: a program
+ * that shares pages between requests counts them itself, and returns them in a row
+ * of its own when the last has ended.
  * The workspace is used for its arrival counters only: any size serves.
  * Errors: FT_ERR_ARG, FT_ERR_HIP.
  * ------------------------------------------------------------------------- */
@@ -695,10 +698,10 @@ ft_status ft_kv_append(const ft_kv_cache* cache, const ft_append* args, void* st
  * for the product with the values.  An infinite value makes its dimension
  * infinite in every head that gives it a weight of 2^-100 or more beside the
  * largest of the logits and the sink, exp(s_t - max) (NaN beside an infinity of
- * the other sign); a lesser weight may count as zero, and makes NaN of an infinite
- * value.  Values up to bf16's largest keep the sum finite.  The work of all requests is divided evenly
- * over workgroups, so the order of a request's sums depends on the lengths of the
- * others.
+ * the other sign); a lesser weight may count as zero, and may make NaN of an
+ * infinite value.  Finite values, the largest too, have a finite mean.
+ * The work of all requests is divided evenly over workgroups, so the order of a
+ * request's sums depends on the lengths of the others.
  * The lengths are on the device: a call whose table has room for at most 1,024
  * positions a request, or whose window is at most 991, takes each KV head of a
  * request as a whole; a wider table, which a captured decode loop has, divides the

@@ -7,7 +7,7 @@
 // are the only points where its threads meet.  The second norm uses the fp32
 // sum; rounding it first would feed the next block the residual's bf16 error
 // twice.  Memory bounds it, or the launch where there are few rows: 4,096 rows of 7,168 with
-// both norms and a gate per element 54 us, 5.4 TB/s (a large copy: 5.1 to 5.3), one row of 2,048 2.9 us.
+// both norms and a gate per element 55 us, 5.3 TB/s (a large copy: 5.1 to 5.3), one row of 2,048 3.0 us.
 #include <float.h>
 
 #include "kv_device.h"

@@ -145,8 +145,8 @@ constexpr int kDirectSteps = 8 * kDirectWaves;
 //   640          7.9, 8.7 / 13.1, 13.7 / 23.3, 29.1          7.2, 7.4 / 10.2, 10.3 / 18.2, 17.6
 //   768          8.5, 9.5 / 14.3, 14.1 / 26.1, 32.6          7.4, 7.7 / 10.7, 11.1 / 19.1, 18.4
 //   800          8.9, 9.7 / 15.0, 16.0 / 28.9, 34.3          7.4, 7.9 / 10.9, 12.1 / 19.6, 21.1
-// So the border is where the last form begins to gain.  Above eight steps two waves lose: windows of 256, 2,000 items 24.6,
-// 23.9 / 46.5, 43.8 / 91.8, 93.2.
+// So the border is where the last form begins to gain.  Above eight steps two waves lose, but for heads of 256: windows of
+// 256, 2,000 items 24.6, 23.9 / 46.5, 43.8 / 91.8, 93.2.
 constexpr int kShortSteps = 8, kManyItems = 768;
 inline int direct_waves(int64_t items, int64_t steps) {
     return steps <= kShortSteps && items >= kManyItems ? kDirectWaves / 2 : kDirectWaves;
